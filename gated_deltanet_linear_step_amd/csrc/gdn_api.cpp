@@ -191,6 +191,41 @@ gdn_status prefill_prepare(const gdn_dims *dims, int32_t num_seqs, const int32_t
     return GDN_OK;
 }
 
+// What gdn_linattn_* check of dims and inputs; fills the kernel-side copies. A call
+// with no token rows reads none of the per-token arrays: they may be NULL.
+gdn_status check_linattn(const gdn_dims *d, const gdn_inputs *in, int64_t tokens, int32_t out_dtype,
+                         const void *out, const float *state, uint32_t known_flags, gdn::LinattnParams &p)
+{
+    if (!d || !in)
+        return GDN_ERR_NULL;
+    if ((d->flags & ~known_flags) != 0)
+        return GDN_ERR_UNSUPPORTED;
+    const bool head_decay = (d->flags & GDN_HEAD_DECAY) != 0;
+    if (head_decay && d->decay != GDN_DECAY_LOG_RATE && d->decay != GDN_DECAY_NEGATIVE_RATE)
+        return GDN_ERR_SHAPE;
+    // the shared checks, with the decay standing in for the gate pair they require
+    gdn_dims dd = *d;
+    dd.flags &= GDN_STREAM_STATE;
+    dd.l2_eps = dd.norm_eps = 0.f;
+    gdn_inputs ii = *in;
+    ii.g = ii.beta = head_decay ? in->decay_param : in->g;
+    if (tokens == 0) {
+        alignas(16) static const float none[4] = {};
+        ii.q = ii.k = ii.v = out = none;
+        ii.g = ii.beta = state = none;
+    }
+    const gdn_status st = check_common(&dd, &ii, out_dtype, out, state, gdn::linattn_supported,
+                                       GDN_STREAM_STATE, p.hc, p.in);
+    if (st != GDN_OK)
+        return st;
+    p.hc.flags = d->flags;
+    p.in.g = head_decay ? nullptr : in->g;
+    p.in.beta = nullptr;
+    p.in.decay_param = head_decay ? in->decay_param : nullptr;
+    p.out_dt = out_dtype;
+    return GDN_OK;
+}
+
 // ---- the static scratch of gdn_prefill_chunked_noalloc ----------------------
 // The prefill's workspace for callers that cannot allocate (graph capture, tight
 // serving loops): a file-scope device array, one copy per GPU, held until the
@@ -244,7 +279,7 @@ const char *gdn_status_string(gdn_status s)
     return "unknown status";
 }
 
-int32_t gdn_version(void) { return 200; }
+int32_t gdn_version(void) { return 300; }
 
 gdn_status gdn_decode_launch_info(const gdn_dims *d, int32_t batch, int32_t tokens_per_seq,
                                   int32_t fused_conv, gdn_launch_info *info)
@@ -466,6 +501,166 @@ gdn_status gdn_prefill_chunked_noalloc(const gdn_dims *dims, int32_t num_seqs,
         return GDN_ERR_LAUNCH;
     gdn::prefill_carve(p, ws, max_chunk_bound(dims, num_seqs, total_tokens));
     return launch_status(gdn::launch_prefill(p, static_cast<hipStream_t>(stream)));
+}
+
+gdn_status gdn_linattn_decode_step(const gdn_dims *dims, int32_t batch, int32_t tokens_per_seq,
+                                   const gdn_inputs *in, float *state, const int32_t *state_slots,
+                                   int32_t num_slots, int32_t out_dtype, void *out, void *stream)
+{
+    gdn::LinattnParams p{};
+    if (batch < 0 || tokens_per_seq < 1 || num_slots < 0)
+        return GDN_ERR_SHAPE;
+    const gdn_status st = check_linattn(dims, in, batch, out_dtype, out, state,
+                                        GDN_HEAD_DECAY | GDN_STREAM_STATE, p);
+    if (st != GDN_OK)
+        return st;
+    if (!state_slots && num_slots < batch)
+        return GDN_ERR_SHAPE;
+    if ((int64_t)batch * tokens_per_seq > kI32Max ||
+        gdn::linattn_decode_workgroups(batch, dims->num_v_heads, dims->head_dim_k, dims->head_dim_v) > kI32Max)
+        return GDN_ERR_OVERFLOW;
+    if (batch == 0)
+        return GDN_OK;
+    p.state = state;
+    p.slots = state_slots;
+    p.num_slots = num_slots;
+    p.out = out;
+    p.N = batch;
+    p.T = tokens_per_seq;
+    p.total = batch * tokens_per_seq;
+    return launch_status(gdn::launch_linattn_decode(p, static_cast<hipStream_t>(stream)));
+}
+
+size_t gdn_linattn_prefill_workspace_bytes(const gdn_dims *d, int32_t num_seqs, int32_t total_tokens)
+{
+    if (!d || num_seqs < 0 || total_tokens < 0 || d->num_k_heads < 1 || d->num_v_heads < 1 ||
+        d->num_v_heads % d->num_k_heads != 0 || !gdn::linattn_supported(d->head_dim_k, d->head_dim_v))
+        return 0;
+    return gdn::linattn_prefill_workspace_bytes(d->num_k_heads, d->num_v_heads, d->head_dim_k,
+                                                d->head_dim_v, num_seqs, total_tokens);
+}
+
+gdn_status gdn_linattn_prefill_chunked(const gdn_dims *dims, int32_t num_seqs,
+                                       const int32_t *cu_seqlens_host, const int32_t *cu_seqlens_dev,
+                                       int32_t total_tokens, const gdn_inputs *in, float *state,
+                                       int32_t out_dtype, void *out, void *workspace,
+                                       size_t workspace_bytes, void *stream)
+{
+    gdn::LinattnParams p{};
+    if (num_seqs < 0 || total_tokens < 0)
+        return GDN_ERR_SHAPE;
+    gdn_status st = check_linattn(dims, in, total_tokens, out_dtype, out, state, GDN_HEAD_DECAY, p);
+    if (st != GDN_OK)
+        return st;
+    if (!cu_seqlens_host || !cu_seqlens_dev)
+        return GDN_ERR_NULL;
+    if (num_seqs == 0)
+        return total_tokens == 0 ? GDN_OK : GDN_ERR_SHAPE;
+    int64_t chunks = 0, longest = 0;
+    st = check_cu(cu_seqlens_host, num_seqs, total_tokens, 1, &chunks, &longest);
+    if (st != GDN_OK)
+        return st;
+    if ((int64_t)total_tokens * dims->num_v_heads > kI32Max ||
+        gdn::linattn_decode_workgroups(num_seqs, dims->num_v_heads, dims->head_dim_k, dims->head_dim_v) > kI32Max)
+        return GDN_ERR_OVERFLOW;
+    if (total_tokens == 0)
+        return GDN_OK;  // every sequence empty: states untouched
+    const size_t need = gdn::linattn_prefill_workspace_bytes(
+        dims->num_k_heads, dims->num_v_heads, dims->head_dim_k, dims->head_dim_v, num_seqs, total_tokens);
+    if (!workspace || workspace_bytes < need)
+        return GDN_ERR_WORKSPACE;
+    if (!aligned(workspace, 256))
+        return GDN_ERR_ALIGN;
+    p.state = state;
+    p.num_slots = num_seqs;
+    p.out = out;
+    p.N = num_seqs;
+    p.T = (int)longest;
+    p.total = total_tokens;
+    p.cu = cu_seqlens_dev;
+    p.workspace = workspace;
+    return launch_status(gdn::launch_linattn_prefill(p, static_cast<hipStream_t>(stream)));
+}
+
+gdn_status gdn_add_rms_norm(const gdn_norm_args *a, void *stream)
+{
+    if (!a)
+        return GDN_ERR_NULL;
+    if (a->rows < 0 || a->hidden < 1)
+        return GDN_ERR_SHAPE;
+    if (!dtype_ok(a->dtype) || (a->out && !dtype_ok(a->out_dtype)))
+        return GDN_ERR_UNSUPPORTED;
+    if (!std::isfinite(a->eps) || a->eps < 0.f)
+        return GDN_ERR_SHAPE;
+    if (a->rows == 0)
+        return GDN_OK;
+    if (!a->x || !a->weight || (!a->out && !a->out_q) || (a->out_q != nullptr) != (a->out_scale != nullptr))
+        return GDN_ERR_NULL;
+    if (a->x_stride < a->hidden || (a->residual && a->residual_stride < a->hidden) ||
+        (a->residual_out && a->residual_out_stride < a->hidden) || (a->out && a->out_stride < a->hidden) ||
+        (a->out_q && a->out_q_stride < a->hidden))
+        return GDN_ERR_SHAPE;
+    const int64_t es = dtype_size(a->dtype);
+    if (!aligned(a->x, es) || !aligned(a->residual, es) || !aligned(a->residual_out, es) ||
+        !aligned(a->weight, 4) || (a->out && !aligned(a->out, dtype_size(a->out_dtype))) ||
+        !aligned(a->out_scale, 4))
+        return GDN_ERR_ALIGN;
+    gdn::NormParams p{};
+    p.rows = a->rows;
+    p.hidden = a->hidden;
+    p.dt = a->dtype;
+    p.out_dt = a->out_dtype;
+    p.x = a->x;
+    p.x_stride = a->x_stride;
+    p.residual = a->residual;
+    p.residual_stride = a->residual_stride;
+    p.residual_out = a->residual_out;
+    p.residual_out_stride = a->residual_out_stride;
+    p.weight = a->weight;
+    p.eps = a->eps > 0.f ? a->eps : 1e-6f;
+    p.out = a->out;
+    p.out_stride = a->out_stride;
+    p.out_q = a->out_q;
+    p.out_q_stride = a->out_q_stride;
+    p.out_scale = a->out_scale;
+    return launch_status(gdn::launch_norm(p, static_cast<hipStream_t>(stream)));
+}
+
+gdn_status gdn_quant_matmul(int32_t M, int32_t N, int32_t K, const int8_t *a, int64_t a_stride,
+                            const float *a_scale, const int8_t *w, int64_t w_stride,
+                            const float *w_scale, int32_t out_dtype, void *out, int64_t out_stride,
+                            void *stream)
+{
+    if (M < 0 || N < 0 || K < 1)
+        return GDN_ERR_SHAPE;
+    if (!dtype_ok(out_dtype) || K % 16 != 0)
+        return GDN_ERR_UNSUPPORTED;
+    // |a w| <= 2^14, so K products stay below 2^31; the grid's tiles are at least 16 x 16
+    if (K > 131056 || (((int64_t)M + 15) / 16) * (((int64_t)N + 15) / 16) > kI32Max)
+        return GDN_ERR_OVERFLOW;
+    if (M == 0 || N == 0)
+        return GDN_OK;
+    if (!a || !a_scale || !w || !w_scale || !out)
+        return GDN_ERR_NULL;
+    if (a_stride < K || w_stride < K || out_stride < N)
+        return GDN_ERR_SHAPE;
+    if (!aligned(a, 16) || !aligned(w, 16) || a_stride % 16 != 0 || w_stride % 16 != 0 ||
+        !aligned(a_scale, 4) || !aligned(w_scale, 4) || !aligned(out, dtype_size(out_dtype)))
+        return GDN_ERR_ALIGN;
+    gdn::MatmulParams p{};
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.a = a;
+    p.a_stride = a_stride;
+    p.a_scale = a_scale;
+    p.w = w;
+    p.w_stride = w_stride;
+    p.w_scale = w_scale;
+    p.out = out;
+    p.out_dt = out_dtype;
+    p.out_stride = out_stride;
+    return launch_status(gdn::launch_matmul(p, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,222 @@
+// gdn_linattn.hip -- decayed linear attention on gfx950: per v-head, with a state
+// S[dv][dk] (f32, key index innermost) and a log decay g_t,
+//     S <- exp(g_t) S + v_t k_t^T,   o_t = scale (S q_t).
+// The decay is one rate per head (GDN_HEAD_DECAY) or one value per token and head.
+//
+// recur_kernel runs the recurrence token by token: the decode step.
+//  * HBM bound: 0.5 flop per state byte. Every state row is loaded into VGPRs once
+//    per call, carried through the call's tokens and stored once.
+//  * Rows are independent (there is no delta rule to couple them), so a head's rows
+//    are split over workgroups as finely as the batch needs.
+//  * LPR lanes hold a row as float4 pieces, 16-byte loads of contiguous runs; the
+//    row's dot with q reduces over LPR <= 16 lanes on DPP alone. Lane r of a row
+//    group stores the output of the group's row r, so a wave's rows leave in one
+//    store instruction.
+//  * The next token's k, q, v and decay are loaded while the current one runs.
+
+#include "gdn_device.h"
+#include "gdn_kernels.h"
+
+namespace gdn {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+template <bool NT>
+__device__ __forceinline__ float4 load_row4(const float *p)
+{
+    f32x4 v;
+    if constexpr (NT)
+        v = __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(p));
+    else
+        v = *reinterpret_cast<const f32x4 *>(p);
+    return make_float4(v.x, v.y, v.z, v.w);
+}
+
+template <bool NT>
+__device__ __forceinline__ void store_row4(float *p, float4 s)
+{
+    f32x4 v = {s.x, s.y, s.z, s.w};
+    if constexpr (NT)
+        __builtin_nontemporal_store(v, reinterpret_cast<f32x4 *>(p));
+    else
+        *reinterpret_cast<f32x4 *>(p) = v;
+}
+
+// ---- the recurrence ----------------------------------------------------------
+
+constexpr int kRecurWaves = 4;
+
+// Lanes per state row: 16 lanes of one or more float4 pieces; 8 where a row has
+// too few pieces for 16 (dk = 32) or they do not divide (dk = 96).
+constexpr int recur_lpr(int dk) { return dk % 64 == 0 ? 16 : 8; }
+
+// Rows a workgroup of R rows per lane group covers.
+constexpr int recur_rows(int dk, int r) { return kRecurWaves * r * (64 / recur_lpr(dk)); }
+
+template <int DK, int QT, int R>
+struct RecurToken {
+    static constexpr int P = DK / (4 * recur_lpr(DK));
+    Raw4<QT> k[P], q[P];
+    uint32_t v[R];
+    float g;
+};
+
+template <int DK, int QT, int R>
+__device__ __forceinline__ void load_recur_token(RecurToken<DK, QT, R> &t, const LinattnParams &p,
+                                                 int64_t row, int h, int kh, int col, const int *vrow)
+{
+    constexpr int LPR = recur_lpr(DK);
+    const ActInputs &in = p.in;
+#pragma unroll
+    for (int m = 0; m < t.P; ++m) {
+        const int64_t c = (int64_t)kh * DK + col + 4 * LPR * m;
+        t.k[m] = load_raw4<QT>(in.k, row * in.k_stride + c);
+        t.q[m] = load_raw4<QT>(in.q, row * in.q_stride + c);
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        t.v[i] = load_raw1<QT>(in.v, row * in.v_stride + (int64_t)h * p.hc.dv + vrow[i]);
+    if (!(p.hc.flags & F_HEAD_DECAY))
+        t.g = in.g[row * p.hc.Hv + h + vgpr_zero()];
+}
+
+// One workgroup per (sequence, v-head, recur_rows rows). R rows per lane group.
+template <int DK, int QT, int R, bool NT>
+__global__ __launch_bounds__(64 * kRecurWaves) void recur_kernel(const LinattnParams p)
+{
+    constexpr int LPR = recur_lpr(DK), P = DK / (4 * LPR), ROWS = recur_rows(DK, R);
+    const int slices = (p.hc.dv + ROWS - 1) / ROWS;
+    const int slice = blockIdx.x % slices;
+    const int h = (blockIdx.x / slices) % p.hc.Hv;
+    const int b = blockIdx.x / slices / p.hc.Hv;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int r = lane % LPR, grp = lane / LPR;
+    const int col = 4 * r;
+
+    int64_t row0 = (int64_t)b * p.T;
+    int T = p.T;
+    if (p.cu) {
+        row0 = p.cu[b];
+        T = p.cu[b + 1] - p.cu[b];
+    }
+    const int slot = p.slots ? p.slots[b] : b;
+    if (slot < 0 || slot >= p.num_slots || T <= 0)
+        return;
+
+    // the group's R rows; rows past dv repeat the last one and store nothing
+    const int first = slice * ROWS + (wave * (64 / LPR) + grp) * R;
+    int vrow[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        vrow[i] = min(first + i, p.hc.dv - 1);
+    const int kh = k_head_of(p.hc.head_map, h, p.hc.Hk, p.hc.Hv);
+    RecurToken<DK, QT, R> tok;
+    load_recur_token<DK, QT, R>(tok, p, row0, h, kh, col, vrow);
+
+    float *sb = p.state + ((int64_t)slot * p.hc.Hv + h) * p.hc.dv * DK;
+    float4 S[R][P];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int m = 0; m < P; ++m)
+            S[i][m] = load_row4<NT>(sb + (int64_t)vrow[i] * DK + col + 4 * LPR * m);
+
+    if (p.hc.flags & F_HEAD_DECAY) {
+        const float d = p.in.decay_param[h];
+        tok.g = p.hc.decay_kind == 0 ? -expf(d) : d;
+    }
+    for (int t = 0; t < T; ++t) {
+        const RecurToken<DK, QT, R> cur = tok;
+        if (t + 1 < T)
+            load_recur_token<DK, QT, R>(tok, p, row0 + t + 1, h, kh, col, vrow);
+        const float a = expf(cur.g);
+        float o[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            o[i] = 0.f;
+#pragma unroll
+        for (int m = 0; m < P; ++m) {
+            const float4 k = raw4_to_f32<QT>(cur.k[m]), q = raw4_to_f32<QT>(cur.q[m]);
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const float v = raw1_to_f32<QT>(cur.v[i]);
+                float4 &s = S[i][m];
+                s.x = fmaf(v, k.x, a * s.x);
+                s.y = fmaf(v, k.y, a * s.y);
+                s.z = fmaf(v, k.z, a * s.z);
+                s.w = fmaf(v, k.w, a * s.w);
+                o[i] += dot4(s, q);
+            }
+        }
+        float mine = 0.f;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const float sum = group_sum<LPR>(o[i]);
+            mine = r == i ? sum : mine;
+        }
+        if (r < R && first + r < p.hc.dv)
+            store_act(p.out, ((row0 + t) * p.hc.Hv + h) * p.hc.dv + first + r, p.out_dt, p.hc.scale * mine);
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        if (first + i < p.hc.dv) {
+#pragma unroll
+            for (int m = 0; m < P; ++m)
+                store_row4<NT>(sb + (int64_t)vrow[i] * DK + col + 4 * LPR * m, S[i][m]);
+        }
+}
+
+template <int DK, int QT, int R, bool NT>
+hipError_t launch_recur_t(const LinattnParams &p, hipStream_t s)
+{
+    const int slices = (p.hc.dv + recur_rows(DK, R) - 1) / recur_rows(DK, R);
+    recur_kernel<DK, QT, R, NT><<<dim3((unsigned)((int64_t)p.N * p.hc.Hv * slices)), 64 * kRecurWaves, 0, s>>>(p);
+    return hipGetLastError();
+}
+
+template <int DK, int QT>
+hipError_t launch_recur_q(const LinattnParams &p, hipStream_t s)
+{
+    return p.hc.flags & F_STREAM_STATE ? launch_recur_t<DK, QT, 4, true>(p, s) : launch_recur_t<DK, QT, 4, false>(p, s);
+}
+
+template <int DK>
+hipError_t launch_recur_d(const LinattnParams &p, hipStream_t s)
+{
+    switch (p.in.qkv_dt) {
+    case DT_F32: return launch_recur_q<DK, DT_F32>(p, s);
+    case DT_F16: return launch_recur_q<DK, DT_F16>(p, s);
+    default: return launch_recur_q<DK, DT_BF16>(p, s);
+    }
+}
+
+hipError_t launch_recur(const LinattnParams &p, hipStream_t s)
+{
+    switch (p.hc.dk) {
+    case 32: return launch_recur_d<32>(p, s);
+    case 64: return launch_recur_d<64>(p, s);
+    case 96: return launch_recur_d<96>(p, s);
+    case 128: return launch_recur_d<128>(p, s);
+    default: return launch_recur_d<256>(p, s);
+    }
+}
+
+}  // namespace
+
+bool linattn_supported(int dk, int dv) { return decode_supported(dk, dv); }
+
+// Workgroups of the recurrence for the smallest split it uses: the host checks that
+// the grid stays within 31 bits.
+int64_t linattn_decode_workgroups(int N, int Hv, int dk, int dv)
+{
+    return (int64_t)N * Hv * ((dv + recur_rows(dk, 1) - 1) / recur_rows(dk, 1));
+}
+
+hipError_t launch_linattn_decode(const LinattnParams &p, hipStream_t s) { return launch_recur(p, s); }
+
+size_t linattn_prefill_workspace_bytes(int, int, int, int, int, int64_t) { return 256; }
+
+hipError_t launch_linattn_prefill(const LinattnParams &p, hipStream_t s) { return launch_recur(p, s); }
+
+}  // namespace gdn

@@ -24,12 +24,14 @@ NOALLOC_SCRATCH_BYTES = 64 << 20
 F32, F16, BF16 = 0, 1, 2
 MAP_GROUPED, MAP_TILED = 0, 1
 DECAY_LOG_RATE, DECAY_NEGATIVE_RATE = 0, 1
-L2NORM_QK, RAW_GATES, GATED_NORM, STREAM_STATE = 1, 2, 4, 8
+L2NORM_QK, RAW_GATES, GATED_NORM, STREAM_STATE, HEAD_DECAY = 1, 2, 4, 8, 16
 CHUNK = 64
 
 EXPORTED = ["gdn_conv_update", "gdn_decode_step", "gdn_prefill_workspace_bytes",
             "gdn_prefill_chunked", "gdn_status_string", "gdn_version", "gdn_decode_layer",
-            "gdn_decode_launch_info", "gdn_prefill_launch_info", "gdn_prefill_chunked_noalloc"]
+            "gdn_decode_launch_info", "gdn_prefill_launch_info", "gdn_prefill_chunked_noalloc",
+            "gdn_linattn_decode_step", "gdn_linattn_prefill_workspace_bytes",
+            "gdn_linattn_prefill_chunked", "gdn_add_rms_norm", "gdn_quant_matmul"]
 
 _DT = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 _VP = ctypes.c_void_p
@@ -65,6 +67,16 @@ class LaunchInfo(ctypes.Structure):
 
     def as_dict(self):
         return {n: getattr(self, n) for n, _ in self._fields_}
+
+
+class NormArgs(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("hidden", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("x", _VP), ("x_stride", ctypes.c_int64),
+                ("residual", _VP), ("residual_stride", ctypes.c_int64),
+                ("residual_out", _VP), ("residual_out_stride", ctypes.c_int64),
+                ("weight", _VP), ("eps", ctypes.c_float), ("out_dtype", ctypes.c_int32),
+                ("out", _VP), ("out_stride", ctypes.c_int64),
+                ("out_q", _VP), ("out_q_stride", ctypes.c_int64), ("out_scale", _VP)]
 
 
 class GdnError(RuntimeError):
@@ -119,6 +131,18 @@ def load() -> ctypes.CDLL:
     lib.gdn_prefill_launch_info.argtypes = [ctypes.POINTER(Dims), ctypes.c_int32, _VP,
                                             ctypes.c_int32, ctypes.c_int32,
                                             ctypes.POINTER(LaunchInfo)]
+    lib.gdn_linattn_decode_step.restype = ctypes.c_int
+    lib.gdn_linattn_decode_step.argtypes = lib.gdn_decode_step.argtypes
+    lib.gdn_linattn_prefill_workspace_bytes.restype = ctypes.c_size_t
+    lib.gdn_linattn_prefill_workspace_bytes.argtypes = lib.gdn_prefill_workspace_bytes.argtypes
+    lib.gdn_linattn_prefill_chunked.restype = ctypes.c_int
+    lib.gdn_linattn_prefill_chunked.argtypes = lib.gdn_prefill_chunked.argtypes
+    lib.gdn_add_rms_norm.restype = ctypes.c_int
+    lib.gdn_add_rms_norm.argtypes = [ctypes.POINTER(NormArgs), _VP]
+    lib.gdn_quant_matmul.restype = ctypes.c_int
+    lib.gdn_quant_matmul.argtypes = [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _VP,
+                                     ctypes.c_int64, _VP, _VP, ctypes.c_int64, _VP,
+                                     ctypes.c_int32, _VP, ctypes.c_int64, _VP]
     _LIB = lib
     return lib
 
@@ -554,3 +578,272 @@ def prepare_prefill_chunked(q, k, v, state, cu_seqlens_dev, cu_seqlens_host, out
     return PreparedCall(load().gdn_prefill_chunked, args, "gdn_prefill_chunked",
                         keep + [dims, inp, state, out, workspace, cu_seqlens_dev,
                                 cu_seqlens_host])
+
+
+# ---- decayed linear attention, residual RMS norm with 8-bit output, int8 product ----
+# These calls run on the tensors' own device, whatever the current one is. What they
+# allocate (outputs, workspaces, offset copies) is allocated on the stream they run on,
+# so its memory is not handed out again before the kernels have read it.
+
+def _device_of(**tensors):
+    """The one GPU that every given tensor is on."""
+    device = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be on the GPU")
+        if device is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, other tensors are on {device}")
+        device = t.device
+    return device
+
+
+class _RunOn:
+    """The device and stream a call runs on, made current while it is prepared and
+    issued. stream: the caller's, or the current stream of the tensors' device."""
+
+    def __init__(self, device, stream):
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+        elif stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+        self.handle = ctypes.c_void_p(stream.cuda_stream)
+        self._context = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        self._context.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        return self._context.__exit__(*exc)
+
+
+class DeviceCall(PreparedCall):
+    """A prepared call that is issued on its tensors' device, whatever the current
+    device is. ``out`` is what the call returns."""
+
+    def __init__(self, fn, args, what, keep, device, out):
+        super().__init__(fn, args, what, keep)
+        self._device, self.out = device, out
+
+    def launch(self):
+        if torch.cuda.current_device() == self._device.index:
+            st = self._fn(*self._args)
+        else:
+            with torch.cuda.device(self._device):
+                st = self._fn(*self._args)
+        if st != GDN_OK:
+            raise GdnError(st, self._what)
+
+
+def _linattn_args(q, k, v, state, out, tokens, *, Hk, Hv, dk, dv, head_map, g, decay_param, decay,
+                  scale, stream_state=False):
+    """(dims, inputs, tensors to keep) of a gdn_linattn_* call over `tokens` rows."""
+    if (g is None) == (decay_param is None):
+        raise ValueError("give g [tokens][Hv] or decay_param [Hv], one of the two")
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t.dim() < 2 or t.shape[0] != tokens:
+            raise ValueError(f"{name} must have {tokens} token rows, got {tuple(t.shape)}")
+    inp, keep = make_inputs(q, k, v, Hk=Hk, Hv=Hv, dk=dk, dv=dv)
+    flags = STREAM_STATE if stream_state else 0
+    name, t, shape = ("g", g, (tokens, Hv)) if decay_param is None else ("decay_param", decay_param, (Hv,))
+    if t.dtype != torch.float32 or not t.is_contiguous() or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be contiguous float32 {list(shape)}")
+    if decay_param is None:
+        inp.g = _ptr(t)
+    else:
+        inp.decay_param = _ptr(t)
+        flags |= HEAD_DECAY
+    _check_state(state, Hv, dv, dk)
+    _check_out(out, tokens, Hv, dv)
+    dims = make_dims(Hk, Hv, dk, dv, head_map, flags, decay, scale)
+    return dims, inp, keep + [t, state, out]
+
+
+def prepare_linattn_decode_step(q, k, v, state, out, *, Hk, Hv, dk, dv, head_map, batch,
+                                tokens_per_seq=1, g=None, decay_param=None,
+                                decay=DECAY_LOG_RATE, scale=0.0, state_slots=None,
+                                stream_state=False, stream=None) -> DeviceCall:
+    """linattn_decode_step with its arguments checked and marshalled once."""
+    device = _device_of(state=state, q=q, k=k, v=v, out=out, g=g, decay_param=decay_param,
+                        state_slots=state_slots)
+    dims, inp, keep = _linattn_args(q, k, v, state, out, batch * tokens_per_seq, Hk=Hk, Hv=Hv,
+                                    dk=dk, dv=dv, head_map=head_map, g=g, decay_param=decay_param,
+                                    decay=decay, scale=scale, stream_state=stream_state)
+    _check_slots(state_slots, batch)
+    args = (ctypes.byref(dims), batch, tokens_per_seq, ctypes.byref(inp), _ptr(state),
+            _ptr(state_slots), state.shape[0], _dt(out), _ptr(out), _RunOn(device, stream).handle)
+    return DeviceCall(load().gdn_linattn_decode_step, args, "gdn_linattn_decode_step",
+                      keep + [dims, inp, state_slots], device, out)
+
+
+def linattn_decode_step(q, k, v, state, *, Hk, Hv, dk, dv, head_map, batch, tokens_per_seq=1,
+                        g=None, decay_param=None, decay=DECAY_LOG_RATE, scale=0.0,
+                        state_slots=None, out=None, out_dtype=torch.float32, stream_state=False,
+                        stream=None):
+    """One call of gdn_linattn_decode_step: S <- exp(g) S + v k^T, o = scale (S q) for each
+    token. q, k [B*T][Hk*dk], v [B*T][Hv*dv] (views of a mixed row allowed); the log decay is
+    g [B*T][Hv] f32, or one rate per head from decay_param [Hv] f32; state [slots][Hv][dv][dk]
+    f32 updated in place, the slots of one call distinct. Returns out [B*T][Hv][dv]."""
+    with _RunOn(_device_of(state=state), stream):
+        if out is None:
+            out = torch.empty((batch * tokens_per_seq, Hv, dv), dtype=out_dtype, device=state.device)
+        prepare_linattn_decode_step(q, k, v, state, out, Hk=Hk, Hv=Hv, dk=dk, dv=dv,
+                                    head_map=head_map, batch=batch, tokens_per_seq=tokens_per_seq,
+                                    g=g, decay_param=decay_param, decay=decay, scale=scale,
+                                    state_slots=state_slots, stream_state=stream_state).launch()
+    return out
+
+
+def linattn_prefill_workspace_bytes(*, Hk, Hv, dk, dv, num_seqs, total_tokens,
+                                    head_map=MAP_GROUPED):
+    """Workspace gdn_linattn_prefill_chunked needs."""
+    dims = make_dims(Hk, Hv, dk, dv, head_map, 0)
+    return int(load().gdn_linattn_prefill_workspace_bytes(ctypes.byref(dims), num_seqs, total_tokens))
+
+
+def prepare_linattn_prefill_chunked(q, k, v, state, cu_seqlens_dev, cu_seqlens_host, out, workspace,
+                                    *, Hk, Hv, dk, dv, head_map, g=None, decay_param=None,
+                                    decay=DECAY_LOG_RATE, scale=0.0, stream=None) -> DeviceCall:
+    """linattn_prefill_chunked with its arguments checked and marshalled once: the offsets as
+    int32 [N+1] tensors on the GPU and on the host, the workspace a contiguous uint8 tensor."""
+    device = _device_of(state=state, q=q, k=k, v=v, out=out, g=g, decay_param=decay_param,
+                        cu_seqlens_dev=cu_seqlens_dev, workspace=workspace)
+    for name, t in (("cu_seqlens_dev", cu_seqlens_dev), ("cu_seqlens_host", cu_seqlens_host)):
+        if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous 1-d int32 tensor")
+    if cu_seqlens_host.device.type != "cpu" or cu_seqlens_host.numel() != cu_seqlens_dev.numel() or \
+            cu_seqlens_host.numel() < 1:
+        raise ValueError("cu_seqlens_host must hold cu_seqlens_dev's offsets on the host")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    N, total = cu_seqlens_host.numel() - 1, int(cu_seqlens_host[-1])
+    if state.shape[0] != N:
+        raise ValueError(f"state must hold one slot per sequence ({N})")
+    dims, inp, keep = _linattn_args(q, k, v, state, out, total, Hk=Hk, Hv=Hv, dk=dk, dv=dv,
+                                    head_map=head_map, g=g, decay_param=decay_param, decay=decay,
+                                    scale=scale)
+    args = (ctypes.byref(dims), N, ctypes.c_void_p(cu_seqlens_host.data_ptr()),
+            _ptr(cu_seqlens_dev), total, ctypes.byref(inp), _ptr(state), _dt(out), _ptr(out),
+            _ptr(workspace), workspace.numel() * workspace.element_size(),
+            _RunOn(device, stream).handle)
+    return DeviceCall(load().gdn_linattn_prefill_chunked, args, "gdn_linattn_prefill_chunked",
+                      keep + [dims, inp, workspace, cu_seqlens_dev, cu_seqlens_host], device, out)
+
+
+def linattn_prefill_chunked(q, k, v, state, cu_seqlens, *, Hk, Hv, dk, dv, head_map, g=None,
+                            decay_param=None, decay=DECAY_LOG_RATE, scale=0.0, out=None,
+                            out_dtype=torch.float32, workspace=None, cu_seqlens_host=None,
+                            stream=None):
+    """One call of gdn_linattn_prefill_chunked over packed sequences (cu_seqlens integer [N+1],
+    on either side; cu_seqlens_host saves the copy to the host). The log decay is
+    g [tokens][Hv] f32 or one rate per head from decay_param [Hv] f32. state [N][Hv][dv][dk] f32:
+    initial in, final out. Returns out [tokens][Hv][dv]."""
+    with _RunOn(_device_of(state=state), stream):
+        cu_host = _cu_host(cu_seqlens if cu_seqlens_host is None else cu_seqlens_host)
+        cu_dev = _cu_device(cu_seqlens, state.device)
+        N, total = cu_host.numel() - 1, int(cu_host[-1]) if cu_host.numel() else 0
+        if out is None:
+            out = torch.empty((total, Hv, dv), dtype=out_dtype, device=state.device)
+        if workspace is None:
+            need = linattn_prefill_workspace_bytes(Hk=Hk, Hv=Hv, dk=dk, dv=dv, num_seqs=N,
+                                                   total_tokens=total)
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=state.device)
+        prepare_linattn_prefill_chunked(q, k, v, state, cu_dev, cu_host, out, workspace, Hk=Hk,
+                                        Hv=Hv, dk=dk, dv=dv, head_map=head_map, g=g,
+                                        decay_param=decay_param, decay=decay, scale=scale).launch()
+    return out
+
+
+def _rows(name, t, rows, hidden, dtypes):
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    if t.dim() != 2 or tuple(t.shape) != (rows, hidden) or (hidden > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [{rows}][{hidden}] with contiguous rows, "
+                         f"got {tuple(t.shape)}")
+    return t.stride(0) if rows > 1 else max(t.stride(0), hidden)
+
+
+def prepare_add_rms_norm(x, weight, *, residual=None, residual_out=None, out=None, out_q=None,
+                         out_scale=None, eps=0.0, stream=None) -> DeviceCall:
+    """add_rms_norm into the caller's buffers, checked and marshalled once: residual_out
+    [rows][hidden] (x's or residual's own buffer allowed), out [rows][hidden], out_q int8
+    [rows][hidden] with out_scale [rows] f32; each may be None, out and out_q not both."""
+    device = _device_of(x=x, weight=weight, residual=residual, residual_out=residual_out, out=out,
+                        out_q=out_q, out_scale=out_scale)
+    if x.dim() != 2:
+        raise ValueError("x must be [rows][hidden]")
+    rows, hidden = x.shape
+    args = NormArgs(rows=rows, hidden=hidden, dtype=_dt(x), x=_ptr(x),
+                    x_stride=_rows("x", x, rows, hidden, _DT), weight=_ptr(weight), eps=eps)
+    if weight.dtype != torch.float32 or not weight.is_contiguous() or tuple(weight.shape) != (hidden,):
+        raise ValueError(f"weight must be contiguous float32 [{hidden}]")
+    if residual is not None:
+        args.residual, args.residual_stride = _ptr(residual), _rows("residual", residual, rows, hidden, (x.dtype,))
+    if residual_out is not None:
+        args.residual_out = _ptr(residual_out)
+        args.residual_out_stride = _rows("residual_out", residual_out, rows, hidden, (x.dtype,))
+    if out is not None:
+        args.out, args.out_dtype, args.out_stride = _ptr(out), _dt(out), _rows("out", out, rows, hidden, _DT)
+    if out_q is not None:
+        args.out_q, args.out_q_stride = _ptr(out_q), _rows("out_q", out_q, rows, hidden, (torch.int8,))
+    if out_scale is not None:
+        if out_scale.dtype != torch.float32 or not out_scale.is_contiguous() or tuple(out_scale.shape) != (rows,):
+            raise ValueError(f"out_scale must be contiguous float32 [{rows}]")
+        args.out_scale = _ptr(out_scale)
+    return DeviceCall(load().gdn_add_rms_norm, (ctypes.byref(args), _RunOn(device, stream).handle),
+                      "gdn_add_rms_norm",
+                      [args, x, weight, residual, residual_out, out, out_q, out_scale], device,
+                      (out, residual_out, out_q, out_scale))
+
+
+def add_rms_norm(x, weight, *, residual=None, residual_out=None, out=None, out_dtype=None,
+                 quantize=False, eps=0.0, stream=None):
+    """One call of gdn_add_rms_norm: h = x + residual; y = h rsqrt(mean h^2 + eps) weight.
+    x, residual [rows][hidden] (rows may be strided), weight [hidden] f32. Returns a dict of
+    new tensors: `out` y in out_dtype (default x's; with quantize only if out_dtype is given),
+    `residual` h (with a residual; in residual_out if given, which may be x or residual
+    itself), and with quantize `out_q` int8 and `out_scale` [rows] f32, ready for quant_matmul."""
+    with _RunOn(_device_of(x=x), stream):
+        if x.dim() != 2:
+            raise ValueError("x must be [rows][hidden]")
+        rows, hidden = x.shape
+        new = lambda dtype, *shape: torch.empty(shape, dtype=dtype, device=x.device)  # noqa: E731
+        if out is None and (out_dtype is not None or not quantize):
+            out = new(out_dtype or x.dtype, rows, hidden)
+        if residual is not None and residual_out is None:
+            residual_out = new(x.dtype, rows, hidden)
+        out_q, out_scale = (new(torch.int8, rows, hidden), new(torch.float32, rows)) if quantize else (None, None)
+        prepare_add_rms_norm(x, weight, residual=residual, residual_out=residual_out, out=out,
+                             out_q=out_q, out_scale=out_scale, eps=eps).launch()
+    got = dict(out=out, residual=residual_out, out_q=out_q, out_scale=out_scale)
+    return {name: t for name, t in got.items() if t is not None}
+
+
+def prepare_quant_matmul(a, a_scale, w, w_scale, out, *, stream=None) -> DeviceCall:
+    """quant_matmul into the caller's out [M][N], checked and marshalled once."""
+    device = _device_of(a=a, a_scale=a_scale, w=w, w_scale=w_scale, out=out)
+    if a.dim() != 2 or w.dim() != 2 or a.shape[1] != w.shape[1]:
+        raise ValueError("a must be [M][K] and w [N][K]")
+    (M, K), N = a.shape, w.shape[0]
+    strides = [_rows("a", a, M, K, (torch.int8,)), _rows("w", w, N, K, (torch.int8,)),
+               _rows("out", out, M, N, _DT)]
+    for name, t, n in (("a_scale", a_scale, M), ("w_scale", w_scale, N)):
+        if t.dtype != torch.float32 or not t.is_contiguous() or t.numel() != n:
+            raise ValueError(f"{name} must be contiguous float32 [{n}]")
+    args = (M, N, K, _ptr(a), strides[0], _ptr(a_scale), _ptr(w), strides[1], _ptr(w_scale), _dt(out),
+            _ptr(out), strides[2], _RunOn(device, stream).handle)
+    return DeviceCall(load().gdn_quant_matmul, args, "gdn_quant_matmul",
+                      [a, a_scale, w, w_scale, out], device, out)
+
+
+def quant_matmul(a, a_scale, w, w_scale, *, out=None, out_dtype=torch.bfloat16, stream=None):
+    """One call of gdn_quant_matmul: out[m][n] = (sum_k a[m][k] w[n][k]) a_scale[m] w_scale[n].
+    a [M][K] and w [N][K] int8 (rows may be strided by multiples of 16 bytes), a_scale [M] and
+    w_scale [N] f32. Returns out [M][N]."""
+    with _RunOn(_device_of(a=a), stream):
+        if out is None:
+            out = torch.empty((a.shape[0], w.shape[0]), dtype=out_dtype, device=a.device)
+        prepare_quant_matmul(a, a_scale, w, w_scale, out).launch()
+    return out

@@ -13,6 +13,11 @@
  * inputs, L2 norm of q and k, the softplus/sigmoid gates, the grouped or tiled
  * k-head map, and the gated RMS norm of the output.
  *
+ * Beside it: linear attention with a decay per head (the same state without the
+ * delta rule), and what feeds a layer in 8 bits -- the RMS norm with the residual's
+ * addition and an 8-bit output, and the product of 8-bit integers that projects
+ * it to the mixed q, k, v row.
+ *
  * Conventions shared by every entry point
  *  - Every array pointer is a DEVICE pointer unless its comment says "host".
  *    The caller owns all memory; the library allocates nothing and keeps no
@@ -84,7 +89,11 @@ enum {
      * cache holds). The state is loaded and stored with non-temporal hints;
      * results are bit for bit those of a call without the flag. On states the
      * cache does keep, the flag makes the step slower. */
-    GDN_STREAM_STATE = 8u
+    GDN_STREAM_STATE = 8u,
+    /* gdn_linattn_* only (the gated delta entry points return UNSUPPORTED): every
+     * token of v-head h decays by the one rate that decay_param[h] gives
+     * (gdn_dims.decay). Without it the log decay is g, per token and head. */
+    GDN_HEAD_DECAY = 16u
 };
 
 typedef struct gdn_dims {
@@ -291,6 +300,124 @@ gdn_status gdn_prefill_chunked_noalloc(const gdn_dims *dims, int32_t num_seqs,
                                        const int32_t *cu_seqlens_dev, int32_t total_tokens,
                                        const gdn_inputs *in, float *state, int32_t out_dtype,
                                        void *out, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Linear attention with a decay: per v-head and token,
+ *
+ *     S <- exp(g) S + v k^T,   o = scale (S q)
+ *
+ * on the state layout, head maps, activations (gdn_inputs: q, k, v with their
+ * strides and dtype) and head shapes of the gated delta entry points.
+ *
+ *   dims   flags: GDN_HEAD_DECAY, and GDN_STREAM_STATE for the decode step; others
+ *          UNSUPPORTED. l2_eps and norm_eps are ignored.
+ *   in     with GDN_HEAD_DECAY the log decay of head h is -exp(decay_param[h])
+ *          (GDN_DECAY_LOG_RATE) or decay_param[h] (GDN_DECAY_NEGATIVE_RATE), [Hv]
+ *          f32; without it in->g [tokens][Hv] f32. Both 4-byte aligned. The other
+ *          gate fields, z and norm_weight are ignored.
+ *
+ * A log decay is at most 0. -inf stands for exp(g) = 0: the state is forgotten.
+ * A NaN or infinity in q, k, v or the state goes where the formula takes it (a
+ * later exp(g) = 0 does not clear it).
+ * Sums are f32 or more exact. A call without tokens does nothing, whatever its
+ * per-token pointers.
+ * ------------------------------------------------------------------------- */
+
+/* gdn_linattn_decode_step -- B sequences of T tokens each; arguments, slots and
+ * errors as gdn_decode_step's. Each state is read and written once per call. The
+ * slots that a call names must differ from one another: a slot named twice holds
+ * either sequence's rows afterwards. */
+gdn_status gdn_linattn_decode_step(const gdn_dims *dims, int32_t batch, int32_t tokens_per_seq,
+                                   const gdn_inputs *in, float *state, const int32_t *state_slots,
+                                   int32_t num_slots, int32_t out_dtype, void *out, void *stream);
+
+/* gdn_linattn_prefill_workspace_bytes -- device workspace that
+ * gdn_linattn_prefill_chunked needs for at most num_seqs sequences and total_tokens
+ * packed tokens. Returns 0 when the arguments are invalid. */
+size_t gdn_linattn_prefill_workspace_bytes(const gdn_dims *dims, int32_t num_seqs,
+                                           int32_t total_tokens);
+
+/* gdn_linattn_prefill_chunked -- the same over packed variable-length sequences;
+ * arguments and errors as gdn_prefill_chunked's. An empty sequence keeps its state.
+ * The workspace is scratch: calls that may overlap in time (other streams, two
+ * captured graphs) need one each. */
+gdn_status gdn_linattn_prefill_chunked(const gdn_dims *dims, int32_t num_seqs,
+                                       const int32_t *cu_seqlens_host,
+                                       const int32_t *cu_seqlens_dev, int32_t total_tokens,
+                                       const gdn_inputs *in, float *state, int32_t out_dtype,
+                                       void *out, void *workspace, size_t workspace_bytes,
+                                       void *stream);
+
+/* ---------------------------------------------------------------------------
+ * gdn_add_rms_norm -- RMS norm of rows, with the residual's addition before it and
+ * an 8-bit output after it, each as the caller asks:
+ *
+ *     h = x + residual;   y = h (mean_i h_i^2 + eps)^(-1/2) weight
+ *     residual_out = h;   out = y;   out_scale = max_i |y_i| / 127
+ *     out_q = y 127 / max_i |y_i|, rounded to nearest, ties to even
+ *
+ * computed in f32 from the unrounded h, each output rounded once.
+ * A row whose largest |y| is below 2^-100 has out_q = 0 and out_scale = 0. A row
+ * with an infinite or NaN y has out_q = 0 and out_scale = NaN.
+ *
+ *   rows, hidden   >= 0 rows of >= 1 elements
+ *   dtype          of x, residual and residual_out
+ *   x, residual    rows of x_stride / residual_stride elements (>= hidden), aligned to
+ *                  their element size; residual may be NULL (h = x)
+ *   residual_out   NULL, or rows of residual_out_stride elements; may be x's or
+ *                  residual's own buffer (same pointer and stride), else may not
+ *                  overlap an input
+ *   weight         [hidden] f32, 4-byte aligned
+ *   eps            0 selects 1e-6
+ *   out            NULL, or rows of out_stride elements of out_dtype; may be x's own
+ *                  buffer (same pointer, stride and dtype), else may not overlap an input
+ *   out_q          NULL, or int8 rows of out_q_stride; out_scale [rows] f32 goes with it
+ *                  (both or neither)
+ * At least one of out and out_q. Outputs may not overlap one another.
+ * Errors: NULL, SHAPE (counts, strides, eps), UNSUPPORTED (dtype), ALIGN, LAUNCH.
+ * ------------------------------------------------------------------------- */
+typedef struct gdn_norm_args {
+    int32_t rows, hidden;
+    int32_t dtype;
+    const void *x;
+    int64_t x_stride;
+    const void *residual;
+    int64_t residual_stride;
+    void *residual_out;
+    int64_t residual_out_stride;
+    const float *weight;
+    float eps;
+    int32_t out_dtype;
+    void *out;
+    int64_t out_stride;
+    int8_t *out_q;
+    int64_t out_q_stride;
+    float *out_scale;
+} gdn_norm_args;
+gdn_status gdn_add_rms_norm(const gdn_norm_args *args, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * gdn_quant_matmul -- product of 8-bit integers with a scale for each token (row of
+ * a) and each channel (row of w):
+ *
+ *     out[m][n] = (sum_k a[m][k] w[n][k]) a_scale[m] w_scale[n]
+ *
+ * The integer sums are exact (32 bits); the scales are applied in f32 and the result is
+ * rounded once. A NaN scale makes its row or column NaN.
+ *
+ *   M, N, K      M, N >= 0; K >= 1 a multiple of 16 (else UNSUPPORTED), at most 131056
+ *                (else OVERFLOW: the sum could leave 32 bits)
+ *   a            [M] int8 rows of a_stride bytes (>= K)
+ *   w            [N] int8 rows of w_stride bytes (>= K): a torch Linear's weight layout
+ *                a, w and both strides are multiples of 16 bytes
+ *   a_scale      [M] f32; w_scale [N] f32; 4-byte aligned
+ *   out          [M] rows of out_stride elements (>= N) of out_dtype, aligned to the element
+ * Errors: NULL, SHAPE, UNSUPPORTED, OVERFLOW, ALIGN, LAUNCH.
+ * ------------------------------------------------------------------------- */
+gdn_status gdn_quant_matmul(int32_t M, int32_t N, int32_t K, const int8_t *a, int64_t a_stride,
+                            const float *a_scale, const int8_t *w, int64_t w_stride,
+                            const float *w_scale, int32_t out_dtype, void *out,
+                            int64_t out_stride, void *stream);
 
 /* ---------------------------------------------------------------------------
  * Kernel selection, for inspection and host-side tests. Which kernel a call runs
