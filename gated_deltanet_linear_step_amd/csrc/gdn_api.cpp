@@ -579,7 +579,7 @@ gdn_status gdn_linattn_prefill_chunked(const gdn_dims *dims, int32_t num_seqs,
     p.total = total_tokens;
     p.cu = cu_seqlens_dev;
     p.workspace = workspace;
-    return launch_status(gdn::launch_linattn_prefill(p, static_cast<hipStream_t>(stream)));
+    return launch_status(gdn::launch_linattn_prefill(p, cu_seqlens_host, static_cast<hipStream_t>(stream)));
 }
 
 gdn_status gdn_add_rms_norm(const gdn_norm_args *a, void *stream)

@@ -143,12 +143,21 @@ struct LinattnParams {
     int total;
     const int32_t *cu;
     void *workspace;
+    // prefill: sequences are split into segments of seg_tokens; states after (and
+    // summed log decays of) each segment but a sequence's last, [slot][Hv]
+    int seg_tokens;
+    float *seg_state, *seg_decay;
 };
 bool linattn_supported(int dk, int dv);
 int64_t linattn_decode_workgroups(int N, int Hv, int dk, int dv);
 hipError_t launch_linattn_decode(const LinattnParams &p, hipStream_t s);
 size_t linattn_prefill_workspace_bytes(int Hk, int Hv, int dk, int dv, int N, int64_t total_tokens);
-hipError_t launch_linattn_prefill(const LinattnParams &p, hipStream_t s);
+// cu: the offsets on the host
+hipError_t launch_linattn_prefill(const LinattnParams &p, const int32_t *cu, hipStream_t s);
+// The chunk kernels per activation dtype (gdn_linattn_chunk.h): `second` the later segments
+hipError_t launch_linattn_chunk_bf16(const LinattnParams &p, int blocks, bool second, hipStream_t s);
+hipError_t launch_linattn_chunk_f16(const LinattnParams &p, int blocks, bool second, hipStream_t s);
+hipError_t launch_linattn_chunk_f32(const LinattnParams &p, int blocks, bool second, hipStream_t s);
 
 // RMS norm with residual and 8-bit output (gdn_norm.hip). Strides in elements.
 struct NormParams {

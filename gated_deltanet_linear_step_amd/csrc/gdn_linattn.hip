@@ -17,6 +17,8 @@
 #include "gdn_device.h"
 #include "gdn_kernels.h"
 
+#include <algorithm>
+
 namespace gdn {
 namespace {
 
@@ -215,8 +217,95 @@ int64_t linattn_decode_workgroups(int N, int Hv, int dk, int dv)
 
 hipError_t launch_linattn_decode(const LinattnParams &p, hipStream_t s) { return launch_recur(p, s); }
 
-size_t linattn_prefill_workspace_bytes(int, int, int, int, int, int64_t) { return 256; }
+// ---- the chunked prefill (kernels: gdn_linattn_chunk.h) ------------------------
 
-hipError_t launch_linattn_prefill(const LinattnParams &p, hipStream_t s) { return launch_recur(p, s); }
+namespace {
+
+// Segments are a multiple of 64 tokens (whole chunks of 64 or 32), at least kMinSegment,
+// and long enough that a call's segments number about kSegments over all heads: two
+// workgroups for each of the 256 CUs.
+constexpr int kMinSegment = 256, kSegments = 512;
+
+int segment_tokens(int Hv, int64_t total)
+{
+    const int64_t per = (total * Hv + kSegments - 1) / kSegments;
+    return (int)std::max<int64_t>(kMinSegment, (per + 63) / 64 * 64);
+}
+
+// States between segments a call may need: total / segment_tokens of them per head, at
+// most total / kMinSegment and kSegments / Hv. Grows with total.
+int64_t segment_slots(int Hv, int64_t total)
+{
+    return std::min<int64_t>(total / kMinSegment, kSegments / Hv + 1);
+}
+
+// Entering states: slot s of a sequence (state after its segment s, entered with zero
+// from s = 1 on) becomes the state after segment s. HBM bound, one float4 a thread; the
+// loads of later segments do not wait for the running sum.
+__global__ __launch_bounds__(256) void scan_kernel(const LinattnParams p, int vecs)
+{
+    const int blocks = (vecs + 255) / 256;
+    const int part = blockIdx.x % blocks, h = blockIdx.x / blocks % p.hc.Hv, seq = blockIdx.x / blocks / p.hc.Hv;
+    const int at = part * 256 + threadIdx.x;
+    const int first = p.cu[seq], len = p.cu[seq + 1] - first;
+    const int segs = (len + p.seg_tokens - 1) / p.seg_tokens;
+    if (segs < 3 || at >= vecs)
+        return;
+    const int64_t step = (int64_t)p.hc.Hv * vecs;
+    const int64_t slot = (int64_t)(first / p.seg_tokens) * p.hc.Hv + h;
+    float4 *x = reinterpret_cast<float4 *>(p.seg_state) + slot * vecs + at;
+    const float *d = p.seg_decay + slot;
+    float4 run = *x;
+#pragma unroll 4
+    for (int s = 1; s < segs - 1; ++s) {
+        const float4 add = x[s * step];
+        const float a = expf(d[(int64_t)s * p.hc.Hv]);
+        run = make_float4(fmaf(a, run.x, add.x), fmaf(a, run.y, add.y), fmaf(a, run.z, add.z), fmaf(a, run.w, add.w));
+        x[s * step] = run;
+    }
+}
+
+hipError_t launch_chunk_dt(const LinattnParams &p, int64_t segments, bool second, hipStream_t s)
+{
+    const int blocks = (int)(segments * p.hc.Hv);
+    switch (p.in.qkv_dt) {
+    case DT_F32: return launch_linattn_chunk_f32(p, blocks, second, s);
+    case DT_F16: return launch_linattn_chunk_f16(p, blocks, second, s);
+    default: return launch_linattn_chunk_bf16(p, blocks, second, s);
+    }
+}
+
+}  // namespace
+
+size_t linattn_prefill_workspace_bytes(int, int Hv, int dk, int dv, int, int64_t total)
+{
+    return 256 + (size_t)segment_slots(Hv, total) * Hv * (4 * (size_t)dk * dv + 4);
+}
+
+hipError_t launch_linattn_prefill(const LinattnParams &given, const int32_t *cu, hipStream_t s)
+{
+    LinattnParams p = given;
+    p.seg_tokens = segment_tokens(p.hc.Hv, p.total);
+    p.seg_state = static_cast<float *>(p.workspace);
+    p.seg_decay = p.seg_state + segment_slots(p.hc.Hv, p.total) * p.hc.Hv * p.hc.dk * p.hc.dv;
+    int64_t first = 0, second = 0, longest = 0;
+    for (int i = 0; i < p.N; ++i) {
+        const int64_t segs = ((int64_t)cu[i + 1] - cu[i] + p.seg_tokens - 1) / p.seg_tokens;
+        first += segs > 1 ? segs - 1 : segs;
+        second += segs > 1 ? segs - 1 : 0;
+        longest = std::max(longest, segs);
+    }
+    hipError_t e = launch_chunk_dt(p, first, false, s);
+    if (e != hipSuccess || second == 0)
+        return e;
+    if (longest > 2) {
+        const int vecs = p.hc.dk * p.hc.dv / 4;
+        scan_kernel<<<(unsigned)((int64_t)p.N * p.hc.Hv * ((vecs + 255) / 256)), 256, 0, s>>>(p, vecs);
+        e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return launch_chunk_dt(p, second, true, s);
+}
 
 }  // namespace gdn

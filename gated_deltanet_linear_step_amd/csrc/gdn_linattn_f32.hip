@@ -1,0 +1,12 @@
+// gdn_linattn_f32.hip -- the chunked decayed linear attention for f32 activations.
+
+#include "gdn_linattn_chunk.h"
+
+namespace gdn {
+
+hipError_t launch_linattn_chunk_f32(const LinattnParams &p, int blocks, bool second, hipStream_t s)
+{
+    return linattn::launch_chunk_for<DT_F32>(p, blocks, second, s);
+}
+
+}  // namespace gdn
