@@ -556,6 +556,13 @@ gdn_status gdn_linattn_prefill_chunked(const gdn_dims *dims, int32_t num_seqs,
         return GDN_ERR_NULL;
     if (num_seqs == 0)
         return total_tokens == 0 ? GDN_OK : GDN_ERR_SHAPE;
+    // the chunk kernels address the 64 rows of a chunk with 32-bit byte offsets
+    constexpr int64_t kMaxStride = (int64_t)1 << 24;
+    if (in->q_stride >= kMaxStride || in->k_stride >= kMaxStride || in->v_stride >= kMaxStride ||
+        (int64_t)dims->num_v_heads * dims->head_dim_v >= kMaxStride)
+        return GDN_ERR_OVERFLOW;
+    if (total_tokens > 0 && !aligned(out, 16))
+        return GDN_ERR_ALIGN;
     int64_t chunks = 0, longest = 0;
     st = check_cu(cu_seqlens_host, num_seqs, total_tokens, 1, &chunks, &longest);
     if (st != GDN_OK)

@@ -155,9 +155,9 @@ size_t linattn_prefill_workspace_bytes(int Hk, int Hv, int dk, int dv, int N, in
 // cu: the offsets on the host
 hipError_t launch_linattn_prefill(const LinattnParams &p, const int32_t *cu, hipStream_t s);
 // The chunk kernels per activation dtype (gdn_linattn_chunk.h): `second` the later segments
-hipError_t launch_linattn_chunk_bf16(const LinattnParams &p, int blocks, bool second, hipStream_t s);
-hipError_t launch_linattn_chunk_f16(const LinattnParams &p, int blocks, bool second, hipStream_t s);
-hipError_t launch_linattn_chunk_f32(const LinattnParams &p, int blocks, bool second, hipStream_t s);
+hipError_t launch_linattn_chunk_bf16(const LinattnParams &p, int64_t segments, bool second, hipStream_t s);
+hipError_t launch_linattn_chunk_f16(const LinattnParams &p, int64_t segments, bool second, hipStream_t s);
+hipError_t launch_linattn_chunk_f32(const LinattnParams &p, int64_t segments, bool second, hipStream_t s);
 
 // RMS norm with residual and 8-bit output (gdn_norm.hip). Strides in elements.
 struct NormParams {

@@ -222,9 +222,11 @@ hipError_t launch_linattn_decode(const LinattnParams &p, hipStream_t s) { return
 namespace {
 
 // Segments are a multiple of 64 tokens (whole chunks of 64 or 32), at least kMinSegment,
-// and long enough that a call's segments number about kSegments over all heads: two
-// workgroups for each of the 256 CUs.
-constexpr int kMinSegment = 256, kSegments = 512;
+// and long enough that a call's segments number about kSegments over all heads. Two
+// workgroups run on each of the 256 CUs; twice as many segments even out sequences of
+// different lengths (30208 tokens of 8 sequences, 32 heads: 485 us with 1024 segments,
+// 553 with 512, 508 with 2048; the more segments, the more states are formed twice).
+constexpr int kMinSegment = 256, kSegments = 1024;
 
 int segment_tokens(int Hv, int64_t total)
 {
@@ -267,11 +269,10 @@ __global__ __launch_bounds__(256) void scan_kernel(const LinattnParams p, int ve
 
 hipError_t launch_chunk_dt(const LinattnParams &p, int64_t segments, bool second, hipStream_t s)
 {
-    const int blocks = (int)(segments * p.hc.Hv);
     switch (p.in.qkv_dt) {
-    case DT_F32: return launch_linattn_chunk_f32(p, blocks, second, s);
-    case DT_F16: return launch_linattn_chunk_f16(p, blocks, second, s);
-    default: return launch_linattn_chunk_bf16(p, blocks, second, s);
+    case DT_F32: return launch_linattn_chunk_f32(p, segments, second, s);
+    case DT_F16: return launch_linattn_chunk_f16(p, segments, second, s);
+    default: return launch_linattn_chunk_bf16(p, segments, second, s);
     }
 }
 

@@ -30,11 +30,12 @@
 //    lie, an operand over dk whose slot 8 lg + e is index 4 lg + e (e < 4) or
 //    16 + 4 lg + e - 4, and Q is read in that order: S never leaves its registers.
 //  * K^T and V^T operands are transposing LDS reads (ds_read_b64_tr_b16) of the
-//    row-major K and V tiles.
+//    row-major K and V tiles; P's columns and the weights are stored in their token order.
 //  * P is formed transposed, D[j][t], so that a lane holds four consecutive j of one
-//    t and stores them as one LDS word pair; it is shared through LDS because the
-//    waves split dv.
-//  * O is formed as D[dv][t]: a lane stores four consecutive dv.
+//    t and stores them in pairs; it is shared through LDS because the waves split dv.
+//  * O is formed as D[dv][t]. A wave's NT tiles take its dv rows in groups of four in
+//    turn (row 4 g + i of tile v is row 4 NT g + 4 v + i of the wave's), so that a lane
+//    holds 4 NT consecutive dv of one t.
 // LDS pitches are an odd number of 16-byte blocks: 16 rows of a column, or 16
 // 32-byte row pieces of a transposing read, fall into different banks.
 #pragma once
@@ -53,12 +54,12 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 // bf16 parts of an input of dtype QT
 constexpr int input_parts(int qt) { return qt == DT_BF16 ? 1 : qt == DT_F16 ? 2 : 3; }
 
+// A workgroup covers DV of a head's dv rows (all of them up to 128; two workgroups share
+// a head of 256), NT tiles of 16 to a wave.
 template <int DK, int DV, int QT>
 struct Geo {
     static constexpr int IP = input_parts(QT);
-    // dv tiles per wave and waves: 32 dv rows a wave halve the LDS reads of K^T, Q and
-    // P against 16; at dk = 256 the 16-row state alone takes the registers of it
-    static constexpr int NT = (DV >= 128 && !(DK == 256 && DV == 128)) ? 2 : 1;
+    static constexpr int NT = DV == 128 && DK <= 128 ? 2 : 1;
     static constexpr int W = DV / (16 * NT);
     static constexpr int THREADS = 64 * W;
     static constexpr int PK = DK * 2 + 16, PV = DV * 2 + 16;  // row pitches, bytes
@@ -67,7 +68,10 @@ struct Geo {
         return IP * c * (2 * PK + PV) + 3 * c * (2 * c + 16) + 16 * c;
     }
     static constexpr int C = lds(64) <= 160 * 1024 ? 64 : 32;
+    // waves per SIMD that the registers leave room for
+    static constexpr int WAVES = QT == DT_BF16 ? 2 : 1;
 };
+constexpr int rows_per_workgroup(int dv) { return dv > 128 ? 128 : dv; }
 
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c)
 {
@@ -75,13 +79,18 @@ __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c)
 }
 
 // Cuts the leading bf16 off x: returns its bits (upper half of a word) and leaves the
-// rest in x. Nothing is left of an infinity, so that its parts add up to it.
+// rest in x (NaN of an infinity).
 __device__ __forceinline__ uint32_t cut(float &x)
 {
     const uint32_t h = __float_as_uint(x) & 0xffff0000u;
-    const float rest = x - __uint_as_float(h);
-    x = __builtin_isinf(x) ? 0.f : rest;
+    x -= __uint_as_float(h);
     return h;
+}
+
+// The upper halves of two words as one: lo's below hi's.
+__device__ __forceinline__ uint32_t pack_hi(uint32_t lo, uint32_t hi)
+{
+    return __builtin_amdgcn_perm(hi, lo, 0x07060302u);
 }
 
 // Eight values as PARTS operands of eight bf16.
@@ -97,8 +106,12 @@ __device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&out)[PARTS]
         uint32_t w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const uint32_t lo = cut(r[2 * e]), hi = cut(r[2 * e + 1]);
-            w[e] = (lo >> 16) | hi;
+            if (s == PARTS - 1) {
+                w[e] = pack_hi(__float_as_uint(r[2 * e]), __float_as_uint(r[2 * e + 1]));
+            } else {
+                const uint32_t lo = cut(r[2 * e]), hi = cut(r[2 * e + 1]);
+                w[e] = pack_hi(lo, hi);
+            }
         }
         __builtin_memcpy(&out[s], w, 16);
     }
@@ -120,21 +133,22 @@ struct Raw8 {
     uint32_t w[QT == DT_F32 ? 8 : 4];
 };
 
-// Activations are aligned to 4 elements (the host checks): 8 bytes of 16-bit ones.
-template <int QT>
-__device__ __forceinline__ Raw8<QT> load_raw8(const void *p, int64_t idx)
+// A buffer of `bytes` from a scalar base: one 32-bit lane offset addresses it, loads past its end give 0 and
+// stores there are dropped.
+typedef __amdgpu_buffer_rsrc_t Buffer;
+__device__ __forceinline__ Buffer buffer_of(const void *base, uint32_t bytes)
 {
-    struct __attribute__((packed, aligned(8))) Words {
-        uint32_t w[4];
-    };
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, bytes, 0x00020000);
+}
+
+template <int QT>
+__device__ __forceinline__ Raw8<QT> load_raw8(Buffer b, uint32_t off)
+{
     Raw8<QT> r;
-    const char *b = static_cast<const char *>(p) + idx * (QT == DT_F32 ? 4 : 2);
 #pragma unroll
     for (int i = 0; i < (QT == DT_F32 ? 2 : 1); ++i) {
-        const Words v = *reinterpret_cast<const Words *>(b + 16 * i);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            r.w[4 * i + e] = v.w[e];
+        const auto v = __builtin_amdgcn_raw_buffer_load_b128(b, off + 16 * i, 0, 0);
+        __builtin_memcpy(r.w + 4 * i, &v, 16);
     }
     return r;
 }
@@ -154,38 +168,74 @@ __device__ __forceinline__ void raw8_parts(const Raw8<QT> &r, bf16x8 (&out)[inpu
     }
 }
 
-// A tile of C rows of D elements on its way from global memory to the LDS parts.
+// A tile of C rows of D elements on its way from global memory to the LDS parts. A
+// thread's units (8 elements) are STEP rows apart.
 template <int QT, int C, int D, int THREADS>
 struct Tile {
-    static constexpr int U = C * D / 8, N = (U + THREADS - 1) / THREADS, PITCH = D * 2 + 16;
+    static constexpr int U = C * D / 8, N = U / THREADS, STEP = THREADS * 8 / D, PITCH = D * 2 + 16;
+    static constexpr int ES = QT == DT_F32 ? 4 : 2;
+    static_assert(U % THREADS == 0 && THREADS * 8 % D == 0, "units split evenly over the threads, whole rows apart");
     Raw8<QT> r[N];
 
-    // rows [0, n) of the tile at element base `at`; the others are zero
-    __device__ __forceinline__ void load(const void *p, int64_t at, int64_t stride, int n)
+    // rows [0, n) of the tile at `base`, rows `stride` bytes apart (below 2^26: the host checks, so that a
+    // tile's offsets fit 32 bits); those past them are 0
+    __device__ __forceinline__ void load(const char *base, uint32_t stride, int n, int tid)
     {
+        const Buffer b = buffer_of(base, (uint32_t)(min(n, C) - 1) * stride + D * ES);
+        const uint32_t off = tid / (D / 8) * stride + tid % (D / 8) * 8 * ES;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int u = i * THREADS + threadIdx.x, row = u / (D / 8), c = u % (D / 8) * 8;
-            r[i] = Raw8<QT>{};
-            if ((U % THREADS == 0 || u < U) && row < n)
-                r[i] = load_raw8<QT>(p, at + row * stride + c);
-        }
+        for (int i = 0; i < N; ++i)
+            r[i] = load_raw8<QT>(b, off + i * STEP * stride);
     }
-    __device__ __forceinline__ void store(unsigned char *lds) const
+    __device__ __forceinline__ void store(unsigned char *lds, int tid) const
     {
+        const int row = tid / (D / 8), c = tid % (D / 8) * 8;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int u = i * THREADS + threadIdx.x, row = u / (D / 8), c = u % (D / 8) * 8;
-            if (U % THREADS == 0 || u < U) {
-                bf16x8 part[input_parts(QT)];
-                raw8_parts<QT>(r[i], part);
+            bf16x8 part[input_parts(QT)];
+            raw8_parts<QT>(r[i], part);
 #pragma unroll
-                for (int s = 0; s < input_parts(QT); ++s)
-                    *reinterpret_cast<bf16x8 *>(lds + s * C * PITCH + row * PITCH + 2 * c) = part[s];
-            }
+            for (int s = 0; s < input_parts(QT); ++s)
+                *reinterpret_cast<bf16x8 *>(lds + s * C * PITCH + (row + i * STEP) * PITCH + 2 * c) = part[s];
         }
     }
 };
+
+// N consecutive outputs (4 or 8) at a byte offset, as 16- or 8-byte stores (the host checks the alignment).
+template <bool F32, int N>
+__device__ __forceinline__ void store_out(Buffer b, uint32_t off, int dt, const float (&x)[N])
+{
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    if constexpr (F32) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            u32x4 w;
+            __builtin_memcpy(&w, x + i, 16);
+            __builtin_amdgcn_raw_buffer_store_b128(w, b, off + 4 * i, 0, 0);
+        }
+    } else {
+        uint16_t y[N];
+        if (dt == DT_BF16) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                y[i] = __builtin_bit_cast(uint16_t, (__bf16)x[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                y[i] = __builtin_bit_cast(uint16_t, (_Float16)x[i]);
+        }
+        if constexpr (N == 8) {
+            u32x4 w;
+            __builtin_memcpy(&w, y, 16);
+            __builtin_amdgcn_raw_buffer_store_b128(w, b, off, 0, 0);
+        } else {
+            u32x2 w;
+            __builtin_memcpy(&w, y, 8);
+            __builtin_amdgcn_raw_buffer_store_b64(w, b, off, 0, 0);
+        }
+    }
+}
 
 __device__ __forceinline__ bf16x8 lds8(const unsigned char *p) { return *reinterpret_cast<const bf16x8 *>(p); }
 
@@ -198,13 +248,24 @@ __device__ __forceinline__ bf16x8 lds4x2(const unsigned char *p)
     return v;
 }
 
-// Transposed operand: column c0 + li of rows row0 + 8 lg .. + 7 of a row-major bf16 tile. A transposing
-// read hands lane i of 16 column i of the four rows whose 16 columns the lanes point at.
-__device__ __forceinline__ bf16x8 lds_tr8(unsigned char *tile, int pitch, int row0, int c0, int li, int lg)
+// Token j of a chunk as a k-value of an operand: the 32 tokens of a product go to its slots 8 lg + e so that
+// lane group lg's four rows of a transposing read (e < 4, and 16 on for e >= 4) are two apart and the groups
+// that the LDS serves together, 0 with 1 and 2 with 3, cover 8 even or 8 odd rows: rows one 16-byte block
+// past a multiple of all banks apart then fall into different banks (consecutive rows overlap by half).
+__device__ __forceinline__ int token_of(int lg, int e) { return 8 * (lg & 1) + (lg >> 1) + 2 * (e & 3) + 4 * (e & 4); }
+__device__ __forceinline__ int slot_of(int j)
 {
-    unsigned char *p = tile + (row0 + 8 * lg + (li >> 2)) * pitch + 2 * (c0 + 4 * (li & 3));
+    return (j & ~31) + 8 * (((j >> 3) & 1) + 2 * (j & 1)) + ((j >> 1) & 3) + ((j >> 2) & 4);
+}
+
+// Transposed operand of a row-major bf16 tile: rows row0 + token_of(lg, e) of column c0 + gap (li / 4) + li % 4.
+// A transposing read hands lane i of 16 column i of the four rows whose 16 columns, in groups of four, the lanes
+// point at.
+__device__ __forceinline__ bf16x8 lds_tr8(unsigned char *tile, int pitch, int row0, int c0, int gap, int li, int lg)
+{
+    unsigned char *p = tile + (row0 + token_of(lg, li >> 2)) * pitch + 2 * (c0 + gap * (li & 3));
     s16x4 w[2] = {__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p),
-                  __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * pitch))};
+                  __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 16 * pitch))};
     bf16x8 v;
     __builtin_memcpy(&v, w, 16);
     return v;
@@ -237,16 +298,17 @@ __device__ __forceinline__ Segment find_segment(const int32_t *cu, int N, int id
         }
         const uint64_t hit = __ballot(idx >= before + upto - cnt && idx < before + upto);
         if (hit) {
+            // scalar reads: what follows from the segment stays in scalar registers
             const int src = __builtin_ctzll(hit);
             Segment r;
             r.seq = s0 + src;
-            r.segs = __shfl(segs, src, 64);
-            r.seg = idx - before - __shfl(upto - cnt, src, 64) + (second ? 1 : 0);
-            r.start = __shfl(start, src, 64) + r.seg * tokens;
-            r.len = min(tokens, __shfl(len, src, 64) - r.seg * tokens);
+            r.segs = __builtin_amdgcn_readlane(segs, src);
+            r.seg = idx - before - __builtin_amdgcn_readlane(upto - cnt, src) + (second ? 1 : 0);
+            r.start = __builtin_amdgcn_readlane(start, src) + r.seg * tokens;
+            r.len = min(tokens, __builtin_amdgcn_readlane(len, src) - r.seg * tokens);
             return r;
         }
-        before += __shfl(upto, 63, 64);
+        before += __builtin_amdgcn_readlane(upto, 63);
     }
     return Segment{-1, 0, 0, 0, 0};
 }
@@ -266,11 +328,12 @@ struct Walk {
     struct __align__(16) Lds {
         unsigned char q[IP * C * PK], k[IP * C * PK], v[IP * C * PV], p[OP * C * PP];
         double g[C];        // prefix sums of the log decays
-        float eg[C], w[C];  // e^G_t and e^(G_last - G_t)
+        float eg[C], w[C];  // scale e^G_t and e^(G_last - G_t)
+        float decay;        // e^G_last
     };
 
-    // The chunk's decay rows, by one wave (C <= 64 lanes).
-    static __device__ __forceinline__ void decays(Lds &l, double g)
+    // Prefix sum of the lanes' log decays, in f64 (one wave; C <= 64 lanes).
+    static __device__ __forceinline__ double prefix(double g)
     {
         const int lane = threadIdx.x & 63;
         double s = g < kLowest ? kLowest : g;
@@ -279,23 +342,22 @@ struct Walk {
             const double o = __shfl_up(s, d, 64);
             s += lane >= d ? o : 0.0;
         }
-        const double last = __shfl(s, C - 1, 64);
-        if (lane < C) {
-            l.g[lane] = s;
-            l.eg[lane] = expf((float)s);
-            l.w[lane] = expf((float)(last - s));
-        }
+        return s;
     }
 
     // Walks the segment's chunks from the state at `in` (NULL: zero) and stores the state after them at
-    // `out_state`; OUT: with the tokens' outputs. Returns the segment's summed log decay.
+    // `out_state`; OUT: with the tokens' outputs. Returns the segment's summed log decay. in, out_state and
+    // dvh are those of the workgroup's DV rows, the first of which is row dvh of the head.
     template <bool OUT>
-    static __device__ __forceinline__ double run(Lds &l, const LinattnParams &p, const Segment sg, int h, const float *in,
-                                                 float *out_state)
+    static __device__ __forceinline__ double run(Lds &l, const LinattnParams &p, const Segment sg, int h, int dvh,
+                                                 const float *in, float *out_state)
     {
-        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, lg = lane >> 4;
+        int tid = threadIdx.x;
+        int lane = tid & 63, li = lane & 15, lg = lane >> 4;
+        const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         const int kh = k_head_of(p.hc.head_map, h, p.hc.Hk, p.hc.Hv);
         const int dv0 = wave * 16 * NT;
+        const int row0 = dv0 + 4 * NT * (li >> 2) + (li & 3);  // the lane's state row of tile 0; tile v's is 4 v on
         const bool head_decay = p.hc.flags & F_HEAD_DECAY;
         double rate = 0.0;
         if (head_decay) {
@@ -308,81 +370,139 @@ struct Walk {
         for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
             for (int v = 0; v < NT; ++v)
-                S[kt][v] = in ? *reinterpret_cast<const f32x4 *>(in + (int64_t)(dv0 + 16 * v + li) * DK + 16 * kt + 4 * lg)
+                S[kt][v] = in ? *reinterpret_cast<const f32x4 *>(in + (row0 + 4 * v) * DK + 16 * kt + 4 * lg)
                               : f32x4{0.f, 0.f, 0.f, 0.f};
 
+        // The next chunk's rows are fetched a tile at a time between the current one's products
         Tile<QT, C, DK, THREADS> tq, tk;
         Tile<QT, C, DV, THREADS> tv;
+        constexpr int ES = Tile<QT, C, DK, THREADS>::ES;
+        const uint32_t qs = (uint32_t)(p.in.q_stride * ES), ks_ = (uint32_t)(p.in.k_stride * ES), vs = (uint32_t)(p.in.v_stride * ES);
+        const char *qp = static_cast<const char *>(p.in.q) + (sg.start * p.in.q_stride + (int64_t)kh * DK) * ES;
+        const char *kp = static_cast<const char *>(p.in.k) + (sg.start * p.in.k_stride + (int64_t)kh * DK) * ES;
+        const char *vp = static_cast<const char *>(p.in.v) + (sg.start * p.in.v_stride + (int64_t)h * p.hc.dv + dvh) * ES;
         double tg = 0.0;
-        auto fetch = [&](int c0) {
-            const int n = sg.len - c0;
-            const int64_t row = (int64_t)sg.start + c0;
+        float te = 0.f, tw = 0.f;
+        auto fetch_q = [&](int c0) {
             if constexpr (OUT)
-                tq.load(p.in.q, row * p.in.q_stride + (int64_t)kh * DK, p.in.q_stride, n);
-            tk.load(p.in.k, row * p.in.k_stride + (int64_t)kh * DK, p.in.k_stride, n);
-            tv.load(p.in.v, row * p.in.v_stride + (int64_t)h * DV, p.in.v_stride, n);
-            if (wave == 0)
-                tg = lane < n && lane < C ? (head_decay ? rate : (double)p.in.g[(row + lane) * p.hc.Hv + h]) : 0.0;
+                tq.load(qp + (int64_t)c0 * qs, qs, sg.len - c0, tid);
+        };
+        auto fetch_k = [&](int c0) {
+            tk.load(kp + (int64_t)c0 * ks_, ks_, sg.len - c0, tid);
+            if (wave == W - 1)
+                tg = lane < sg.len - c0 && lane < C
+                         ? (head_decay ? rate : (double)p.in.g[((int64_t)sg.start + c0 + lane) * p.hc.Hv + h])
+                         : 0.0;
+        };
+        auto fetch_v = [&](int c0) { tv.load(vp + (int64_t)c0 * vs, vs, sg.len - c0, tid); };
+        // the last wave turns the fetched decays into the chunk's decay rows before the others need them
+        auto scan = [&](int c0) {
+            if (wave == W - 1) {
+                tg = prefix(tg);
+                const double last = __shfl(tg, C - 1, 64);
+                te = expf((float)tg);
+                tw = lane < sg.len - c0 ? expf((float)(last - tg)) : 0.f;
+            }
         };
         auto stage = [&] {
             if constexpr (OUT)
-                tq.store(l.q);
-            tk.store(l.k);
-            tv.store(l.v);
-            if (wave == 0)
-                decays(l, tg);
+                tq.store(l.q, tid);
+            tk.store(l.k, tid);
+            tv.store(l.v, tid);
+            if (wave == W - 1 && lane < C) {
+                l.g[lane] = tg;
+                l.eg[lane] = p.hc.scale * te;
+                l.w[slot_of(lane)] = tw;
+                if (lane == C - 1)
+                    l.decay = te;
+            }
         };
         if constexpr (OUT) {
-            // the P tiles right of the diagonal that the 32-wide products reach
-            for (int u = threadIdx.x; u < OP * (TT / 2) * 16 * 2; u += THREADS) {
-                const int s = u / (TT / 2 * 32), it = u / 32 % (TT / 2) * 2, row = u / 2 % 16, half = u % 2;
-                *reinterpret_cast<uint4 *>(l.p + s * C * PP + (16 * it + row) * PP + 2 * (16 * it + 16 + 8 * half)) =
-                    make_uint4(0, 0, 0, 0);
+            // the P tiles right of the diagonal that the 32-wide products reach: tokens 16 .. 31 of the
+            // product's, slots 8 lg + 4 .. + 7
+            for (int u = threadIdx.x; u < OP * (TT / 2) * 16 * 4; u += THREADS) {
+                const int s = u / (TT / 2 * 64), it = u / 64 % (TT / 2) * 2, row = u / 4 % 16, g = u % 4;
+                *reinterpret_cast<uint2 *>(l.p + s * C * PP + (16 * it + row) * PP + 2 * (16 * it + 8 * g + 4)) = make_uint2(0, 0);
             }
         }
-        fetch(0);
+        fetch_k(0);
+        fetch_q(0);
+        fetch_v(0);
+        scan(0);
         stage();
         __syncthreads();
 
         double total = 0.0;
         for (int c0 = 0; c0 < sg.len; c0 += C) {
-            if (c0 + C < sg.len)
-                fetch(c0 + C);
+            const bool more = c0 + C < sg.len;
+            // the lane's LDS and buffer offsets are formed anew in each chunk: kept across the loop, some forty
+            // of them push the tiles into scratch, whose reloads wait for the fetches in flight
+            asm volatile("" : "+v"(tid));
+            lane = tid & 63;
+            li = lane & 15;
+            lg = lane >> 4;
             f32x4 O[OUT ? TT : 1][NT];
             if constexpr (OUT) {
-                // P = tril(Q K^T) . e^(G_t - G_j), tiles on and below the diagonal dealt to the waves
-                for (int idx = wave; idx < TT * (TT + 1) / 2; idx += W) {
-                    int it = 0;
+                // P = tril(Q K^T) . e^(G_t - G_j): the tiles on and below the diagonal are dealt to the
+                // waves, and a wave's run side by side
+                constexpr int TILES = TT * (TT + 1) / 2, MINE = (TILES + W - 1) / W;
+                f32x4 a[MINE];
+                int it[MINE], jt[MINE];
+#pragma unroll
+                for (int m = 0; m < MINE; ++m) {
+                    const int idx = min(wave + m * W, TILES - 1);  // one too many repeats the last tile
+                    it[m] = 0;
 #pragma unroll
                     for (int i = 1; i < TT; ++i)
-                        it += idx >= i * (i + 1) / 2 ? 1 : 0;
-                    const int jt = idx - it * (it + 1) / 2;
-                    f32x4 a = {0.f, 0.f, 0.f, 0.f};
+                        it[m] += idx >= i * (i + 1) / 2 ? 1 : 0;
+                    jt[m] = idx - it[m] * (it[m] + 1) / 2;
+                    a[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+                }
 #pragma unroll
-                    for (int ks = 0; ks < KS; ++ks)
+                for (int ks = 0; ks < KS; ++ks) {
+#pragma unroll
+                    for (int m = 0; m < MINE; ++m)
 #pragma unroll
                         for (int x = 0; x < IP; ++x)
 #pragma unroll
                             for (int y = 0; y < IP; ++y)
                                 if (x + y <= LIM)
-                                    a = mfma(lds8(l.k + x * C * PK + (16 * jt + li) * PK + 64 * ks + 16 * lg),
-                                             lds8(l.q + y * C * PK + (16 * it + li) * PK + 64 * ks + 16 * lg), a);
-                    const int t = 16 * it + li;
+                                    a[m] = mfma(lds8(l.k + x * C * PK + (16 * jt[m] + li) * PK + 64 * ks + 16 * lg),
+                                                lds8(l.q + y * C * PK + (16 * it[m] + li) * PK + 64 * ks + 16 * lg), a[m]);
+                    if (ks % 2)
+                        __builtin_amdgcn_sched_barrier(0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int m = 0; m < MINE; ++m) {
+                    const int t = 16 * it[m] + li, j0 = 16 * jt[m] + 4 * lg;
                     const double gt = l.g[t];
                     float x[4];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const int j = 16 * jt + 4 * lg + r;
-                        x[r] = j <= t ? a[r] * __expf((float)(gt - l.g[j])) : 0.f;
+                        x[r] = a[m][r] * (p.hc.scale * __expf((float)(gt - l.g[j0 + r])));
+                        asm volatile("" : "+v"(x[r]));  // taken for every lane: no branch around each exponential
+                        x[r] = j0 + r <= t ? x[r] : 0.f;
                     }
+                    // tokens 4 lg .. + 3 of the tile: two pairs of neighbouring slots
+                    unsigned char *at = l.p + t * PP + 2 * slot_of(j0);
 #pragma unroll
                     for (int s = 0; s < OP; ++s) {
-                        const uint32_t b0 = cut(x[0]), b1 = cut(x[1]), b2 = cut(x[2]), b3 = cut(x[3]);
-                        *reinterpret_cast<uint2 *>(l.p + s * C * PP + t * PP + 2 * (16 * jt + 4 * lg)) =
-                            make_uint2((b0 >> 16) | b1, (b2 >> 16) | b3);
+                        uint32_t b0 = __float_as_uint(x[0]), b1 = __float_as_uint(x[1]);
+                        uint32_t b2 = __float_as_uint(x[2]), b3 = __float_as_uint(x[3]);
+                        if (s < OP - 1) {
+                            cut(x[0]);
+                            cut(x[1]);
+                            cut(x[2]);
+                            cut(x[3]);
+                        }
+                        *reinterpret_cast<uint32_t *>(at + s * C * PP) = pack_hi(b0, b2);
+                        *reinterpret_cast<uint32_t *>(at + s * C * PP + 32) = pack_hi(b1, b3);
                     }
                 }
-                // O = diag(e^G) Q S^T
+                if (more)
+                    fetch_k(c0 + C);
+                // O = scale diag(e^G) Q S^T
 #pragma unroll
                 for (int it = 0; it < TT; ++it)
 #pragma unroll
@@ -409,6 +529,7 @@ struct Walk {
                                     if (s + y <= LIM)
                                         O[it][v] = mfma(sp[v][s], q, O[it][v]);
                         }
+                    __builtin_amdgcn_sched_barrier(0);  // or every step's reads are issued first, into spills
                 }
 #pragma unroll
                 for (int it = 0; it < TT; ++it) {
@@ -417,6 +538,13 @@ struct Walk {
                     for (int v = 0; v < NT; ++v)
                         O[it][v] *= e;
                 }
+                if (more) {
+                    fetch_q(c0 + C);
+                    scan(c0 + C);
+                }
+                __syncthreads();  // P is whole
+            } else if (more) {
+                fetch_k(c0 + C);
             }
             // V^T operands: dv as the row, tokens as k
             bf16x8 vt[JS][NT][IP];
@@ -426,21 +554,22 @@ struct Walk {
                 for (int v = 0; v < NT; ++v)
 #pragma unroll
                     for (int x = 0; x < IP; ++x)
-                        vt[js][v][x] = lds_tr8(l.v + x * C * PV, PV, 32 * js, dv0 + 16 * v, li, lg);
+                        vt[js][v][x] = lds_tr8(l.v + x * C * PV, PV, 32 * js, dv0 + 4 * v, 4 * NT, li, lg);
             if constexpr (OUT) {
-                __syncthreads();  // P is whole
-                bool bad = false;  // a V that is not finite: 0 times it, right of the diagonal, is not 0
+                // a V that is not finite: 0 times it, right of the diagonal, is not 0
+                typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+                u16x2 top = {0, 0};
 #pragma unroll
                 for (int js = 0; js < JS; ++js)
 #pragma unroll
                     for (int v = 0; v < NT; ++v) {
-                        uint32_t w[4];
+                        u16x2 w[4];
                         __builtin_memcpy(w, &vt[js][v][0], 16);
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            bad |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
+                            top = __builtin_elementwise_max(top, w[e] & (uint16_t)0x7fff);
                     }
-                if (__ballot(bad) == 0) {
+                if (__ballot(top[0] >= 0x7f80 || top[1] >= 0x7f80) == 0) {
 #pragma unroll
                     for (int it = 0; it < TT; ++it)
 #pragma unroll
@@ -465,7 +594,7 @@ struct Walk {
 #pragma unroll
                                 for (int s = OP - 1; s >= 0; --s)
                                     pj += bf16_bits_to_f32(*reinterpret_cast<const uint16_t *>(
-                                        l.p + s * C * PP + (16 * it + li) * PP + 2 * j));
+                                        l.p + s * C * PP + (16 * it + li) * PP + 2 * slot_of(j)));
 #pragma unroll
                                 for (int v = 0; v < NT; ++v)
 #pragma unroll
@@ -474,27 +603,31 @@ struct Walk {
 #pragma unroll
                                         for (int y = IP - 1; y >= 0; --y)
                                             x += bf16_bits_to_f32(*reinterpret_cast<const uint16_t *>(
-                                                l.v + y * C * PV + j * PV + 2 * (dv0 + 16 * v + 4 * lg + r)));
+                                                l.v + y * C * PV + j * PV + 2 * (dv0 + 4 * NT * lg + 4 * v + r)));
                                         O[it][v][r] = fmaf(pj, x, O[it][v][r]);
                                     }
                             }
                 }
+                if (more)
+                    fetch_v(c0 + C);
+                constexpr int OES = F32OUT ? 4 : 2;
+                const uint32_t os = (uint32_t)(p.hc.Hv * p.hc.dv) * OES;
+                const Buffer ob = buffer_of(static_cast<char *>(p.out) +
+                                                (((int64_t)sg.start + c0) * p.hc.Hv + h) * p.hc.dv * OES,
+                                            (uint32_t)(min(sg.len - c0, C) - 1) * os + p.hc.dv * OES);
 #pragma unroll
                 for (int it = 0; it < TT; ++it) {
-                    const int t = c0 + 16 * it + li;
-                    if (t < sg.len) {
+                    float x[4 * NT];
 #pragma unroll
-                        for (int v = 0; v < NT; ++v) {
-                            const int64_t at = (((int64_t)sg.start + t) * p.hc.Hv + h) * DV + dv0 + 16 * v + 4 * lg;
-#pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                store_act(p.out, at + r, p.out_dt, p.hc.scale * O[it][v][r]);
-                        }
-                    }
+                    for (int e = 0; e < 4 * NT; ++e)
+                        x[e] = O[it][e / 4][e % 4];
+                    store_out<F32OUT>(ob, (16 * it + li) * os + (dvh + dv0 + 4 * NT * lg) * OES, p.out_dt, x);
                 }
+            } else if (more) {
+                fetch_v(c0 + C);
             }
             // S <- e^G_last S + K^T diag(w) V
-            const float dec = l.eg[C - 1];
+            const float dec = l.decay;
             total += l.g[C - 1];
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt)
@@ -517,18 +650,23 @@ struct Walk {
 #pragma unroll
                 for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-                    for (int x = 0; x < IP; ++x) {
-                        const bf16x8 k = lds_tr8(l.k + x * C * PK, PK, 32 * js, 16 * kt, li, lg);
+                    for (int y = 0; y < IP; ++y) {
+                        const bf16x8 k = lds_tr8(l.k + y * C * PK, PK, 32 * js, 16 * kt, 4, li, lg);
 #pragma unroll
                         for (int v = 0; v < NT; ++v)
 #pragma unroll
                             for (int s = 0; s < 3; ++s)
-                                if (s + x <= 2)
+                                if (s + y <= 2)
                                     S[kt][v] = mfma(k, vd[v][s], S[kt][v]);
                     }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if constexpr (!OUT) {
+                if (more)
+                    scan(c0 + C);
             }
             __syncthreads();  // every wave is done with the chunk's tiles
-            if (c0 + C < sg.len) {
+            if (more) {
                 stage();
                 __syncthreads();
             }
@@ -537,41 +675,43 @@ struct Walk {
         for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
             for (int v = 0; v < NT; ++v)
-                *reinterpret_cast<f32x4 *>(out_state + (int64_t)(dv0 + 16 * v + li) * DK + 16 * kt + 4 * lg) = S[kt][v];
+                *reinterpret_cast<f32x4 *>(out_state + (row0 + 4 * v) * DK + 16 * kt + 4 * lg) = S[kt][v];
         return total;
     }
 };
 
-// Blocks: segment-major, heads fastest.
+// Blocks: segment-major, then heads, then a head's parts of DV rows.
 template <int DK, int DV, int QT, bool F32OUT, bool SECOND>
-__global__ __launch_bounds__((Geo<DK, DV, QT>::THREADS), 1) void chunk_kernel(const LinattnParams p)
+__global__ __launch_bounds__((Geo<DK, DV, QT>::THREADS), (Geo<DK, DV, QT>::WAVES)) void chunk_kernel(const LinattnParams p)
 {
     using Wk = Walk<DK, DV, QT, F32OUT>;
     __shared__ typename Wk::Lds l;
-    const int h = blockIdx.x % p.hc.Hv;
-    const Segment sg = find_segment(p.cu, p.N, blockIdx.x / p.hc.Hv, p.seg_tokens, SECOND);
+    const int parts = p.hc.dv / DV, dvh = blockIdx.x % parts * DV;
+    const int h = blockIdx.x / parts % p.hc.Hv;
+    const Segment sg = find_segment(p.cu, p.N, blockIdx.x / parts / p.hc.Hv, p.seg_tokens, SECOND);
     if (sg.seq < 0)
         return;
-    const int64_t size = (int64_t)DK * DV;
-    float *state = p.state + ((int64_t)sg.seq * p.hc.Hv + h) * size;
+    const int64_t size = (int64_t)DK * p.hc.dv, skip = (int64_t)DK * dvh;
+    float *state = p.state + ((int64_t)sg.seq * p.hc.Hv + h) * size + skip;
     const bool last = sg.seg == sg.segs - 1;
     const int64_t slot = last && !sg.seg ? 0 : ((int64_t)first_slot(p.cu, sg.seq, p.seg_tokens) + sg.seg) * p.hc.Hv + h;
-    float *after = last ? state : p.seg_state + slot * size;
+    float *after = last ? state : p.seg_state + slot * size + skip;
     if constexpr (SECOND) {
-        Wk::template run<true>(l, p, sg, h, p.seg_state + (slot - p.hc.Hv) * size, after);
+        Wk::template run<true>(l, p, sg, h, dvh, p.seg_state + (slot - p.hc.Hv) * size + skip, after);
     } else if (sg.seg == 0) {
-        Wk::template run<true>(l, p, sg, h, state, after);
+        Wk::template run<true>(l, p, sg, h, dvh, state, after);
     } else {
-        const double g = Wk::template run<false>(l, p, sg, h, nullptr, after);
-        if (threadIdx.x == 0)
+        const double g = Wk::template run<false>(l, p, sg, h, dvh, nullptr, after);
+        if (threadIdx.x == 0 && dvh == 0)
             p.seg_decay[slot] = (float)g;
     }
 }
 
 template <int DK, int DV, int QT, bool F32OUT>
-hipError_t launch_chunk(const LinattnParams &p, int blocks, bool second, hipStream_t s)
+hipError_t launch_chunk(const LinattnParams &p, int64_t segments, bool second, hipStream_t s)
 {
     constexpr int threads = Geo<DK, DV, QT>::THREADS;
+    const unsigned blocks = (unsigned)(segments * p.hc.Hv * (p.hc.dv / DV));
     if (second)
         chunk_kernel<DK, DV, QT, F32OUT, true><<<blocks, threads, 0, s>>>(p);
     else
@@ -580,42 +720,22 @@ hipError_t launch_chunk(const LinattnParams &p, int blocks, bool second, hipStre
 }
 
 template <int QT>
-hipError_t launch_chunk_for(const LinattnParams &p, int blocks, bool second, hipStream_t s)
+hipError_t launch_chunk_for(const LinattnParams &p, int64_t segments, bool second, hipStream_t s)
 {
-#define GDN_CHUNK(DK, DV)                                                       \
-    if (p.hc.dk == DK && p.hc.dv == DV)                                         \
-        return p.out_dt == DT_F32 ? launch_chunk<DK, DV, QT, true>(p, blocks, second, s) \
-                                  : launch_chunk<DK, DV, QT, false>(p, blocks, second, s);
+    const int dk = p.hc.dk, dv = rows_per_workgroup(p.hc.dv);
+#define GDN_CHUNK(DK, DV)                                                             \
+    if (dk == DK && dv == DV)                                                         \
+        return p.out_dt == DT_F32 ? launch_chunk<DK, DV, QT, true>(p, segments, second, s) \
+                                  : launch_chunk<DK, DV, QT, false>(p, segments, second, s);
     GDN_CHUNK(32, 32)
     GDN_CHUNK(64, 64)
     GDN_CHUNK(96, 96)
     GDN_CHUNK(128, 128)
     GDN_CHUNK(64, 128)
     GDN_CHUNK(128, 64)
-    GDN_CHUNK(128, 256)
     GDN_CHUNK(256, 128)
-    GDN_CHUNK(256, 256)
 #undef GDN_CHUNK
     return hipErrorInvalidValue;
-}
-
-// Tokens per chunk of a head shape
-template <int QT>
-int chunk_tokens_for(int dk, int dv)
-{
-#define GDN_CHUNK(DK, DV)         \
-    if (dk == DK && dv == DV)     \
-        return Geo<DK, DV, QT>::C;
-    GDN_CHUNK(32, 32)
-    GDN_CHUNK(64, 64)
-    GDN_CHUNK(96, 96)
-    GDN_CHUNK(128, 128)
-    GDN_CHUNK(64, 128)
-    GDN_CHUNK(128, 64)
-    GDN_CHUNK(128, 256)
-    GDN_CHUNK(256, 128)
-#undef GDN_CHUNK
-    return Geo<256, 256, QT>::C;
 }
 
 }  // namespace linattn

@@ -4,9 +4,9 @@
 
 namespace gdn {
 
-hipError_t launch_linattn_chunk_f16(const LinattnParams &p, int blocks, bool second, hipStream_t s)
+hipError_t launch_linattn_chunk_f16(const LinattnParams &p, int64_t segments, bool second, hipStream_t s)
 {
-    return linattn::launch_chunk_for<DT_F16>(p, blocks, second, s);
+    return linattn::launch_chunk_for<DT_F16>(p, segments, second, s);
 }
 
 }  // namespace gdn

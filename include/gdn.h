@@ -338,7 +338,9 @@ size_t gdn_linattn_prefill_workspace_bytes(const gdn_dims *dims, int32_t num_seq
                                            int32_t total_tokens);
 
 /* gdn_linattn_prefill_chunked -- the same over packed variable-length sequences;
- * arguments and errors as gdn_prefill_chunked's. An empty sequence keeps its state.
+ * arguments and errors as gdn_prefill_chunked's, and: OVERFLOW for a row stride (of q, k
+ * or v, or Hv*dv) of 2^24 elements or more, ALIGN for an out not aligned to 16 bytes. An
+ * empty sequence keeps its state.
  * The workspace is scratch: calls that may overlap in time (other streams, two
  * captured graphs) need one each. */
 gdn_status gdn_linattn_prefill_chunked(const gdn_dims *dims, int32_t num_seqs,

@@ -142,7 +142,7 @@ def prefill(d=None, inp=None, cu=(0, 100, 230), total=230, state=P, out_dtype=0,
     (SHAPE, dict(total=-1)), (NULL, dict(cu_dev=0)), (WORKSPACE, dict(ws=0)), (WORKSPACE, dict(nbytes=0)),
     (ALIGN, dict(ws=P + 128)), (UNSUPPORTED, dict(d=dims(flags=ops.STREAM_STATE))), (NULL, dict(inp=inputs(v=None))),
     (OVERFLOW, dict(d=dims(Hk=2, Hv=2048), cu=(0, 2 ** 21), total=2 ** 21, inp=inputs(v_stride=2048 * 128))),
-    (OK, dict(cu=(0, 0, 0), total=0)), (OK, dict(cu=(0,), total=0)), (SHAPE, dict(cu=(0,), total=3)),
+    (OVERFLOW, dict(inp=inputs(q_stride=2 ** 24))), (ALIGN, dict(out=P + 8)), (OK, dict(cu=(0, 0, 0), total=0)), (OK, dict(cu=(0,), total=0)), (SHAPE, dict(cu=(0,), total=3)),
     (OK, dict(cu=(0, 0), total=0, inp=inputs(q=None, k=None, v=None, g=None), out=0, ws=0)),
 ])
 def test_prefill_refusals(want, kw):
