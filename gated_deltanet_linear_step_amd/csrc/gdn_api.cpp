@@ -643,7 +643,9 @@ gdn_status gdn_quant_matmul(int32_t M, int32_t N, int32_t K, const int8_t *a, in
     if (!dtype_ok(out_dtype) || K % 16 != 0)
         return GDN_ERR_UNSUPPORTED;
     // |a w| <= 2^14, so K products stay below 2^31; the grid's tiles are at least 16 x 16
-    if (K > 131056 || (((int64_t)M + 15) / 16) * (((int64_t)N + 15) / 16) > kI32Max)
+    // and rows are addressed with 32-bit byte offsets within a tile of 256
+    if (K > 131056 || (((int64_t)M + 15) / 16) * (((int64_t)N + 15) / 16) > kI32Max ||
+        a_stride >= (int64_t)1 << 23 || w_stride >= (int64_t)1 << 23)
         return GDN_ERR_OVERFLOW;
     if (M == 0 || N == 0)
         return GDN_OK;

@@ -411,7 +411,8 @@ gdn_status gdn_add_rms_norm(const gdn_norm_args *args, void *stream);
  *                (else OVERFLOW: the sum could leave 32 bits)
  *   a            [M] int8 rows of a_stride bytes (>= K)
  *   w            [N] int8 rows of w_stride bytes (>= K): a torch Linear's weight layout
- *                a, w and both strides are multiples of 16 bytes
+ *                a, w and both strides are multiples of 16 bytes, strides below 2^23
+ *                (else OVERFLOW)
  *   a_scale      [M] f32; w_scale [N] f32; 4-byte aligned
  *   out          [M] rows of out_stride elements (>= N) of out_dtype, aligned to the element
  * Errors: NULL, SHAPE, UNSUPPORTED, OVERFLOW, ALIGN, LAUNCH.
