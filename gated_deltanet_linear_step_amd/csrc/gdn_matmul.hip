@@ -9,8 +9,13 @@
 //
 // Two kernels:
 //  * tile_kernel -- M above kSkinnyRows: BM x BN outputs a workgroup through LDS,
-//    128 bytes of k at a time, double buffered.
-//  * skinny_kernel -- a few rows: bound by the weights, which stream through once.
+//    128 bytes of k (a stage) at a time, double buffered, with two or three more stages on
+//    their way in registers. Bound by the LDS: a stage of 256 x 256 moves 192 KB out of
+//    it and 64 KB in for 2048 clocks of products. 4096^3: 66 us, 2071 TOPS (a library's
+//    int8 product reaches 2078 at 8192^3); 8192 x 8192 x 2048: 154 us, where storing the
+//    128 MB of bf16 outputs adds about 20 us that no product covers.
+//  * skinny_kernel -- a few rows: bound by the weights, which stream through once
+//    (1 x 8192 x 2048: 4.9 us).
 
 #include "gdn_device.h"
 #include "gdn_kernels.h"
@@ -72,7 +77,7 @@ constexpr int BK = 128;  // bytes of k per stage: an LDS row, 8 blocks of 16
 __device__ __forceinline__ int stage_at(int row, int block) { return row * BK + 16 * (block ^ (row & 7)); }
 
 // WGM x WGN waves, each (BM / WGM) x (BN / WGN) outputs as 32 x 32 tiles.
-template <int BM, int BN, int WGM, int WGN, int WAVES>
+template <int BM, int BN, int WGM, int WGN, int WAVES, int D>
 __global__ __launch_bounds__(64 * WGM * WGN, WAVES) void tile_kernel(const MatmulParams p)
 {
     constexpr int THREADS = 64 * WGM * WGN, TM = BM / WGM / 32, TN = BN / WGN / 32;
@@ -99,55 +104,93 @@ __global__ __launch_bounds__(64 * WGM * WGN, WAVES) void tile_kernel(const Matmu
     const uint32_t a_bytes = (uint32_t)(min(p.M - m0, BM) - 1) * as + p.K;
     const uint32_t w_bytes = (uint32_t)(min(p.N - n0, BN) - 1) * ws + p.K;
     const int row = tid / 8, block = tid % 8;
-    i32x4 ra[UA], rw[UW];
-    auto fetch = [&](int k0) {
-        const Buffer ba = buffer_of(ab + k0, a_bytes - k0), bw = buffer_of(wb + k0, w_bytes - k0);
+    // Loads and writes of one stage, in BK / 32 parts that go between the products of a stage: the L1 delivers 64
+    // bytes a clock, so that a wave issuing a whole stage's loads at once stands still until most have left.
+    constexpr int U = UA + UW, KS = BK / 32, PART = (U + KS - 1) / KS;
+    i32x4 regs[D][U];
+    uint32_t off[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+        off[i] = i < UA ? (row + i * STEP) * as : (row + (i - UA) * STEP) * ws;
+    auto fetch = [&](int k0, i32x4 (&r)[U], int part) {
+        // behind the last stage nothing is read, but the loads stay, so that the loop has no branch and each
+        // wait counts exactly the loads issued since
+        const bool in = k0 < p.K;
+        const Buffer ba = buffer_of(ab + k0, in ? a_bytes - k0 : 0), bw = buffer_of(wb + k0, in ? w_bytes - k0 : 0);
         // past K an offset past every buffer's end: 0
         const uint32_t c = k0 + 16 * block < p.K ? 16 * block : 0xf0000000u;
 #pragma unroll
-        for (int i = 0; i < UA; ++i)
-            ra[i] = load16(ba, max((row + i * STEP) * as + c, c));
-#pragma unroll
-        for (int i = 0; i < UW; ++i)
-            rw[i] = load16(bw, max((row + i * STEP) * ws + c, c));
+        for (int i = part * PART; i < U && i < (part + 1) * PART; ++i)
+            r[i] = load16(i < UA ? ba : bw, max(off[i] + c, c));
     };
-    auto stage = [&](unsigned char *s) {
+    auto stage = [&](unsigned char *s, const i32x4 (&r)[U], int part) {
 #pragma unroll
-        for (int i = 0; i < UA; ++i)
-            *reinterpret_cast<i32x4 *>(s + stage_at(row + i * STEP, block)) = ra[i];
-#pragma unroll
-        for (int i = 0; i < UW; ++i)
-            *reinterpret_cast<i32x4 *>(s + BM * BK + stage_at(row + i * STEP, block)) = rw[i];
+        for (int i = part * PART; i < U && i < (part + 1) * PART; ++i)
+            *reinterpret_cast<i32x4 *>(s + (i < UA ? stage_at(row + i * STEP, block)
+                                                   : BM * BK + stage_at(row + (i - UA) * STEP, block))) = r[i];
     };
 
     i32x16 acc[TN][TM] = {};
-    fetch(0);
-    stage(lds);
-    __syncthreads();
-    for (int k0 = 0, buf = 0; k0 < p.K; k0 += BK, buf ^= 1) {
-        const bool more = k0 + BK < p.K;
-        if (more)
-            fetch(k0 + BK);
+    i32x4 f[2][TM + TN];
+    auto read = [&](const unsigned char *s, int ks, i32x4 (&f)[TM + TN]) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            f[i] = *reinterpret_cast<const i32x4 *>(s + stage_at(wm * TM * 32 + 32 * i + l32, 2 * ks + half));
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            f[TM + j] = *reinterpret_cast<const i32x4 *>(s + BM * BK + stage_at(wn * TN * 32 + 32 * j + l32, 2 * ks + half));
+    };
+    // One stage: each step's operands are read during the step before it
+    auto step = [&](int buf, int d, int k0, bool load, const i32x4 (&next)[U]) {
         const unsigned char *s = lds + buf * STAGE;
+        read(s, 0, f[0]);
 #pragma unroll
-        for (int ks = 0; ks < BK / 32; ++ks) {
-            i32x4 fa[TM], fw[TN];
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-                fa[i] = *reinterpret_cast<const i32x4 *>(s + stage_at(wm * TM * 32 + 32 * i + l32, 2 * ks + half));
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-                fw[j] = *reinterpret_cast<const i32x4 *>(s + BM * BK + stage_at(wn * TN * 32 + 32 * j + l32, 2 * ks + half));
+        for (int ks = 0; ks < KS; ++ks) {
+            if (ks + 1 < KS)
+                read(s, ks + 1, f[(ks + 1) & 1]);
+            if (load)
+                fetch(k0, regs[d], ks);
 #pragma unroll
             for (int j = 0; j < TN; ++j)
 #pragma unroll
                 for (int i = 0; i < TM; ++i)
-                    acc[j][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[j], fa[i], acc[j][i], 0, 0, 0);
+                    acc[j][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f[ks & 1][TM + j], f[ks & 1][i], acc[j][i], 0, 0, 0);
+            if (D > 1)
+                stage(lds + (buf ^ 1) * STAGE, next, ks);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        if (more)
-            stage(lds + (buf ^ 1) * STAGE);
+        if (D == 1) {
+#pragma unroll
+            for (int part = 0; part < KS; ++part)
+                stage(lds + (buf ^ 1) * STAGE, next, part);
+        }
         __syncthreads();
+    };
+    // D stages of k in registers on their way to the LDS, besides the two in it
+    const int stages = (p.K + BK - 1) / BK;
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+#pragma unroll
+        for (int part = 0; part < KS; ++part)
+            fetch(d * BK, regs[d], part);
+#pragma unroll
+    for (int part = 0; part < KS; ++part)
+        stage(lds, regs[0], part);
+    __syncthreads();
+    int buf = 0, k0 = D * BK;
+    for (int g = 0; g < stages / D; ++g) {
+#pragma unroll
+        for (int d = 0; d < D; ++d, k0 += BK) {
+            step(buf, d, k0, true, regs[(d + 1) % D]);
+            buf ^= 1;
+        }
     }
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d)
+        if (d < stages % D) {
+            step(buf, d, 0, false, regs[d + 1]);
+            buf ^= 1;
+        }
 
     // Epilogue, 32 rows of m at a time through the wave's own LDS: a lane holds n = 8 g + 4 half + e of row l32
     unsigned char *mine = lds + wave * 32 * EP;
@@ -190,17 +233,17 @@ __global__ __launch_bounds__(64 * WGM * WGN, WAVES) void tile_kernel(const Matmu
     }
 }
 
-template <int BM, int BN, int WGM, int WGN, int WAVES>
+template <int BM, int BN, int WGM, int WGN, int WAVES, int D>
 hipError_t launch_tiles(const MatmulParams &p, hipStream_t s)
 {
     const int64_t tiles = (int64_t)((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
-    tile_kernel<BM, BN, WGM, WGN, WAVES><<<(unsigned)tiles, 64 * WGM * WGN, 0, s>>>(p);
+    tile_kernel<BM, BN, WGM, WGN, WAVES, D><<<(unsigned)tiles, 64 * WGM * WGN, 0, s>>>(p);
     return hipGetLastError();
 }
 
 // ---- a few rows ---------------------------------------------------------------
 
-constexpr int kSkinnyRows = 64, kSkinnyWaves = 8;
+constexpr int kSkinnyRows = 32, kSkinnyWaves = 8;
 
 // 16 MT rows by 16 NT columns a workgroup; its waves take 256 bytes of k in turn, straight from global memory (a
 // weight is read by one lane, once), and add up their sums through LDS.
@@ -278,26 +321,37 @@ hipError_t launch_skinny(const MatmulParams &p, hipStream_t s)
     return hipGetLastError();
 }
 
-int64_t tiles_of(const MatmulParams &p, int bm, int bn)
+// Microseconds that a CU takes for a stage (BK bytes of k) of its tiles, as measured at K = 4096: `alone` for a
+// workgroup by itself, `each` for each of several that share or follow one another on the CU.
+double stage_cost(const MatmulParams &p, int bm, int bn, double alone, double each)
 {
-    return (int64_t)((p.M + bm - 1) / bm) * ((p.N + bn - 1) / bn);
+    const int64_t tiles = (int64_t)((p.M + bm - 1) / bm) * ((p.N + bn - 1) / bn), per_cu = (tiles + 255) / 256;
+    return per_cu <= 1 ? alone : (double)per_cu * each;
 }
 
 }  // namespace
 
 hipError_t launch_matmul(const MatmulParams &p, hipStream_t s)
 {
+    // M x 8192 x 2048, us (skinny, 64 x 64 tiles): M = 1 4.9 7.4, 16 5.4 7.2, 32 6.5 7.5, 48 7.7 7.5, 64 8.3 7.5
     if (p.M <= 16)
         return launch_skinny<1>(p, s);
-    if (p.M <= 32)
-        return launch_skinny<2>(p, s);
     if (p.M <= kSkinnyRows)
-        return launch_skinny<4>(p, s);
-    if (tiles_of(p, 256, 256) >= 200)
-        return launch_tiles<256, 256, 2, 4, 2>(p, s);
-    if (tiles_of(p, 128, 128) >= 300)
-        return launch_tiles<128, 128, 2, 2, 2>(p, s);
-    return launch_tiles<64, 128, 1, 4, 2>(p, s);
+        return launch_skinny<2>(p, s);
+    // A larger tile reads each operand from the LDS fewer times, but a stage of it takes a lone workgroup longer:
+    // the tile whose slowest CU is done first. M x N x K, us (256 x 256, 128 x 128, 64 x 128, 64 x 64):
+    //   1001 x 2050 x 4112  50  24  30  31      100 x 8192 x 2048  27  13  9.6  8.0
+    //   1001 x 2048 x 4096  47  21  17  20      2048 x 4096 x 2048 31  26  30   36
+    //   4096 x 4096 x 4096  66  81  99  122     300 x 12288 x 2048 29  22  17   19
+    const double a = stage_cost(p, 256, 256, 1.42, 1.42), b = stage_cost(p, 128, 128, 0.63, 0.66),
+                 c = stage_cost(p, 64, 128, 0.49, 0.41), d = stage_cost(p, 64, 64, 0.33, 0.28);
+    if (a <= b && a <= c && a <= d)
+        return launch_tiles<256, 256, 2, 4, 2, 2>(p, s);
+    if (b <= c && b <= d)
+        return launch_tiles<128, 128, 2, 2, 2, 2>(p, s);
+    if (c <= d)
+        return launch_tiles<64, 128, 1, 4, 2, 2>(p, s);
+    return launch_tiles<64, 64, 2, 2, 2, 3>(p, s);
 }
 
 }  // namespace gdn
