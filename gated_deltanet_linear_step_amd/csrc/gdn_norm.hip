@@ -6,15 +6,17 @@
 // HBM bound: each row is read once, and its outputs written once.
 //
 // row_kernel holds a row in the registers of one workgroup (one wave up to 512
-// elements, 16 waves up to 32768), 8 consecutive elements of it to a thread's vector.
+// elements, 16 waves up to 16384), 8 consecutive elements of it to a thread's vector.
 // A workgroup takes several rows, with the weights kept in registers -- read again
 // for every row they would be more L2 traffic than the 16-bit rows themselves -- and
 // the next row's loads in flight while the current one is reduced. Vectors need no
 // alignment beyond the element's (the hardware splits them), so odd widths and
 // strides take the same path; a width's last hidden % 8 elements go one to a thread.
-// loop_kernel takes wider rows in passes over memory.
+// loop_kernel takes wider rows (and those of less than 8) in passes over memory.
 // Sums and maxima are f32, in a fixed order: lanes, DPP tree, waves.
-// 8192 x 4096 bf16, residual in and out, 16- and 8-bit rows out: NORMPROMPT.
+// 8192 x 4096 bf16, residual in and out, 16- and 8-bit rows out: 57 us, 5.3 TB/s (a large
+// copy reaches 5.0). 1537 x 5003 f16: 9.1 us, 3.4 TB/s; 64 x 2048: 3.3 us, a launch and
+// one round trip to memory.
 
 #include "gdn_device.h"
 #include "gdn_kernels.h"
@@ -112,8 +114,10 @@ __device__ __forceinline__ void store_vec8(void *p, int64_t idx, int dt, const f
         store_vec8_t<DT_F16>(p, idx, x);
 }
 
-// V vectors of 8 to each of NT threads: rows of up to 8 V NT elements (and the tail).
-template <int DT, int V, int NT>
+// V vectors of 8 to each of NT threads: rows of 8 up to 8 V NT elements (and the tail). Loads are never
+// conditional -- a thread without a vector loads the last one, and counts it with weight 0 -- so that all of a
+// row's are in flight together.
+template <int DT, int V, int NT, bool RES>
 __global__ __launch_bounds__(NT) void row_kernel(const NormParams p)
 {
     constexpr int WAVES = NT / 64;
@@ -122,47 +126,52 @@ __global__ __launch_bounds__(NT) void row_kernel(const NormParams p)
     const int tid = threadIdx.x, wave = tid >> 6;
     const int whole = p.hidden / 8, tail = p.hidden % 8;
     const bool tails = tid < tail;
-    const int ti = whole * 8 + tid;  // this thread's element of the tail
-
-    float w[V][8], wt = tails ? p.weight[ti] : 0.f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int u = v * NT + tid;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            w[v][e] = u < whole ? p.weight[8 * u + e] : 0.f;
-    }
+    const int ti = whole * 8 + tid, tc = min(ti, p.hidden - 1);  // this thread's element of the tail
 
     Vec8<DT> x[V], r[V];
-    float xt = 0.f;
+    uint32_t xt, rt = 0;
     auto fetch = [&](int64_t row) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int u = v * NT + tid;
-            x[v] = r[v] = Vec8<DT>{};
-            if (u < whole) {
-                x[v] = load_vec8<DT>(p.x, row * p.x_stride + 8 * u);
-                if (p.residual)
-                    r[v] = load_vec8<DT>(p.residual, row * p.residual_stride + 8 * u);
-            }
+            const int64_t u = 8 * min(v * NT + tid, whole - 1);
+            x[v] = load_vec8<DT>(p.x, row * p.x_stride + u);
+            if constexpr (RES)
+                r[v] = load_vec8<DT>(p.residual, row * p.residual_stride + u);
         }
-        if (tails) {
-            xt = load_act_t<DT>(p.x, row * p.x_stride + ti);
-            if (p.residual)
-                xt += load_act_t<DT>(p.residual, row * p.residual_stride + ti);
-        }
+        xt = load_raw1<DT>(p.x, row * p.x_stride + tc);
+        if constexpr (RES)
+            rt = load_raw1<DT>(p.residual, row * p.residual_stride + tc);
     };
     fetch(blockIdx.x);
+    Vec8<DT_F32> w[V];
+    float wt = p.weight[tc];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        w[v] = load_vec8<DT_F32>(p.weight, 8 * min(v * NT + tid, whole - 1));
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            w[v].w[e] = v * NT + tid < whole ? w[v].w[e] : 0u;
+    }
+    wt = tails ? wt : 0.f;
+
     int par = 0;
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, par ^= 1) {
-        float h[V][8], ht = xt, ss = ht * ht;
+        float h[V][8], ht = raw1_to_f32<DT>(xt);
+        if constexpr (RES)
+            ht += raw1_to_f32<DT>(rt);
+        float ss = tails ? ht * ht : 0.f;
 #pragma unroll
-        for (int v = 0; v < V; ++v)
+        for (int v = 0; v < V; ++v) {
+            float sv = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                h[v][e] = p.residual ? element<DT>(x[v], e) + element<DT>(r[v], e) : element<DT>(x[v], e);
-                ss = fmaf(h[v][e], h[v][e], ss);
+                h[v][e] = element<DT>(x[v], e);
+                if constexpr (RES)
+                    h[v][e] += element<DT>(r[v], e);
+                sv = fmaf(h[v][e], h[v][e], sv);
             }
+            ss += v * NT + tid < whole ? sv : 0.f;
+        }
         if (row + gridDim.x < p.rows)
             fetch(row + gridDim.x);
         if (p.residual_out) {
@@ -191,7 +200,7 @@ __global__ __launch_bounds__(NT) void row_kernel(const NormParams p)
         for (int v = 0; v < V; ++v)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                h[v][e] = h[v][e] * rs * w[v][e];
+                h[v][e] = h[v][e] * rs * __uint_as_float(w[v].w[e]);
                 top = max(top, __float_as_uint(h[v][e]) & 0x7fffffffu);
             }
         ht = tails ? ht * rs * wt : 0.f;
@@ -298,7 +307,10 @@ hipError_t launch_rows_t(const NormParams &p, hipStream_t s)
 {
     // as many workgroups as the card holds at 2048 threads a CU; each takes every grid-th row
     const int grid = std::min(p.rows, 256 * (2048 / NT));
-    row_kernel<DT, V, NT><<<grid, NT, 0, s>>>(p);
+    if (p.residual)
+        row_kernel<DT, V, NT, true><<<grid, NT, 0, s>>>(p);
+    else
+        row_kernel<DT, V, NT, false><<<grid, NT, 0, s>>>(p);
     return hipGetLastError();
 }
 
@@ -313,18 +325,16 @@ hipError_t launch_rows(const NormParams &p, hipStream_t s)
         return launch_rows_t<DT, 2, 256>(p, s);
     if (p.hidden < 16 * 512 + 8)
         return launch_rows_t<DT, 2, 512>(p, s);
-    if (p.hidden < 16 * 1024 + 8)
-        return launch_rows_t<DT, 2, 1024>(p, s);
-    return launch_rows_t<DT, 4, 1024>(p, s);
+    return launch_rows_t<DT, 2, 1024>(p, s);
 }
 
-constexpr int kRowMost = 32 * 1024 + 8;
+constexpr int kRowMost = 16 * 1024 + 8;  // four vectors a thread would spill
 
 }  // namespace
 
 hipError_t launch_norm(const NormParams &p, hipStream_t s)
 {
-    if (p.hidden >= kRowMost) {
+    if (p.hidden < 8 || p.hidden >= kRowMost) {
         loop_kernel<<<p.rows, kLoopThreads, 0, s>>>(p);
         return hipGetLastError();
     }
