@@ -13,6 +13,8 @@
 //    group stores the output of the group's row r, so a wave's rows leave in one
 //    store instruction.
 //  * The next token's k, q, v and decay are loaded while the current one runs.
+// B=64, 32 heads of 128 x 128, one token: 48.7 us, 5.5 TB/s of state (a large copy reaches
+// 5.0, the last-level cache holds part of the states); one sequence of 48 heads: 3.7 us.
 
 #include "gdn_device.h"
 #include "gdn_kernels.h"
@@ -180,7 +182,15 @@ hipError_t launch_recur_t(const LinattnParams &p, hipStream_t s)
 template <int DK, int QT>
 hipError_t launch_recur_q(const LinattnParams &p, hipStream_t s)
 {
-    return p.hc.flags & F_STREAM_STATE ? launch_recur_t<DK, QT, 4, true>(p, s) : launch_recur_t<DK, QT, 4, false>(p, s);
+    // Rows per lane group. One token: 2 (B=64 x 32 heads of 128 x 128: 48.7 us, 50.3 with 4, 54.1 with 8; 8
+    // sequences 7.2, 7.5, 7.1). Several tokens: 4, which share each token's k, q and decay (B=64, T=8: 68 us, 76
+    // with 2), unless that leaves CUs idle: then 1 (B=1, T=8: 6.1 us, 7.4 with 4).
+    const bool nt = p.hc.flags & F_STREAM_STATE;
+    if (p.T == 1)
+        return nt ? launch_recur_t<DK, QT, 2, true>(p, s) : launch_recur_t<DK, QT, 2, false>(p, s);
+    if ((int64_t)p.N * p.hc.Hv * p.hc.dv < 256 * recur_rows(DK, 4))
+        return launch_recur_t<DK, QT, 1, false>(p, s);
+    return nt ? launch_recur_t<DK, QT, 4, true>(p, s) : launch_recur_t<DK, QT, 4, false>(p, s);
 }
 
 template <int DK>
