@@ -178,14 +178,23 @@ struct Tile {
     Raw8<QT> r[N];
 
     // rows [0, n) of the tile at `base`, rows `stride` bytes apart (below 2^26: the host checks, so that a
-    // tile's offsets fit 32 bits); those past them are 0
-    __device__ __forceinline__ void load(const char *base, uint32_t stride, int n, int tid)
+    // tile's offsets fit 32 bits); those past them are 0, and all of them where n <= 0
+    struct From {
+        Buffer b;
+        uint32_t off, step;
+    };
+    static __device__ __forceinline__ From from(const char *base, uint32_t stride, int n, int tid)
     {
-        const Buffer b = buffer_of(base, (uint32_t)(min(n, C) - 1) * stride + D * ES);
-        const uint32_t off = tid / (D / 8) * stride + tid % (D / 8) * 8 * ES;
+        return From{buffer_of(base, n > 0 ? (uint32_t)(min(n, C) - 1) * stride + D * ES : 0),
+                    tid / (D / 8) * stride + tid % (D / 8) * 8 * ES, STEP * stride};
+    }
+    // the units that fall to part `part` of `parts`
+    __device__ __forceinline__ void load(const From &f, int part = 0, int parts = 1)
+    {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            r[i] = load_raw8<QT>(b, off + i * STEP * stride);
+            if (i * parts / N == part)
+                r[i] = load_raw8<QT>(f.b, f.off + i * f.step);
     }
     __device__ __forceinline__ void store(unsigned char *lds, int tid) const
     {
@@ -327,9 +336,10 @@ struct Walk {
 
     struct __align__(16) Lds {
         unsigned char q[IP * C * PK], k[IP * C * PK], v[IP * C * PV], p[OP * C * PP];
-        double g[C];        // prefix sums of the log decays
+        float2 g[C];        // prefix sums of the log decays in base 2, as the sum of two f32
         float eg[C], w[C];  // scale e^G_t and e^(G_last - G_t)
         float decay;        // e^G_last
+        double last;        // G_last
     };
 
     // Prefix sum of the lanes' log decays, in f64 (one wave; C <= 64 lanes).
@@ -381,25 +391,22 @@ struct Walk {
         const char *qp = static_cast<const char *>(p.in.q) + (sg.start * p.in.q_stride + (int64_t)kh * DK) * ES;
         const char *kp = static_cast<const char *>(p.in.k) + (sg.start * p.in.k_stride + (int64_t)kh * DK) * ES;
         const char *vp = static_cast<const char *>(p.in.v) + (sg.start * p.in.v_stride + (int64_t)h * p.hc.dv + dvh) * ES;
-        double tg = 0.0;
-        float te = 0.f, tw = 0.f;
-        auto fetch_q = [&](int c0) {
-            if constexpr (OUT)
-                tq.load(qp + (int64_t)c0 * qs, qs, sg.len - c0, tid);
+        double tg = 0.0, last = 0.0;
+        float graw = 0.f, te = 0.f, tw = 0.f;
+        using TK = Tile<QT, C, DK, THREADS>;
+        using TV = Tile<QT, C, DV, THREADS>;
+        auto from_q = [&](int c0) { return TK::from(qp + (int64_t)c0 * qs, qs, sg.len - c0, tid); };
+        auto from_k = [&](int c0) { return TK::from(kp + (int64_t)c0 * ks_, ks_, sg.len - c0, tid); };
+        auto from_v = [&](int c0) { return TV::from(vp + (int64_t)c0 * vs, vs, sg.len - c0, tid); };
+        auto fetch_g = [&](int c0) {
+            if (wave == W - 1 && !head_decay)
+                graw = p.in.g[((int64_t)sg.start + c0 + min(lane, sg.len - c0 - 1)) * p.hc.Hv + h];
         };
-        auto fetch_k = [&](int c0) {
-            tk.load(kp + (int64_t)c0 * ks_, ks_, sg.len - c0, tid);
-            if (wave == W - 1)
-                tg = lane < sg.len - c0 && lane < C
-                         ? (head_decay ? rate : (double)p.in.g[((int64_t)sg.start + c0 + lane) * p.hc.Hv + h])
-                         : 0.0;
-        };
-        auto fetch_v = [&](int c0) { tv.load(vp + (int64_t)c0 * vs, vs, sg.len - c0, tid); };
         // the last wave turns the fetched decays into the chunk's decay rows before the others need them
         auto scan = [&](int c0) {
             if (wave == W - 1) {
-                tg = prefix(tg);
-                const double last = __shfl(tg, C - 1, 64);
+                tg = prefix(lane < sg.len - c0 && lane < C ? (head_decay ? rate : (double)graw) : 0.0);
+                last = __shfl(tg, C - 1, 64);
                 te = expf((float)tg);
                 tw = lane < sg.len - c0 ? expf((float)(last - tg)) : 0.f;
             }
@@ -410,11 +417,15 @@ struct Walk {
             tk.store(l.k, tid);
             tv.store(l.v, tid);
             if (wave == W - 1 && lane < C) {
-                l.g[lane] = tg;
+                constexpr double kLog2e = 1.4426950408889634;
+                const float hi = (float)(tg * kLog2e);
+                l.g[lane] = make_float2(hi, (float)(tg * kLog2e - hi));
                 l.eg[lane] = p.hc.scale * te;
                 l.w[slot_of(lane)] = tw;
-                if (lane == C - 1)
+                if (lane == C - 1) {
                     l.decay = te;
+                    l.last = last;
+                }
             }
         };
         if constexpr (OUT) {
@@ -425,9 +436,11 @@ struct Walk {
                 *reinterpret_cast<uint2 *>(l.p + s * C * PP + (16 * it + row) * PP + 2 * (16 * it + 8 * g + 4)) = make_uint2(0, 0);
             }
         }
-        fetch_k(0);
-        fetch_q(0);
-        fetch_v(0);
+        fetch_g(0);
+        tk.load(from_k(0));
+        if constexpr (OUT)
+            tq.load(from_q(0));
+        tv.load(from_v(0));
         scan(0);
         stage();
         __syncthreads();
@@ -443,44 +456,107 @@ struct Walk {
             lg = lane >> 4;
             f32x4 O[OUT ? TT : 1][NT];
             if constexpr (OUT) {
-                // P = tril(Q K^T) . e^(G_t - G_j): the tiles on and below the diagonal are dealt to the
-                // waves, and a wave's run side by side
+                // P = tril(Q K^T) . e^(G_t - G_j), the 16 x 16 tiles (it, jt) on and below the diagonal dealt to
+                // the waves, and O = scale diag(e^G) Q S^T
                 constexpr int TILES = TT * (TT + 1) / 2, MINE = (TILES + W - 1) / W;
+                constexpr bool MERGED = TT == 4 && W == 4;
                 f32x4 a[MINE];
                 int it[MINE], jt[MINE];
+                if constexpr (MERGED) {
+                    // Both in one loop over dk, on the same Q operands (Q and K in the state's slot order). Wave w
+                    // takes tiles (1, w), (2, w), (3, w); the two of these that wave 2 and 3 have above the diagonal
+                    // leave room for (0, 0) at wave 2 and for the decays at wave 3, whose one tile is (3, 3).
+                    it[0] = wave == 2 ? 0 : 1;
+                    it[1] = 2;
+                    it[2] = 3;
+                    jt[0] = wave == 2 ? 0 : wave;
+                    jt[1] = jt[2] = wave;
+                } else {
 #pragma unroll
-                for (int m = 0; m < MINE; ++m) {
-                    const int idx = min(wave + m * W, TILES - 1);  // one too many repeats the last tile
-                    it[m] = 0;
+                    for (int m = 0; m < MINE; ++m) {
+                        const int idx = min(wave + m * W, TILES - 1);  // one too many repeats the last tile
+                        it[m] = 0;
 #pragma unroll
-                    for (int i = 1; i < TT; ++i)
-                        it[m] += idx >= i * (i + 1) / 2 ? 1 : 0;
-                    jt[m] = idx - it[m] * (it[m] + 1) / 2;
-                    a[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+                        for (int i = 1; i < TT; ++i)
+                            it[m] += idx >= i * (i + 1) / 2 ? 1 : 0;
+                        jt[m] = idx - it[m] * (it[m] + 1) / 2;
+                    }
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) {
+#pragma unroll
+                        for (int m = 0; m < MINE; ++m)
+#pragma unroll
+                            for (int x = 0; x < IP; ++x)
+#pragma unroll
+                                for (int y = 0; y < IP; ++y)
+                                    if (x + y <= LIM)
+                                        a[m] = mfma(lds8(l.k + x * C * PK + (16 * jt[m] + li) * PK + 64 * ks + 16 * lg),
+                                                    lds8(l.q + y * C * PK + (16 * it[m] + li) * PK + 64 * ks + 16 * lg),
+                                                    ks + x + y == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : a[m]);
+                        if (ks % 2)
+                            __builtin_amdgcn_sched_barrier(0);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
+                // the next chunk's k and q rows are fetched between these products, its v rows between P's
+                if (more)
+                    fetch_g(c0 + C);
+                const typename TK::From fk = from_k(c0 + C), fq = from_q(c0 + C);
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
+                    tk.load(fk, ks, KS);
+                    tq.load(fq, ks, KS);
+                    bf16x8 sp[NT][OP];
 #pragma unroll
-                    for (int m = 0; m < MINE; ++m)
+                    for (int v = 0; v < NT; ++v) {
+                        const f32x4 s0 = S[2 * ks][v], s1 = S[2 * ks + 1][v];
+                        const float x[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]};
+                        split8<OP>(x, sp[v]);
+                    }
+                    bf16x8 q[TT][IP];
 #pragma unroll
-                        for (int x = 0; x < IP; ++x)
+                    for (int i = 0; i < TT; ++i)
+#pragma unroll
+                        for (int y = 0; y < IP; ++y)
+                            q[i][y] = lds4x2(l.q + y * C * PK + (16 * i + li) * PK + 64 * ks + 8 * lg);
+                    if constexpr (MERGED) {
+#pragma unroll
+                        for (int x = 0; x < IP; ++x) {
+                            const unsigned char *kp = l.k + x * C * PK + li * PK + 64 * ks + 8 * lg;
+                            const bf16x8 k0 = lds4x2(kp + 16 * jt[0] * PK), k1 = lds4x2(kp + 16 * jt[1] * PK);
 #pragma unroll
                             for (int y = 0; y < IP; ++y)
-                                if (x + y <= LIM)
-                                    a[m] = mfma(lds8(l.k + x * C * PK + (16 * jt[m] + li) * PK + 64 * ks + 16 * lg),
-                                                lds8(l.q + y * C * PK + (16 * it[m] + li) * PK + 64 * ks + 16 * lg), a[m]);
-                    if (ks % 2)
-                        __builtin_amdgcn_sched_barrier(0);
+                                if (x + y <= LIM) {
+                                    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+                                    a[0] = mfma(k0, wave == 2 ? q[0][y] : q[1][y], ks + x + y == 0 ? zero : a[0]);
+                                    a[1] = mfma(k1, q[2][y], ks + x + y == 0 ? zero : a[1]);
+                                    a[2] = mfma(k1, q[3][y], ks + x + y == 0 ? zero : a[2]);
+                                }
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < TT; ++i)
+#pragma unroll
+                        for (int y = 0; y < IP; ++y)
+#pragma unroll
+                            for (int v = 0; v < NT; ++v)
+#pragma unroll
+                                for (int s = 0; s < OP; ++s)
+                                    if (s + y <= LIM)
+                                        O[i][v] = mfma(sp[v][s], q[i][y], ks + y + s == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : O[i][v]);
+                    __builtin_amdgcn_sched_barrier(0);  // or every step's reads are issued first, into spills
                 }
-                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int m = 0; m < MINE; ++m) {
+                    if (MERGED && jt[m] > it[m])
+                        continue;
                     const int t = 16 * it[m] + li, j0 = 16 * jt[m] + 4 * lg;
-                    const double gt = l.g[t];
+                    const float2 gt = l.g[t];
                     float x[4];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        x[r] = a[m][r] * (p.hc.scale * __expf((float)(gt - l.g[j0 + r])));
+                        const float2 gj = l.g[j0 + r];
+                        x[r] = a[m][r] * (p.hc.scale * __builtin_amdgcn_exp2f((gt.x - gj.x) + (gt.y - gj.y)));
                         asm volatile("" : "+v"(x[r]));  // taken for every lane: no branch around each exponential
                         x[r] = j0 + r <= t ? x[r] : 0.f;
                     }
@@ -500,51 +576,20 @@ struct Walk {
                         *reinterpret_cast<uint32_t *>(at + s * C * PP + 32) = pack_hi(b1, b3);
                     }
                 }
+#pragma unroll
+                for (int i = 0; i < TT; ++i) {
+                    const float e = l.eg[16 * i + li];
+#pragma unroll
+                    for (int v = 0; v < NT; ++v)
+                        O[i][v] *= e;
+                }
                 if (more)
-                    fetch_k(c0 + C);
-                // O = scale diag(e^G) Q S^T
-#pragma unroll
-                for (int it = 0; it < TT; ++it)
-#pragma unroll
-                    for (int v = 0; v < NT; ++v)
-                        O[it][v] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    bf16x8 sp[NT][OP];
-#pragma unroll
-                    for (int v = 0; v < NT; ++v) {
-                        const f32x4 a = S[2 * ks][v], b = S[2 * ks + 1][v];
-                        const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-                        split8<OP>(x, sp[v]);
-                    }
-#pragma unroll
-                    for (int it = 0; it < TT; ++it)
-#pragma unroll
-                        for (int y = 0; y < IP; ++y) {
-                            const bf16x8 q = lds4x2(l.q + y * C * PK + (16 * it + li) * PK + 64 * ks + 8 * lg);
-#pragma unroll
-                            for (int v = 0; v < NT; ++v)
-#pragma unroll
-                                for (int s = 0; s < OP; ++s)
-                                    if (s + y <= LIM)
-                                        O[it][v] = mfma(sp[v][s], q, O[it][v]);
-                        }
-                    __builtin_amdgcn_sched_barrier(0);  // or every step's reads are issued first, into spills
-                }
-#pragma unroll
-                for (int it = 0; it < TT; ++it) {
-                    const float e = l.eg[16 * it + li];
-#pragma unroll
-                    for (int v = 0; v < NT; ++v)
-                        O[it][v] *= e;
-                }
-                if (more) {
-                    fetch_q(c0 + C);
                     scan(c0 + C);
-                }
                 __syncthreads();  // P is whole
             } else if (more) {
-                fetch_k(c0 + C);
+                fetch_g(c0 + C);
+                tk.load(from_k(c0 + C));
+                tv.load(from_v(c0 + C));
             }
             // V^T operands: dv as the row, tokens as k
             bf16x8 vt[JS][NT][IP];
@@ -556,6 +601,7 @@ struct Walk {
                     for (int x = 0; x < IP; ++x)
                         vt[js][v][x] = lds_tr8(l.v + x * C * PV, PV, 32 * js, dv0 + 4 * v, 4 * NT, li, lg);
             if constexpr (OUT) {
+                const typename TV::From fv = from_v(c0 + C);
                 // a V that is not finite: 0 times it, right of the diagonal, is not 0
                 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
                 u16x2 top = {0, 0};
@@ -570,6 +616,7 @@ struct Walk {
                             top = __builtin_elementwise_max(top, w[e] & (uint16_t)0x7fff);
                     }
                 if (__ballot(top[0] >= 0x7f80 || top[1] >= 0x7f80) == 0) {
+                    tv.load(fv);
 #pragma unroll
                     for (int it = 0; it < TT; ++it)
 #pragma unroll
@@ -585,6 +632,7 @@ struct Walk {
                                             O[it][v] = mfma(vt[js][v][x], pt, O[it][v]);
                             }
                 } else {
+                    tv.load(fv);
                     // term by term, the tokens up to t alone
                     for (int j = 0; j < C; ++j)
 #pragma unroll
@@ -608,8 +656,6 @@ struct Walk {
                                     }
                             }
                 }
-                if (more)
-                    fetch_v(c0 + C);
                 constexpr int OES = F32OUT ? 4 : 2;
                 const uint32_t os = (uint32_t)(p.hc.Hv * p.hc.dv) * OES;
                 const Buffer ob = buffer_of(static_cast<char *>(p.out) +
@@ -623,12 +669,10 @@ struct Walk {
                         x[e] = O[it][e / 4][e % 4];
                     store_out<F32OUT>(ob, (16 * it + li) * os + (dvh + dv0 + 4 * NT * lg) * OES, p.out_dt, x);
                 }
-            } else if (more) {
-                fetch_v(c0 + C);
             }
             // S <- e^G_last S + K^T diag(w) V
             const float dec = l.decay;
-            total += l.g[C - 1];
+            total += l.last;
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
