@@ -143,9 +143,11 @@ struct LinattnParams {
     int total;
     const int32_t *cu;
     void *workspace;
-    // prefill: sequences are split into segments of seg_tokens; states after (and
-    // summed log decays of) each segment but a sequence's last, [slot][Hv]
-    int seg_tokens;
+    // prefill: sequences longer than seg_tokens are split into segments, the first of
+    // seg_first_tokens, the others of seg_tokens; how many segments come first of a
+    // sequence, and between first and last; states after (and summed log decays of)
+    // each segment but a sequence's last, [slot][Hv]
+    int seg_tokens, seg_first_tokens, segs_first, segs_between;
     float *seg_state, *seg_decay;
 };
 bool linattn_supported(int dk, int dv);

@@ -18,6 +18,7 @@
 
 #include "gdn_device.h"
 #include "gdn_kernels.h"
+#include "gdn_linattn_chunk.h"
 
 #include <algorithm>
 
@@ -231,40 +232,88 @@ hipError_t launch_linattn_decode(const LinattnParams &p, hipStream_t s) { return
 
 namespace {
 
-// Segments are a multiple of 64 tokens (whole chunks of 64 or 32), at least kMinSegment,
-// and long enough that a call's segments number about kSegments over all heads. Two
-// workgroups run on each of the 256 CUs; twice as many segments even out sequences of
-// different lengths (30208 tokens of 8 sequences, 32 heads: 485 us with 1024 segments,
-// 553 with 512, 508 with 2048; the more segments, the more states are formed twice).
-constexpr int kMinSegment = 256, kSegments = 1024;
+using linattn::Cut;
 
-int segment_tokens(int Hv, int64_t total)
+// Segments are a multiple of 64 tokens (whole chunks of 64 or 32), at least kMinSegment, and not more in a call than
+// about kSegments over all heads (and a head's parts of 128 dv rows): every one but a sequence's last costs a pass
+// over its keys and values and its state written and read twice. Two workgroups run on each of the 256 CUs.
+constexpr int kMinSegment = 256, kSegments = 1024, kResident = 512;
+
+int parts_of(int dv) { return dv > 128 ? dv / 128 : 1; }
+
+int least_segment(int Hv, int dv, int64_t total)
 {
-    const int64_t per = (total * Hv + kSegments - 1) / kSegments;
+    const int64_t heads = (int64_t)Hv * parts_of(dv), per = (total * heads + kSegments - 1) / kSegments;
     return (int)std::max<int64_t>(kMinSegment, (per + 63) / 64 * 64);
 }
 
-// States between segments a call may need: total / segment_tokens of them per head, at
-// most total / kMinSegment and kSegments / Hv. Grows with total.
-int64_t segment_slots(int Hv, int64_t total)
+// States between segments a call may need, per head: a sequence of several segments is longer than one of them,
+// so it has at most len / L + 1/2 states. Grows with total.
+int64_t segment_slots(int Hv, int dv, int64_t total)
 {
-    return std::min<int64_t>(total / kMinSegment, kSegments / Hv + 1);
+    const int64_t most = std::min<int64_t>(total / kMinSegment, kSegments / ((int64_t)Hv * parts_of(dv)) + 1);
+    return most + (most + 1) / 2;
 }
 
-// Entering states: slot s of a sequence (state after its segment s, entered with zero
+struct Counts {
+    int64_t first, between, last;
+};
+Counts count_segments(const int32_t *cu, int N, Cut cut)
+{
+    Counts c{0, 0, 0};
+    for (int i = 0; i < N; ++i) {
+        const int segs = cut.segments(cu[i + 1] - cu[i]);
+        c.first += segs > 0;
+        c.between += segs > 2 ? segs - 2 : 0;
+        c.last += segs > 1;
+    }
+    return c;
+}
+
+// The segment length whose launches end first, as rounds of resident workgroups: a few lengths from the least one on
+// (a few only, and for few sequences: the host walks their offsets for each).
+Cut choose_cut(const int32_t *cu, int N, int Hv, int dv, int64_t total)
+{
+    const int least = least_segment(Hv, dv, total);
+    const int64_t heads = (int64_t)Hv * parts_of(dv);
+    Cut best{};
+    int64_t best_cost = 0;
+    for (int i = 0; i < (N <= 64 ? 8 : 1); ++i) {
+        const int L = least + 64 * i * ((least + 511) / 512);
+        const Cut cut{L, (L / 2 + 63) / 64 * 64};
+        const Counts c = count_segments(cu, N, cut);
+        auto rounds = [&](int64_t segs) { return (segs * heads + kResident - 1) / kResident; };
+        const int64_t cost = L * (rounds(c.first + c.between) + 2 * rounds(c.between + c.last));
+        if (i == 0 || cost < best_cost) {
+            best = cut;
+            best_cost = cost;
+        }
+    }
+    return best;
+}
+
+// Entering states: a sequence's slot s (state after its segment s, entered with zero
 // from s = 1 on) becomes the state after segment s. HBM bound, one float4 a thread; the
 // loads of later segments do not wait for the running sum.
 __global__ __launch_bounds__(256) void scan_kernel(const LinattnParams p, int vecs)
 {
     const int blocks = (vecs + 255) / 256;
     const int part = blockIdx.x % blocks, h = blockIdx.x / blocks % p.hc.Hv, seq = blockIdx.x / blocks / p.hc.Hv;
-    const int at = part * 256 + threadIdx.x;
-    const int first = p.cu[seq], len = p.cu[seq + 1] - first;
-    const int segs = (len + p.seg_tokens - 1) / p.seg_tokens;
-    if (segs < 3 || at >= vecs)
+    const int at = part * 256 + threadIdx.x, lane = threadIdx.x & 63;
+    const Cut cut{p.seg_tokens, p.seg_first_tokens};
+    const int segs = cut.segments(p.cu[seq + 1] - p.cu[seq]);
+    if (segs < 3)
+        return;
+    int slot0 = 0;  // the states of the sequences before this one
+    for (int s0 = 0; s0 < seq; s0 += 64) {
+        const int s = s0 + lane;
+        const int n = s < seq ? cut.segments(p.cu[s + 1] - p.cu[s]) : 0;
+        slot0 += __builtin_amdgcn_readlane(linattn::lane_sum(n > 1 ? n - 1 : 0), 63);
+    }
+    if (at >= vecs)
         return;
     const int64_t step = (int64_t)p.hc.Hv * vecs;
-    const int64_t slot = (int64_t)(first / p.seg_tokens) * p.hc.Hv + h;
+    const int64_t slot = (int64_t)slot0 * p.hc.Hv + h;
     float4 *x = reinterpret_cast<float4 *>(p.seg_state) + slot * vecs + at;
     const float *d = p.seg_decay + slot;
     float4 run = *x;
@@ -290,33 +339,31 @@ hipError_t launch_chunk_dt(const LinattnParams &p, int64_t segments, bool second
 
 size_t linattn_prefill_workspace_bytes(int, int Hv, int dk, int dv, int, int64_t total)
 {
-    return 256 + (size_t)segment_slots(Hv, total) * Hv * (4 * (size_t)dk * dv + 4);
+    return 256 + (size_t)segment_slots(Hv, dv, total) * Hv * (4 * (size_t)dk * dv + 4);
 }
 
 hipError_t launch_linattn_prefill(const LinattnParams &given, const int32_t *cu, hipStream_t s)
 {
     LinattnParams p = given;
-    p.seg_tokens = segment_tokens(p.hc.Hv, p.total);
+    const Cut cut = choose_cut(cu, p.N, p.hc.Hv, p.hc.dv, p.total);
+    const Counts c = count_segments(cu, p.N, cut);
+    p.seg_tokens = cut.L;
+    p.seg_first_tokens = cut.L0;
+    p.segs_first = (int)c.first;
+    p.segs_between = (int)c.between;
     p.seg_state = static_cast<float *>(p.workspace);
-    p.seg_decay = p.seg_state + segment_slots(p.hc.Hv, p.total) * p.hc.Hv * p.hc.dk * p.hc.dv;
-    int64_t first = 0, second = 0, longest = 0;
-    for (int i = 0; i < p.N; ++i) {
-        const int64_t segs = ((int64_t)cu[i + 1] - cu[i] + p.seg_tokens - 1) / p.seg_tokens;
-        first += segs > 1 ? segs - 1 : segs;
-        second += segs > 1 ? segs - 1 : 0;
-        longest = std::max(longest, segs);
-    }
-    hipError_t e = launch_chunk_dt(p, first, false, s);
-    if (e != hipSuccess || second == 0)
+    p.seg_decay = p.seg_state + segment_slots(p.hc.Hv, p.hc.dv, p.total) * p.hc.Hv * p.hc.dk * p.hc.dv;
+    hipError_t e = launch_chunk_dt(p, c.first + c.between, false, s);
+    if (e != hipSuccess || c.last == 0)
         return e;
-    if (longest > 2) {
+    if (c.between > 0) {
         const int vecs = p.hc.dk * p.hc.dv / 4;
         scan_kernel<<<(unsigned)((int64_t)p.N * p.hc.Hv * ((vecs + 255) / 256)), 256, 0, s>>>(p, vecs);
         e = hipGetLastError();
         if (e != hipSuccess)
             return e;
     }
-    return launch_chunk_dt(p, second, true, s);
+    return launch_chunk_dt(p, c.between + c.last, true, s);
 }
 
 }  // namespace gdn

@@ -10,8 +10,9 @@
 // sequence) of one v-head, the head's state in MFMA accumulators. Long sequences are
 // split into segments so that few rows still fill the card:
 //   1. chunk_kernel, first launch: every sequence's first segment, complete (from the
-//      given state); every later segment but the last, its contribution to the state
-//      alone, as if it entered with zero.
+//      given state, which the last segment overwrites in the second launch); every later
+//      segment but the last, its contribution to the state alone, as if it entered with
+//      zero.
 //   2. scan_kernel: entering states by a running sum over each sequence's segments.
 //   3. chunk_kernel, second launch: the later segments, complete.
 // A call whose sequences all have one segment is the first launch alone.
@@ -65,7 +66,7 @@ struct Geo {
     static constexpr int PK = DK * 2 + 16, PV = DV * 2 + 16;  // row pitches, bytes
     static constexpr int lds(int c)
     {
-        return IP * c * (2 * PK + PV) + 3 * c * (2 * c + 16) + 16 * c;
+        return IP * c * (2 * PK + PV) + 3 * c * (2 * c + 16) + 32 * c + 32;
     }
     static constexpr int C = lds(64) <= 160 * 1024 ? 64 : 32;
     // waves per SIMD that the registers leave room for
@@ -285,26 +286,47 @@ __device__ __forceinline__ bf16x8 lds_tr8(unsigned char *tile, int pitch, int ro
 // a small decay beside it.
 constexpr double kLowest = -1e4;
 
-// Segment `idx` of a launch: which sequence, which of its segments, its tokens. Every
-// lane scans 64 sequences' counts at once.
-struct Segment {
-    int seq, seg, segs, start, len;
+// How a sequence of `len` tokens is cut: one segment up to L tokens, else L0 tokens and then L at a time. (Only
+// the first segment is walked with its outputs in the first launch; that takes twice as long as the others' states.)
+struct Cut {
+    int L, L0;
+    __host__ __device__ int segments(int len) const { return len <= L ? (len > 0 ? 1 : 0) : 1 + (len - L0 + L - 1) / L; }
 };
-__device__ __forceinline__ Segment find_segment(const int32_t *cu, int N, int idx, int tokens, bool second)
+
+__device__ __forceinline__ float lane_value(float x, int lane)
+{
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), lane));
+}
+
+// Inclusive sum over the lanes of a wave.
+__device__ __forceinline__ int lane_sum(int x)
 {
     const int lane = threadIdx.x & 63;
-    int before = 0;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(x, d, 64);
+        x += lane >= d ? o : 0;
+    }
+    return x;
+}
+
+// Segments are dealt out longest first, by kind: every sequence's first, those between, the last of several.
+enum SegmentKind { kFirst, kBetween, kLast };
+struct Segment {
+    int seq, seg, segs, start, len;
+    int slot0;  // of the sequence's states after its segments but the last
+};
+// Segment `idx` of a kind. Every lane counts for one of 64 sequences at a time.
+__device__ __forceinline__ Segment find_segment(const int32_t *cu, int N, Cut cut, int kind, int idx)
+{
+    const int lane = threadIdx.x & 63;
+    int before = 0, slots_before = 0;
     for (int s0 = 0; s0 < N; s0 += 64) {
         const int s = s0 + lane;
         const int start = s < N ? cu[s] : 0, len = s < N ? cu[s + 1] - start : 0;
-        const int segs = (len + tokens - 1) / tokens;
-        const int cnt = second ? max(segs - 1, 0) : segs > 1 ? segs - 1 : segs;
-        int upto = cnt;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(upto, d, 64);
-            upto += lane >= d ? o : 0;
-        }
+        const int segs = cut.segments(len), slots = max(segs - 1, 0);
+        const int cnt = kind == kFirst ? min(segs, 1) : kind == kBetween ? max(segs - 2, 0) : min(slots, 1);
+        const int upto = lane_sum(cnt), slots_upto = lane_sum(slots);
         const uint64_t hit = __ballot(idx >= before + upto - cnt && idx < before + upto);
         if (hit) {
             // scalar reads: what follows from the segment stays in scalar registers
@@ -312,19 +334,19 @@ __device__ __forceinline__ Segment find_segment(const int32_t *cu, int N, int id
             Segment r;
             r.seq = s0 + src;
             r.segs = __builtin_amdgcn_readlane(segs, src);
-            r.seg = idx - before - __builtin_amdgcn_readlane(upto - cnt, src) + (second ? 1 : 0);
-            r.start = __builtin_amdgcn_readlane(start, src) + r.seg * tokens;
-            r.len = min(tokens, __builtin_amdgcn_readlane(len, src) - r.seg * tokens);
+            const int nth = idx - before - __builtin_amdgcn_readlane(upto - cnt, src);
+            r.seg = kind == kFirst ? 0 : kind == kBetween ? 1 + nth : r.segs - 1;
+            const int whole = __builtin_amdgcn_readlane(len, src), from = r.seg ? cut.L0 + (r.seg - 1) * cut.L : 0;
+            r.start = __builtin_amdgcn_readlane(start, src) + from;
+            r.len = min(r.segs > 1 && r.seg == 0 ? cut.L0 : cut.L, whole - from);
+            r.slot0 = slots_before + __builtin_amdgcn_readlane(slots_upto - slots, src);
             return r;
         }
         before += __builtin_amdgcn_readlane(upto, 63);
+        slots_before += __builtin_amdgcn_readlane(slots_upto, 63);
     }
-    return Segment{-1, 0, 0, 0, 0};
+    return Segment{-1, 0, 0, 0, 0, 0};
 }
-
-// Workspace slot of a sequence's segment 0 state (segments but the last have one):
-// distinct, since a sequence of n tokens has at most n / tokens of them.
-__device__ __forceinline__ int first_slot(const int32_t *cu, int seq, int tokens) { return cu[seq] / tokens; }
 
 template <int DK, int DV, int QT, bool F32OUT>
 struct Walk {
@@ -337,21 +359,36 @@ struct Walk {
     struct __align__(16) Lds {
         unsigned char q[IP * C * PK], k[IP * C * PK], v[IP * C * PV], p[OP * C * PP];
         float2 g[C];        // prefix sums of the log decays in base 2, as the sum of two f32
+        // e^(G_t - G_j) of the tiles left of the diagonal, as the product of a row's and a column's factor about the
+        // row tile's first token r: e^(G_t - G_r) and scale e^(G_r - G_j)
+        float row[C], col[TT - 1][C];
         float eg[C], w[C];  // scale e^G_t and e^(G_last - G_t)
         float decay;        // e^G_last
         double last;        // G_last
     };
 
-    // Prefix sum of the lanes' log decays, in f64 (one wave; C <= 64 lanes).
+    // x of the lane that DPP control CTRL names, 0 where there is none or the row is masked out
+    template <int CTRL, int ROWS>
+    static __device__ __forceinline__ double dpp_f64(double x)
+    {
+        int w[2];
+        __builtin_memcpy(w, &x, 8);
+        w[0] = __builtin_amdgcn_update_dpp(0, w[0], CTRL, ROWS, 0xF, false);
+        w[1] = __builtin_amdgcn_update_dpp(0, w[1], CTRL, ROWS, 0xF, false);
+        __builtin_memcpy(&x, w, 8);
+        return x;
+    }
+    // Prefix sum of the lanes' log decays, in f64: within rows of 16 lanes (row_shr 1, 2, 4, 8), then a row's
+    // total to the next (row_bcast 15) and the first half's to the second (row_bcast 31)
     static __device__ __forceinline__ double prefix(double g)
     {
-        const int lane = threadIdx.x & 63;
         double s = g < kLowest ? kLowest : g;
-#pragma unroll
-        for (int d = 1; d < C; d <<= 1) {
-            const double o = __shfl_up(s, d, 64);
-            s += lane >= d ? o : 0.0;
-        }
+        s += dpp_f64<0x111, 0xF>(s);
+        s += dpp_f64<0x112, 0xF>(s);
+        s += dpp_f64<0x114, 0xF>(s);
+        s += dpp_f64<0x118, 0xF>(s);
+        s += dpp_f64<0x142, 0xA>(s);
+        s += dpp_f64<0x143, 0xC>(s);
         return s;
     }
 
@@ -392,7 +429,8 @@ struct Walk {
         const char *kp = static_cast<const char *>(p.in.k) + (sg.start * p.in.k_stride + (int64_t)kh * DK) * ES;
         const char *vp = static_cast<const char *>(p.in.v) + (sg.start * p.in.v_stride + (int64_t)h * p.hc.dv + dvh) * ES;
         double tg = 0.0, last = 0.0;
-        float graw = 0.f, te = 0.f, tw = 0.f;
+        float graw = 0.f, te = 0.f, tw = 0.f, trow = 0.f, tcol[TT - 1];
+        float2 g2 = {0.f, 0.f};
         using TK = Tile<QT, C, DK, THREADS>;
         using TV = Tile<QT, C, DV, THREADS>;
         auto from_q = [&](int c0) { return TK::from(qp + (int64_t)c0 * qs, qs, sg.len - c0, tid); };
@@ -406,20 +444,45 @@ struct Walk {
         auto scan = [&](int c0) {
             if (wave == W - 1) {
                 tg = prefix(lane < sg.len - c0 && lane < C ? (head_decay ? rate : (double)graw) : 0.0);
-                last = __shfl(tg, C - 1, 64);
+                int w[2];
+                __builtin_memcpy(w, &tg, 8);
+                w[0] = __builtin_amdgcn_readlane(w[0], C - 1);
+                w[1] = __builtin_amdgcn_readlane(w[1], C - 1);
+                __builtin_memcpy(&last, w, 8);
                 te = expf((float)tg);
                 tw = lane < sg.len - c0 ? expf((float)(last - tg)) : 0.f;
+                if constexpr (OUT) {
+                    constexpr double kLog2e = 1.4426950408889634;
+                    const float hi = (float)(tg * kLog2e);
+                    g2 = make_float2(hi, (float)(tg * kLog2e - hi));
+                    trow = 1.f;
+#pragma unroll
+                    for (int i = 1; i < TT; ++i) {
+                        const float rx = lane_value(g2.x, 16 * i), ry = lane_value(g2.y, 16 * i);
+                        const float d = (rx - g2.x) + (ry - g2.y);  // 0 or less up to the row tile's first token
+                        if (i == (lane >> 4))
+                            trow = __builtin_amdgcn_exp2f(-d);
+                        tcol[i - 1] = p.hc.scale * __builtin_amdgcn_exp2f(fminf(d, 0.f));
+                        tcol[i - 1] = d != d ? d : tcol[i - 1];
+                    }
+                    if (lane < 16) {
+                        const float rx = lane_value(g2.x, 0), ry = lane_value(g2.y, 0);
+                        trow = __builtin_amdgcn_exp2f((g2.x - rx) + (g2.y - ry));
+                    }
+                }
             }
         };
         auto stage = [&] {
-            if constexpr (OUT)
-                tq.store(l.q, tid);
             tk.store(l.k, tid);
             tv.store(l.v, tid);
             if (wave == W - 1 && lane < C) {
-                constexpr double kLog2e = 1.4426950408889634;
-                const float hi = (float)(tg * kLog2e);
-                l.g[lane] = make_float2(hi, (float)(tg * kLog2e - hi));
+                if constexpr (OUT) {
+                    l.g[lane] = g2;
+                    l.row[lane] = trow;
+#pragma unroll
+                    for (int i = 1; i < TT; ++i)
+                        l.col[i - 1][lane] = tcol[i - 1];
+                }
                 l.eg[lane] = p.hc.scale * te;
                 l.w[slot_of(lane)] = tw;
                 if (lane == C - 1) {
@@ -442,6 +505,8 @@ struct Walk {
             tq.load(from_q(0));
         tv.load(from_v(0));
         scan(0);
+        if constexpr (OUT)
+            tq.store(l.q, tid);
         stage();
         __syncthreads();
 
@@ -551,14 +616,22 @@ struct Walk {
                     if (MERGED && jt[m] > it[m])
                         continue;
                     const int t = 16 * it[m] + li, j0 = 16 * jt[m] + 4 * lg;
-                    const float2 gt = l.g[t];
                     float x[4];
+                    if (jt[m] < it[m]) {
+                        const float row = l.row[t];
+                        const f32x4 col = *reinterpret_cast<const f32x4 *>(&l.col[it[m] - 1][j0]);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float2 gj = l.g[j0 + r];
-                        x[r] = a[m][r] * (p.hc.scale * __builtin_amdgcn_exp2f((gt.x - gj.x) + (gt.y - gj.y)));
-                        asm volatile("" : "+v"(x[r]));  // taken for every lane: no branch around each exponential
-                        x[r] = j0 + r <= t ? x[r] : 0.f;
+                        for (int r = 0; r < 4; ++r)
+                            x[r] = a[m][r] * (row * col[r]);
+                    } else {
+                        const float2 gt = l.g[t];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const float2 gj = l.g[j0 + r];
+                            x[r] = a[m][r] * (p.hc.scale * __builtin_amdgcn_exp2f((gt.x - gj.x) + (gt.y - gj.y)));
+                            asm volatile("" : "+v"(x[r]));  // taken for every lane: no branch around each exponential
+                            x[r] = j0 + r <= t ? x[r] : 0.f;
+                        }
                     }
                     // tokens 4 lg .. + 3 of the tile: two pairs of neighbouring slots
                     unsigned char *at = l.p + t * PP + 2 * slot_of(j0);
@@ -585,7 +658,9 @@ struct Walk {
                 }
                 if (more)
                     scan(c0 + C);
-                __syncthreads();  // P is whole
+                __syncthreads();  // P is whole, and the chunk's q rows are no longer read
+                if (more)
+                    tq.store(l.q, tid);
             } else if (more) {
                 fetch_g(c0 + C);
                 tk.load(from_k(c0 + C));
@@ -724,7 +799,7 @@ struct Walk {
     }
 };
 
-// Blocks: segment-major, then heads, then a head's parts of DV rows.
+// Blocks: segments (the launch's first kind, then its second), then heads, then a head's parts of DV rows.
 template <int DK, int DV, int QT, bool F32OUT, bool SECOND>
 __global__ __launch_bounds__((Geo<DK, DV, QT>::THREADS), (Geo<DK, DV, QT>::WAVES)) void chunk_kernel(const LinattnParams p)
 {
@@ -732,14 +807,16 @@ __global__ __launch_bounds__((Geo<DK, DV, QT>::THREADS), (Geo<DK, DV, QT>::WAVES
     __shared__ typename Wk::Lds l;
     const int parts = p.hc.dv / DV, dvh = blockIdx.x % parts * DV;
     const int h = blockIdx.x / parts % p.hc.Hv;
-    const Segment sg = find_segment(p.cu, p.N, blockIdx.x / parts / p.hc.Hv, p.seg_tokens, SECOND);
+    const int idx = blockIdx.x / parts / p.hc.Hv, one = SECOND ? p.segs_between : p.segs_first;
+    const Cut cut{p.seg_tokens, p.seg_first_tokens};
+    const Segment sg = find_segment(p.cu, p.N, cut, idx < one ? (SECOND ? kBetween : kFirst) : (SECOND ? kLast : kBetween),
+                                    idx < one ? idx : idx - one);
     if (sg.seq < 0)
         return;
     const int64_t size = (int64_t)DK * p.hc.dv, skip = (int64_t)DK * dvh;
     float *state = p.state + ((int64_t)sg.seq * p.hc.Hv + h) * size + skip;
-    const bool last = sg.seg == sg.segs - 1;
-    const int64_t slot = last && !sg.seg ? 0 : ((int64_t)first_slot(p.cu, sg.seq, p.seg_tokens) + sg.seg) * p.hc.Hv + h;
-    float *after = last ? state : p.seg_state + slot * size + skip;
+    const int64_t slot = (int64_t)(sg.slot0 + sg.seg) * p.hc.Hv + h;
+    float *after = sg.seg == sg.segs - 1 ? state : p.seg_state + slot * size + skip;
     if constexpr (SECOND) {
         Wk::template run<true>(l, p, sg, h, dvh, p.seg_state + (slot - p.hc.Hv) * size + skip, after);
     } else if (sg.seg == 0) {
