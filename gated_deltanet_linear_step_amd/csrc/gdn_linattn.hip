@@ -238,6 +238,7 @@ using linattn::Cut;
 // about kSegments over all heads (and a head's parts of 128 dv rows): every one but a sequence's last costs a pass
 // over its keys and values and its state written and read twice. Two workgroups run on each of the 256 CUs.
 constexpr int kMinSegment = 256, kSegments = 1024, kResident = 512;
+constexpr int kShortest = 8;  // sequences up to this long go token by token
 
 int parts_of(int dv) { return dv > 128 ? dv / 128 : 1; }
 
@@ -345,6 +346,10 @@ size_t linattn_prefill_workspace_bytes(int, int Hv, int dk, int dv, int, int64_t
 hipError_t launch_linattn_prefill(const LinattnParams &given, const int32_t *cu, hipStream_t s)
 {
     LinattnParams p = given;
+    // A chunk costs the same however few tokens are in it. 8 sequences x 32 heads of 128 x 128, us (recurrence,
+    // chunks): 4 tokens 10 14, 8 13.5 13.8, 16 20 14; 64 sequences: 8 68 77, 16 100 78.
+    if (p.T <= kShortest)
+        return launch_recur(p, s);
     const Cut cut = choose_cut(cu, p.N, p.hc.Hv, p.hc.dv, p.total);
     const Counts c = count_segments(cu, p.N, cut);
     p.seg_tokens = cut.L;

@@ -56,9 +56,11 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 constexpr int input_parts(int qt) { return qt == DT_BF16 ? 1 : qt == DT_F16 ? 2 : 3; }
 
 // A workgroup covers DV of a head's dv rows (all of them up to 128; two workgroups share
-// a head of 256), NT tiles of 16 to a wave.
-template <int DK, int DV, int QT>
+// a head of 256), NT tiles of 16 to a wave: two where the registers allow it, which halve the LDS reads of K^T, Q
+// and P against one.
+template <int DK, int DV, int QT, bool F32OUT>
 struct Geo {
+    static constexpr int OP = F32OUT ? 3 : 2;  // parts of P and S in the outputs
     static constexpr int IP = input_parts(QT);
     static constexpr int NT = DV == 128 && DK <= 128 ? 2 : 1;
     static constexpr int W = DV / (16 * NT);
@@ -66,11 +68,14 @@ struct Geo {
     static constexpr int PK = DK * 2 + 16, PV = DV * 2 + 16;  // row pitches, bytes
     static constexpr int lds(int c)
     {
-        return IP * c * (2 * PK + PV) + 3 * c * (2 * c + 16) + 32 * c + 32;
+        return IP * c * (2 * PK + PV) + OP * c * (2 * c + 16) + 32 * c + 32;
     }
-    static constexpr int C = lds(64) <= 160 * 1024 ? 64 : 32;
-    // waves per SIMD that the registers leave room for
-    static constexpr int WAVES = QT == DT_BF16 ? 2 : 1;
+    // Tokens per chunk: 64, or 32 where two workgroups then fit a CU's 160 KB and registers (4096 tokens, 32 heads,
+    // us with 64 and 32: f16 128 x 128 130 108, 96 x 96 103 84, 64 x 64, where two of 64 fit, 52 56; f32 64 x 64 89 68,
+    // 128 x 64 123 92, 96 x 96, where registers leave one workgroup, 126 133) or where 64 do not fit at all
+    static constexpr int kLds = 160 * 1024;
+    static constexpr bool PAIR = 2 * lds(64) > kLds && 2 * lds(32) <= kLds && (W <= 4 || (W <= 6 && QT != DT_F32));
+    static constexpr int C = PAIR || lds(64) > kLds ? 32 : 64;
 };
 constexpr int rows_per_workgroup(int dv) { return dv > 128 ? 128 : dv; }
 
@@ -350,10 +355,10 @@ __device__ __forceinline__ Segment find_segment(const int32_t *cu, int N, Cut cu
 
 template <int DK, int DV, int QT, bool F32OUT>
 struct Walk {
-    using G = Geo<DK, DV, QT>;
+    using G = Geo<DK, DV, QT, F32OUT>;
     static constexpr int IP = G::IP, C = G::C, NT = G::NT, W = G::W, THREADS = G::THREADS;
     static constexpr int PK = G::PK, PV = G::PV, PP = 2 * C + 16;
-    static constexpr int OP = F32OUT ? 3 : 2, LIM = F32OUT ? 2 : 1;  // parts of P and S in the outputs
+    static constexpr int OP = G::OP, LIM = F32OUT ? 2 : 1;  // parts' orders that the outputs' products go to
     static constexpr int KT = DK / 16, KS = DK / 32, TT = C / 16, JS = C / 32;
 
     struct __align__(16) Lds {
@@ -366,6 +371,9 @@ struct Walk {
         float decay;        // e^G_last
         double last;        // G_last
     };
+
+    // waves per SIMD that the registers leave room for: those of two workgroups, where their LDS fits
+    static constexpr int WAVES = 2 * sizeof(Lds) <= 160 * 1024 && W == 4 ? 2 : 1;
 
     // x of the lane that DPP control CTRL names, 0 where there is none or the row is masked out
     template <int CTRL, int ROWS>
@@ -801,7 +809,7 @@ struct Walk {
 
 // Blocks: segments (the launch's first kind, then its second), then heads, then a head's parts of DV rows.
 template <int DK, int DV, int QT, bool F32OUT, bool SECOND>
-__global__ __launch_bounds__((Geo<DK, DV, QT>::THREADS), (Geo<DK, DV, QT>::WAVES)) void chunk_kernel(const LinattnParams p)
+__global__ __launch_bounds__((Geo<DK, DV, QT, F32OUT>::THREADS), (Walk<DK, DV, QT, F32OUT>::WAVES)) void chunk_kernel(const LinattnParams p)
 {
     using Wk = Walk<DK, DV, QT, F32OUT>;
     __shared__ typename Wk::Lds l;
@@ -831,7 +839,7 @@ __global__ __launch_bounds__((Geo<DK, DV, QT>::THREADS), (Geo<DK, DV, QT>::WAVES
 template <int DK, int DV, int QT, bool F32OUT>
 hipError_t launch_chunk(const LinattnParams &p, int64_t segments, bool second, hipStream_t s)
 {
-    constexpr int threads = Geo<DK, DV, QT>::THREADS;
+    constexpr int threads = Geo<DK, DV, QT, F32OUT>::THREADS;
     const unsigned blocks = (unsigned)(segments * p.hc.Hv * (p.hc.dv / DV));
     if (second)
         chunk_kernel<DK, DV, QT, F32OUT, true><<<blocks, threads, 0, s>>>(p);
