@@ -261,10 +261,9 @@ struct Counts {
 };
 Counts count_segments(const int32_t *cu, int N, Cut cut)
 {
-    Counts c{0, 0, 0};
+    Counts c{N, 0, 0};  // an empty sequence counts for a first segment, which ends at once
     for (int i = 0; i < N; ++i) {
         const int segs = cut.segments(cu[i + 1] - cu[i]);
-        c.first += segs > 0;
         c.between += segs > 2 ? segs - 2 : 0;
         c.last += segs > 1;
     }
@@ -300,17 +299,12 @@ __global__ __launch_bounds__(256) void scan_kernel(const LinattnParams p, int ve
 {
     const int blocks = (vecs + 255) / 256;
     const int part = blockIdx.x % blocks, h = blockIdx.x / blocks % p.hc.Hv, seq = blockIdx.x / blocks / p.hc.Hv;
-    const int at = part * 256 + threadIdx.x, lane = threadIdx.x & 63;
+    const int at = part * 256 + threadIdx.x;
     const Cut cut{p.seg_tokens, p.seg_first_tokens};
     const int segs = cut.segments(p.cu[seq + 1] - p.cu[seq]);
     if (segs < 3)
         return;
-    int slot0 = 0;  // the states of the sequences before this one
-    for (int s0 = 0; s0 < seq; s0 += 64) {
-        const int s = s0 + lane;
-        const int n = s < seq ? cut.segments(p.cu[s + 1] - p.cu[s]) : 0;
-        slot0 += __builtin_amdgcn_readlane(linattn::lane_sum(n > 1 ? n - 1 : 0), 63);
-    }
+    const int slot0 = linattn::slots_before(p.cu, cut, seq);
     if (at >= vecs)
         return;
     const int64_t step = (int64_t)p.hc.Hv * vecs;

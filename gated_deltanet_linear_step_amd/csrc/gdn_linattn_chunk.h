@@ -315,22 +315,39 @@ __device__ __forceinline__ int lane_sum(int x)
     return x;
 }
 
+// The states between segments of the sequences before `seq`.
+__device__ __forceinline__ int slots_before(const int32_t *cu, Cut cut, int seq)
+{
+    int slots = 0;
+    for (int s0 = 0; s0 < seq; s0 += 64) {
+        const int s = s0 + (threadIdx.x & 63);
+        const int n = s < seq ? cut.segments(cu[s + 1] - cu[s]) : 0;
+        slots += __builtin_amdgcn_readlane(lane_sum(n > 1 ? n - 1 : 0), 63);
+    }
+    return slots;
+}
+
 // Segments are dealt out longest first, by kind: every sequence's first, those between, the last of several.
 enum SegmentKind { kFirst, kBetween, kLast };
 struct Segment {
     int seq, seg, segs, start, len;
     int slot0;  // of the sequence's states after its segments but the last
 };
-// Segment `idx` of a kind. Every lane counts for one of 64 sequences at a time.
+// Segment `idx` of a kind; len 0 if there is none. Every sequence counts for one of the first kind, so that many
+// short sequences need no search; else every lane counts for one of 64 sequences at a time.
 __device__ __forceinline__ Segment find_segment(const int32_t *cu, int N, Cut cut, int kind, int idx)
 {
+    if (kind == kFirst) {
+        const int start = cu[idx], len = cu[idx + 1] - start, segs = cut.segments(len);
+        return Segment{idx, 0, segs, start, segs > 1 ? cut.L0 : len, segs > 1 ? slots_before(cu, cut, idx) : 0};
+    }
     const int lane = threadIdx.x & 63;
-    int before = 0, slots_before = 0;
+    int before = 0, slots_upto_here = 0;
     for (int s0 = 0; s0 < N; s0 += 64) {
         const int s = s0 + lane;
         const int start = s < N ? cu[s] : 0, len = s < N ? cu[s + 1] - start : 0;
         const int segs = cut.segments(len), slots = max(segs - 1, 0);
-        const int cnt = kind == kFirst ? min(segs, 1) : kind == kBetween ? max(segs - 2, 0) : min(slots, 1);
+        const int cnt = kind == kBetween ? max(segs - 2, 0) : min(slots, 1);
         const int upto = lane_sum(cnt), slots_upto = lane_sum(slots);
         const uint64_t hit = __ballot(idx >= before + upto - cnt && idx < before + upto);
         if (hit) {
@@ -340,17 +357,17 @@ __device__ __forceinline__ Segment find_segment(const int32_t *cu, int N, Cut cu
             r.seq = s0 + src;
             r.segs = __builtin_amdgcn_readlane(segs, src);
             const int nth = idx - before - __builtin_amdgcn_readlane(upto - cnt, src);
-            r.seg = kind == kFirst ? 0 : kind == kBetween ? 1 + nth : r.segs - 1;
-            const int whole = __builtin_amdgcn_readlane(len, src), from = r.seg ? cut.L0 + (r.seg - 1) * cut.L : 0;
+            r.seg = kind == kBetween ? 1 + nth : r.segs - 1;
+            const int from = cut.L0 + (r.seg - 1) * cut.L;
             r.start = __builtin_amdgcn_readlane(start, src) + from;
-            r.len = min(r.segs > 1 && r.seg == 0 ? cut.L0 : cut.L, whole - from);
-            r.slot0 = slots_before + __builtin_amdgcn_readlane(slots_upto - slots, src);
+            r.len = min(cut.L, __builtin_amdgcn_readlane(len, src) - from);
+            r.slot0 = slots_upto_here + __builtin_amdgcn_readlane(slots_upto - slots, src);
             return r;
         }
         before += __builtin_amdgcn_readlane(upto, 63);
-        slots_before += __builtin_amdgcn_readlane(slots_upto, 63);
+        slots_upto_here += __builtin_amdgcn_readlane(slots_upto, 63);
     }
-    return Segment{-1, 0, 0, 0, 0, 0};
+    return Segment{0, 0, 0, 0, 0, 0};
 }
 
 template <int DK, int DV, int QT, bool F32OUT>
@@ -467,11 +484,10 @@ struct Walk {
 #pragma unroll
                     for (int i = 1; i < TT; ++i) {
                         const float rx = lane_value(g2.x, 16 * i), ry = lane_value(g2.y, 16 * i);
-                        const float d = (rx - g2.x) + (ry - g2.y);  // 0 or less up to the row tile's first token
+                        const float d = (rx - g2.x) + (ry - g2.y);
                         if (i == (lane >> 4))
                             trow = __builtin_amdgcn_exp2f(-d);
-                        tcol[i - 1] = p.hc.scale * __builtin_amdgcn_exp2f(fminf(d, 0.f));
-                        tcol[i - 1] = d != d ? d : tcol[i - 1];
+                        tcol[i - 1] = p.hc.scale * __builtin_amdgcn_exp2f(d);  // read left of row tile i only
                     }
                     if (lane < 16) {
                         const float rx = lane_value(g2.x, 0), ry = lane_value(g2.y, 0);
@@ -819,7 +835,7 @@ __global__ __launch_bounds__((Geo<DK, DV, QT, F32OUT>::THREADS), (Walk<DK, DV, Q
     const Cut cut{p.seg_tokens, p.seg_first_tokens};
     const Segment sg = find_segment(p.cu, p.N, cut, idx < one ? (SECOND ? kBetween : kFirst) : (SECOND ? kLast : kBetween),
                                     idx < one ? idx : idx - one);
-    if (sg.seq < 0)
+    if (sg.len <= 0)
         return;
     const int64_t size = (int64_t)DK * p.hc.dv, skip = (int64_t)DK * dvh;
     float *state = p.state + ((int64_t)sg.seq * p.hc.Hv + h) * size + skip;

@@ -762,7 +762,7 @@ def _rows(name, t, rows, hidden, dtypes):
     if t.dim() != 2 or tuple(t.shape) != (rows, hidden) or (hidden > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must be [{rows}][{hidden}] with contiguous rows, "
                          f"got {tuple(t.shape)}")
-    return t.stride(0) if rows > 1 else max(t.stride(0), hidden)
+    return t.stride(0) if rows > 1 else hidden
 
 
 def prepare_add_rms_norm(x, weight, *, residual=None, residual_out=None, out=None, out_q=None,

@@ -104,9 +104,9 @@ typedef struct gdn_dims {
                             (96,96), (128,128), (64,128), (128,64), (128,256),
                             (256,128), (256,256). Others: UNSUPPORTED. */
     int32_t head_map;    /* gdn_head_map */
-    int32_t decay;       /* gdn_decay, used with GDN_RAW_GATES */
+    int32_t decay;       /* gdn_decay, used with GDN_RAW_GATES (and GDN_HEAD_DECAY) */
     uint32_t flags;      /* GDN_L2NORM_QK | GDN_RAW_GATES | GDN_GATED_NORM |
-                            GDN_STREAM_STATE */
+                            GDN_STREAM_STATE; gdn_linattn_*: GDN_HEAD_DECAY | GDN_STREAM_STATE */
     float scale;         /* read-out scale; 0 selects 1/sqrt(dk) */
     float l2_eps;        /* 0 selects 1e-6 */
     float norm_eps;      /* 0 selects 1e-6 */
@@ -316,9 +316,10 @@ gdn_status gdn_prefill_chunked_noalloc(const gdn_dims *dims, int32_t num_seqs,
  *          f32; without it in->g [tokens][Hv] f32. Both 4-byte aligned. The other
  *          gate fields, z and norm_weight are ignored.
  *
- * A log decay is at most 0. -inf stands for exp(g) = 0: the state is forgotten.
- * A NaN or infinity in q, k, v or the state goes where the formula takes it (a
- * later exp(g) = 0 does not clear it).
+ * -inf stands for exp(g) = 0: the state is forgotten. A NaN or infinity in q, k, v or
+ * the state makes what the formula makes of it not finite, and nothing else (where the
+ * formula has an infinity, the prefill may have a NaN; a later exp(g) = 0 does not clear
+ * either).
  * Sums are f32 or more exact. A call without tokens does nothing, whatever its
  * per-token pointers.
  * ------------------------------------------------------------------------- */

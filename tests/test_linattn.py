@@ -290,6 +290,55 @@ def test_prefill_lengths(lens, Hk, Hv, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lens,Hv", [([257] * 7, 4), ([256, 257, 255, 600, 0, 1025], 2), ([9000], 16), ([3] * 70 + [900] + [0] * 5 + [700], 2)])
+def test_prefill_segments_keep_to_the_workspace(lens, Hv):
+    """Sequences just past and far past one segment, among many short ones: states within the bound, two runs alike bit
+    for bit, and no byte outside the workspace that the query asks for."""
+    Hk, d, n = 1, 32, sum(lens)
+    c = make(n, Hk, Hv, d, d, torch.bfloat16, n, slots=len(lens))
+    need = ops.linattn_prefill_workspace_bytes(Hk=Hk, Hv=Hv, dk=d, dv=d, num_seqs=len(lens), total_tokens=n)
+    room = torch.full((need + 8192,), 77, dtype=torch.uint8, device=DEV)
+    out, state, cu = run_prefill(c, lens, Hk, Hv, d, d, ops.MAP_GROUPED, "token", torch.float32, workspace=room[4096:4096 + need])
+    assert (room[:4096] == 77).all() and (room[4096 + need:] == 77).all()
+    again, state_again, _ = run_prefill(c, lens, Hk, Hv, d, d, ops.MAP_GROUPED, "token", torch.float32)
+    assert torch.equal(out, again) and torch.equal(state, state_again)
+    check_prefill(c, lens, Hk, Hv, d, d, ops.MAP_GROUPED, "token", out, state, cu)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens", [[1] * 5, [8, 3, 0, 5], [9, 8]])
+def test_prefill_of_short_sequences(lens):
+    Hk, Hv, d = 2, 4, 128
+    c = make(sum(lens), Hk, Hv, d, d, torch.float16, 77, slots=len(lens))
+    out, state, cu = run_prefill(c, lens, Hk, Hv, d, d, ops.MAP_TILED, "rate", torch.float16)
+    check_prefill(c, lens, Hk, Hv, d, d, ops.MAP_TILED, "rate", out, state, cu)
+
+
+@pytest.mark.gpu
+def test_growing_states():
+    """Log decays above 0 are no decay, but the formula holds for them too."""
+    Hk, Hv, d, n = 1, 2, 64, 150
+    c = make(n, Hk, Hv, d, d, torch.bfloat16, 8)
+    c["g"] = c["g"] + 0.2
+    out, state, cu = run_prefill(c, [n], Hk, Hv, d, d, ops.MAP_GROUPED, "token", torch.float32)
+    check_prefill(c, [n], Hk, Hv, d, d, ops.MAP_GROUPED, "token", out, state, cu)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_decay_that_is_not_a_number(dtype):
+    """It spoils its head's outputs and state from its token on, and nothing else."""
+    Hk, Hv, d, n, at = 1, 2, 64, 100, 37
+    c = make(n, Hk, Hv, d, d, dtype, 6)
+    fine, fine_state, _ = run_prefill(c, [n], Hk, Hv, d, d, ops.MAP_GROUPED, "token", torch.float32)
+    c["g"][at, 0] = float("nan")
+    out, state, _ = run_prefill(c, [n], Hk, Hv, d, d, ops.MAP_GROUPED, "token", torch.float32)
+    assert torch.equal(out[:, 1], fine[:, 1]) and torch.equal(out[:at, 0], fine[:at, 0])
+    assert torch.equal(state[0, 1], fine_state[0, 1])
+    assert torch.isnan(out[at:, 0]).all() and torch.isnan(state[0, 0]).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_forgetting_and_strong_decays(dtype):
     """Log decays of -inf, of -1e5 and of 0 among ordinary ones: exp(g) is 0, 0 and 1."""
