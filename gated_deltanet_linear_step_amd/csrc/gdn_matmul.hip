@@ -76,19 +76,21 @@ constexpr int BK = 128;  // bytes of k per stage: an LDS row, 8 blocks of 16
 // rows one read serves at a time (pitch 128 bytes: half the banks) use every bank.
 __device__ __forceinline__ int stage_at(int row, int block) { return row * BK + 16 * (block ^ (row & 7)); }
 
-// WGM x WGN waves, each (BM / WGM) x (BN / WGN) outputs as 32 x 32 tiles.
-template <int BM, int BN, int WGM, int WGN, int WAVES, int D>
-__global__ __launch_bounds__(64 * WGM * WGN, WAVES) void tile_kernel(const MatmulParams p)
+// WGM x WGN waves, each (BM / WGM) x (BN / WGN) outputs as 32 x 32 tiles; KG groups of them, each every KG-th stage
+// of k, whose sums are added at the end. D stages (of every group) are on their way in registers.
+template <int BM, int BN, int WGM, int WGN, int WAVES, int D, int KG>
+__global__ __launch_bounds__(64 * WGM * WGN * KG, WAVES) void tile_kernel(const MatmulParams p)
 {
-    constexpr int THREADS = 64 * WGM * WGN, TM = BM / WGM / 32, TN = BN / WGN / 32;
-    constexpr int UA = BM * 8 / THREADS, UW = BN * 8 / THREADS, STEP = THREADS / 8;
-    constexpr int STAGE = (BM + BN) * BK;
+    constexpr int THREADS = 64 * WGM * WGN * KG, TM = BM / WGM / 32, TN = BN / WGN / 32;
+    constexpr int KB = BK * KG, STEP = THREADS / (8 * KG), UA = BM / STEP, UW = BN / STEP;
+    constexpr int PLANE = (BM + BN) * BK, STAGE = PLANE * KG;
     // epilogue: a wave's 32 rows of its BN / WGN columns, in f32
     constexpr int EP = BN / WGN * 4 + 16, EPI = WGM * WGN * 32 * EP;
-    __shared__ __align__(16) unsigned char lds[2 * STAGE > EPI ? 2 * STAGE : EPI];
+    __shared__ __align__(64) unsigned char lds[2 * STAGE > EPI ? 2 * STAGE : EPI];
 
     const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, half = lane >> 5;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave % WGM, wn = wave / WGM;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), kg = wave / (WGM * WGN);
+    const int wm = wave % WGM, wn = wave / WGM % WGN;
 
     // Workgroups go to the 8 XCDs in turn: give each XCD (with an L2 of its own) a run of
     // neighbouring tiles, 8 tiles of m deep.
@@ -103,7 +105,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, WAVES) void tile_kernel(const Matmu
     const int8_t *ab = p.a + (int64_t)m0 * p.a_stride, *wb = p.w + (int64_t)n0 * p.w_stride;
     const uint32_t a_bytes = (uint32_t)(min(p.M - m0, BM) - 1) * as + p.K;
     const uint32_t w_bytes = (uint32_t)(min(p.N - n0, BN) - 1) * ws + p.K;
-    const int row = tid / 8, block = tid % 8;
+    const int row = tid / (8 * KG), block = tid % (8 * KG);
     // Loads and writes of one stage, in BK / 32 parts that go between the products of a stage: the L1 delivers 64
     // bytes a clock, so that a wave issuing a whole stage's loads at once stands still until most have left.
     constexpr int U = UA + UW, KS = BK / 32, PART = (U + KS - 1) / KS;
@@ -126,8 +128,8 @@ __global__ __launch_bounds__(64 * WGM * WGN, WAVES) void tile_kernel(const Matmu
     auto stage = [&](unsigned char *s, const i32x4 (&r)[U], int part) {
 #pragma unroll
         for (int i = part * PART; i < U && i < (part + 1) * PART; ++i)
-            *reinterpret_cast<i32x4 *>(s + (i < UA ? stage_at(row + i * STEP, block)
-                                                   : BM * BK + stage_at(row + (i - UA) * STEP, block))) = r[i];
+            *reinterpret_cast<i32x4 *>(s + block / 8 * PLANE + (i < UA ? stage_at(row + i * STEP, block % 8)
+                                                                       : BM * BK + stage_at(row + (i - UA) * STEP, block % 8))) = r[i];
     };
 
     i32x16 acc[TN][TM] = {};
@@ -142,7 +144,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, WAVES) void tile_kernel(const Matmu
     };
     // One stage: each step's operands are read during the step before it
     auto step = [&](int buf, int d, int k0, bool load, const i32x4 (&next)[U]) {
-        const unsigned char *s = lds + buf * STAGE;
+        const unsigned char *s = lds + buf * STAGE + kg * PLANE;
         read(s, 0, f[0]);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
@@ -167,20 +169,20 @@ __global__ __launch_bounds__(64 * WGM * WGN, WAVES) void tile_kernel(const Matmu
         __syncthreads();
     };
     // D stages of k in registers on their way to the LDS, besides the two in it
-    const int stages = (p.K + BK - 1) / BK;
+    const int stages = (p.K + KB - 1) / KB;
 #pragma unroll
     for (int d = 0; d < D; ++d)
 #pragma unroll
         for (int part = 0; part < KS; ++part)
-            fetch(d * BK, regs[d], part);
+            fetch(d * KB, regs[d], part);
 #pragma unroll
     for (int part = 0; part < KS; ++part)
         stage(lds, regs[0], part);
     __syncthreads();
-    int buf = 0, k0 = D * BK;
+    int buf = 0, k0 = D * KB;
     for (int g = 0; g < stages / D; ++g) {
 #pragma unroll
-        for (int d = 0; d < D; ++d, k0 += BK) {
+        for (int d = 0; d < D; ++d, k0 += KB) {
             step(buf, d, k0, true, regs[(d + 1) % D]);
             buf ^= 1;
         }
@@ -191,6 +193,21 @@ __global__ __launch_bounds__(64 * WGM * WGN, WAVES) void tile_kernel(const Matmu
             step(buf, d, 0, false, regs[d + 1]);
             buf ^= 1;
         }
+
+    // With KG > 1 the other groups of waves hand their sums over, behind the epilogue's part of the LDS
+    if constexpr (KG > 1) {
+        constexpr int WAVES1 = WGM * WGN;
+        static_assert(TM == 1 && TN == 1 && EPI % 64 == 0 && EPI + (KG - 1) * WAVES1 * 4096 <= 2 * STAGE, "one tile a wave");
+        i32x16 *sums = reinterpret_cast<i32x16 *>(lds + EPI) + wave % WAVES1 * 64 + lane;
+        if (kg > 0)
+            sums[(kg - 1) * WAVES1 * 64] = acc[0][0];
+        __syncthreads();
+        if (kg > 0)
+            return;
+#pragma unroll
+        for (int g = 0; g < KG - 1; ++g)
+            acc[0][0] += sums[g * WAVES1 * 64];
+    }
 
     // Epilogue, 32 rows of m at a time through the wave's own LDS: a lane holds n = 8 g + 4 half + e of row l32
     unsigned char *mine = lds + wave * 32 * EP;
@@ -233,37 +250,35 @@ __global__ __launch_bounds__(64 * WGM * WGN, WAVES) void tile_kernel(const Matmu
     }
 }
 
-template <int BM, int BN, int WGM, int WGN, int WAVES, int D>
+template <int BM, int BN, int WGM, int WGN, int WAVES, int D, int KG = 1>
 hipError_t launch_tiles(const MatmulParams &p, hipStream_t s)
 {
     const int64_t tiles = (int64_t)((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
-    tile_kernel<BM, BN, WGM, WGN, WAVES, D><<<(unsigned)tiles, 64 * WGM * WGN, 0, s>>>(p);
+    tile_kernel<BM, BN, WGM, WGN, WAVES, D, KG><<<(unsigned)tiles, 64 * WGM * WGN * KG, 0, s>>>(p);
     return hipGetLastError();
 }
 
 // ---- a few rows ---------------------------------------------------------------
 
-constexpr int kSkinnyRows = 32, kSkinnyWaves = 8;
+constexpr int kSkinnyRows = 16, kSkinnyWaves = 8;
 
-// 16 MT rows by 16 NT columns a workgroup; its waves take 256 bytes of k in turn, straight from global memory (a
+// 16 rows by 16 NT columns a workgroup; its waves take 256 bytes of k in turn, straight from global memory (a
 // weight is read by one lane, once), and add up their sums through LDS.
-template <int MT, int NT>
+template <int NT>
 __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(const MatmulParams p)
 {
     constexpr int STEPS = 4;
-    __shared__ i32x4 part[kSkinnyWaves][MT * NT][64];
+    __shared__ i32x4 part[kSkinnyWaves][NT][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, lg = lane >> 4;
     const int n0 = blockIdx.x * 16 * NT;
-    const int8_t *wr[NT], *ar[MT];
+    const int8_t *wr[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j)
         wr[j] = p.w + (int64_t)min(n0 + 16 * j + li, p.N - 1) * p.w_stride;
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-        ar[i] = p.a + (int64_t)min(16 * i + li, p.M - 1) * p.a_stride;
-    i32x4 acc[MT][NT] = {};
+    const int8_t *ar = p.a + (int64_t)min(li, p.M - 1) * p.a_stride;
+    i32x4 acc[NT] = {};
     for (int k0 = wave * 64 * STEPS; k0 < p.K; k0 += kSkinnyWaves * 64 * STEPS) {
-        i32x4 fw[STEPS][NT], fa[STEPS][MT];
+        i32x4 fw[STEPS][NT], fa[STEPS];
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
             const int k = k0 + 64 * s + 16 * lg;
@@ -272,52 +287,44 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(const MatmulP
 #pragma unroll
             for (int j = 0; j < NT; ++j)
                 fw[s][j] = *reinterpret_cast<const i32x4 *>(wr[j] + kc);
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                fa[s][i] = *reinterpret_cast<const i32x4 *>(ar[i] + kc);
-                fa[s][i] = in ? fa[s][i] : i32x4{0, 0, 0, 0};
-            }
+            fa[s] = *reinterpret_cast<const i32x4 *>(ar + kc);
+            fa[s] = in ? fa[s] : i32x4{0, 0, 0, 0};
         }
 #pragma unroll
         for (int s = 0; s < STEPS; ++s)
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[s][j], fa[s][i], acc[i][j], 0, 0, 0);
+            for (int j = 0; j < NT; ++j)
+                acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[s][j], fa[s], acc[j], 0, 0, 0);
     }
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-            part[wave][i * NT + j][lane] = acc[i][j];
+    for (int j = 0; j < NT; ++j)
+        part[wave][j][lane] = acc[j];
     __syncthreads();
     // wave x adds up tile x: a lane holds columns 4 lg .. + 3 of row li
-    for (int x = wave; x < MT * NT; x += kSkinnyWaves) {
-        i32x4 sum = part[0][x][lane];
+    if (wave < NT) {
+        i32x4 sum = part[0][wave][lane];
 #pragma unroll
         for (int w = 1; w < kSkinnyWaves; ++w)
-            sum += part[w][x][lane];
-        const int m = 16 * (x / NT) + li, n = n0 + 16 * (x % NT) + 4 * lg, valid = min(p.N - n, 4);
-        if (m < p.M && valid > 0) {
-            const float sa = p.a_scale[m];
+            sum += part[w][wave][lane];
+        const int n = n0 + 16 * wave + 4 * lg, valid = min(p.N - n, 4);
+        if (li < p.M && valid > 0) {
+            const float sa = p.a_scale[li];
             float y[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 y[e] = (float)sum[e] * sa * p.w_scale[n + min(e, valid - 1)];
-            store_row<4>(p.out, (int64_t)m * p.out_stride + n, p.out_dt, y, valid);
+            store_row<4>(p.out, (int64_t)li * p.out_stride + n, p.out_dt, y, valid);
         }
     }
 }
 
-template <int MT>
 hipError_t launch_skinny(const MatmulParams &p, hipStream_t s)
 {
     // two column tiles share each read of a, where that leaves a workgroup for every CU
     if (p.N >= 256 * 32)
-        skinny_kernel<MT, 2><<<(p.N + 31) / 32, 64 * kSkinnyWaves, 0, s>>>(p);
+        skinny_kernel<2><<<(p.N + 31) / 32, 64 * kSkinnyWaves, 0, s>>>(p);
     else
-        skinny_kernel<MT, 1><<<(p.N + 15) / 16, 64 * kSkinnyWaves, 0, s>>>(p);
+        skinny_kernel<1><<<(p.N + 15) / 16, 64 * kSkinnyWaves, 0, s>>>(p);
     return hipGetLastError();
 }
 
@@ -333,25 +340,31 @@ double stage_cost(const MatmulParams &p, int bm, int bn, double alone, double ea
 
 hipError_t launch_matmul(const MatmulParams &p, hipStream_t s)
 {
-    // M x 8192 x 2048, us (skinny, 64 x 64 tiles): M = 1 4.9 7.4, 16 5.4 7.2, 32 6.5 7.5, 48 7.7 7.5, 64 8.3 7.5
-    if (p.M <= 16)
-        return launch_skinny<1>(p, s);
+    // M x 8192 x 2048, us (skinny, tiles): M = 1 4.9 5.8, 16 5.4 6.0; M x 2048 x 4096: 1 4.3 6.0, 16 5.7 6.0. A second
+    // block of 16 rows costs the skinny kernel as much again: 32 6.5 6.2, 7.5 6.2.
     if (p.M <= kSkinnyRows)
-        return launch_skinny<2>(p, s);
+        return launch_skinny(p, s);
     // A larger tile reads each operand from the LDS fewer times, but a stage of it takes a lone workgroup longer:
-    // the tile whose slowest CU is done first. M x N x K, us (256 x 256, 128 x 128, 64 x 128, 64 x 64):
-    //   1001 x 2050 x 4112  50  24  30  31      100 x 8192 x 2048  27  13  9.6  8.0
-    //   1001 x 2048 x 4096  47  21  17  20      2048 x 4096 x 2048 31  26  30   36
-    //   4096 x 4096 x 4096  66  81  99  122     300 x 12288 x 2048 29  22  17   19
-    const double a = stage_cost(p, 256, 256, 1.42, 1.42), b = stage_cost(p, 128, 128, 0.63, 0.66),
-                 c = stage_cost(p, 64, 128, 0.49, 0.41), d = stage_cost(p, 64, 64, 0.33, 0.28);
-    if (a <= b && a <= c && a <= d)
-        return launch_tiles<256, 256, 2, 4, 2, 2>(p, s);
-    if (b <= c && b <= d)
-        return launch_tiles<128, 128, 2, 2, 2, 2>(p, s);
-    if (c <= d)
-        return launch_tiles<64, 128, 1, 4, 2, 2>(p, s);
-    return launch_tiles<64, 64, 2, 2, 2, 3>(p, s);
+    // the tile whose slowest CU is done first. The smallest two deal k out to groups of waves besides (2 and 4).
+    // M x N x K, us (256 x 256, 128 x 128, 64 x 128, 64 x 64, 64 x 32, 32 x 32):
+    //   4096 x 4096 x 4096  66  81  99  122  -  -        100 x 8192 x 2048  27  13  9.6  7.9  8.5  12
+    //   2048 x 4096 x 2048  31  26  30  36   -  -         64 x 8192 x 2048  -   -   -    7.7  6.5  7.3
+    //   1001 x 2050 x 4112  50  24  30  29   30 36       128 x 2048 x 4096  46  20  15   11   8.2  6.6
+    //   1001 x 2048 x 4096  47  21  17  20   23 29        64 x 2048 x 4096  -   -   -    11   7.9  6.2
+    const struct {
+        double cost;
+        hipError_t (*launch)(const MatmulParams &, hipStream_t);
+    } tiles[] = {{stage_cost(p, 256, 256, 1.42, 1.42), launch_tiles<256, 256, 2, 4, 2, 2>},
+                 {stage_cost(p, 128, 128, 0.63, 0.66), launch_tiles<128, 128, 2, 2, 2, 2>},
+                 {stage_cost(p, 64, 128, 0.49, 0.41), launch_tiles<64, 128, 1, 4, 2, 2>},
+                 {stage_cost(p, 64, 64, 0.33, 0.28), launch_tiles<64, 64, 2, 2, 2, 3>},
+                 {stage_cost(p, 64, 32, 0.22, 0.21), launch_tiles<64, 32, 2, 1, 1, 2, 2>},
+                 {stage_cost(p, 32, 32, 0.15, 0.17), launch_tiles<32, 32, 1, 1, 1, 2, 4>}};
+    int best = 0;
+    for (int i = 1; i < 6; ++i)
+        if (tiles[i].cost < tiles[best].cost)
+            best = i;
+    return tiles[best].launch(p, s);
 }
 
 }  // namespace gdn
