@@ -115,8 +115,8 @@ __device__ __forceinline__ void store_vec8(void *p, int64_t idx, int dt, const f
 }
 
 // V vectors of 8 to each of NT threads: rows of 8 up to 8 V NT elements (and the tail). Loads are never
-// conditional -- a thread without a vector loads the last one, and counts it with weight 0 -- so that all of a
-// row's are in flight together.
+// conditional -- a thread without a vector loads the last one, and counts it in no sum and no maximum (its owner may
+// have stored residual_out over it by then) -- so that all of a row's are in flight together.
 template <int DT, int V, int NT, bool RES>
 __global__ __launch_bounds__(NT) void row_kernel(const NormParams p)
 {
@@ -146,12 +146,8 @@ __global__ __launch_bounds__(NT) void row_kernel(const NormParams p)
     Vec8<DT_F32> w[V];
     float wt = p.weight[tc];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
+    for (int v = 0; v < V; ++v)
         w[v] = load_vec8<DT_F32>(p.weight, 8 * min(v * NT + tid, whole - 1));
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            w[v].w[e] = v * NT + tid < whole ? w[v].w[e] : 0u;
-    }
     wt = tails ? wt : 0.f;
 
     int par = 0;
@@ -197,12 +193,15 @@ __global__ __launch_bounds__(NT) void row_kernel(const NormParams p)
         const float rs = 1.f / sqrtf(ss / (float)p.hidden + p.eps);
         uint32_t top = 0;
 #pragma unroll
-        for (int v = 0; v < V; ++v)
+        for (int v = 0; v < V; ++v) {
+            uint32_t tv = 0;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 h[v][e] = h[v][e] * rs * __uint_as_float(w[v].w[e]);
-                top = max(top, __float_as_uint(h[v][e]) & 0x7fffffffu);
+                tv = max(tv, __float_as_uint(h[v][e]) & 0x7fffffffu);
             }
+            top = max(top, v * NT + tid < whole ? tv : 0u);
+        }
         ht = tails ? ht * rs * wt : 0.f;
         top = max(top, __float_as_uint(ht) & 0x7fffffffu);
         if (p.out) {

@@ -360,6 +360,7 @@ gdn_status gdn_linattn_prefill_chunked(const gdn_dims *dims, int32_t num_seqs,
  *     out_q = y 127 / max_i |y_i|, rounded to nearest, ties to even
  *
  * computed in f32 from the unrounded h, each output rounded once.
+ * A row whose squares' sum leaves f32's range has y = 0.
  * A row whose largest |y| is below 2^-100 has out_q = 0 and out_scale = 0. A row
  * with an infinite or NaN y has out_q = 0 and out_scale = NaN.
  *

@@ -182,6 +182,19 @@ def test_norm_rows_of_zeros_and_rows_that_are_not_finite(hidden):
     check_norm({n: t[keep] for n, t in got.items()}, x[keep], r[keep], w)
 
 
+@pytest.mark.gpu
+def test_norm_in_place_of_the_largest_numbers():
+    # the squares' sum is infinite, so y is 0 -- also where a thread reads the row's last elements only after
+    # their owner has stored h over the residual: x + h is infinite
+    for hidden in (528, 2056, 2600):
+        x = torch.full((700, hidden), 2e38, device=DEV)
+        r = torch.zeros_like(x)
+        got = ops.add_rms_norm(x, torch.ones(hidden, device=DEV), residual=r, residual_out=r, quantize=True,
+                               out_dtype=torch.float32)
+        assert (got["out"] == 0).all() and (got["out_q"] == 0).all() and (got["out_scale"] == 0).all()
+        assert torch.equal(r, x)
+
+
 # ---- the product ---------------------------------------------------------------
 
 def matmul_inputs(M, N, K, seed, pad=0):
