@@ -599,6 +599,8 @@ gdn_status gdn_add_rms_norm(const gdn_norm_args *a, void *stream)
         return GDN_ERR_UNSUPPORTED;
     if (!std::isfinite(a->eps) || a->eps < 0.f)
         return GDN_ERR_SHAPE;
+    if (a->hidden > 1 << 24)
+        return GDN_ERR_OVERFLOW;
     if (a->rows == 0)
         return GDN_OK;
     if (!a->x || !a->weight || (!a->out && !a->out_q) || (a->out_q != nullptr) != (a->out_scale != nullptr))

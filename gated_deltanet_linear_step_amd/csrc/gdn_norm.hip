@@ -260,44 +260,46 @@ __global__ __launch_bounds__(kLoopThreads) void loop_kernel(const NormParams p)
     constexpr int WAVES = kLoopThreads / 64;
     __shared__ float sums[WAVES];
     __shared__ uint32_t tops[WAVES];
-    const int64_t row = blockIdx.x;
-    float ss = 0.f;
-    for (int i = threadIdx.x; i < p.hidden; i += kLoopThreads) {
-        const float h = norm_input(p, row, i);
-        ss = fmaf(h, h, ss);
-    }
-    ss = group_sum<64>(ss);
-    if ((threadIdx.x & 63) == 0)
-        sums[threadIdx.x >> 6] = ss;
-    __syncthreads();
-    ss = 0.f;
-    for (int w = 0; w < WAVES; ++w)
-        ss += sums[w];
-    const float rs = 1.f / sqrtf(ss / (float)p.hidden + p.eps);
-    Quant q{0.f, 0.f};
-    if (p.out_q) {
-        uint32_t top = 0;
-        for (int i = threadIdx.x; i < p.hidden; i += kLoopThreads)
-            top = max(top, __float_as_uint(norm_input(p, row, i) * rs * p.weight[i]) & 0x7fffffffu);
-        top = wave_max(top);
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        float ss = 0.f;
+        for (int i = threadIdx.x; i < p.hidden; i += kLoopThreads) {
+            const float h = norm_input(p, row, i);
+            ss = fmaf(h, h, ss);
+        }
+        ss = group_sum<64>(ss);
         if ((threadIdx.x & 63) == 0)
-            tops[threadIdx.x >> 6] = top;
+            sums[threadIdx.x >> 6] = ss;
         __syncthreads();
+        ss = 0.f;
         for (int w = 0; w < WAVES; ++w)
-            top = max(top, tops[w]);
-        q = quant_of(top);
-        if (threadIdx.x == 0)
-            p.out_scale[row] = q.scale;
-    }
-    for (int i = threadIdx.x; i < p.hidden; i += kLoopThreads) {
-        const float h = norm_input(p, row, i);
-        if (p.residual_out)
-            store_act(p.residual_out, row * p.residual_out_stride + i, p.dt, h);
-        const float y = h * rs * p.weight[i];
-        if (p.out)
-            store_act(p.out, row * p.out_stride + i, p.out_dt, y);
-        if (p.out_q)
-            p.out_q[row * p.out_q_stride + i] = (int8_t)quant(y, q);
+            ss += sums[w];
+        const float rs = 1.f / sqrtf(ss / (float)p.hidden + p.eps);
+        Quant q{0.f, 0.f};
+        if (p.out_q) {
+            uint32_t top = 0;
+            for (int i = threadIdx.x; i < p.hidden; i += kLoopThreads)
+                top = max(top, __float_as_uint(norm_input(p, row, i) * rs * p.weight[i]) & 0x7fffffffu);
+            top = wave_max(top);
+            if ((threadIdx.x & 63) == 0)
+                tops[threadIdx.x >> 6] = top;
+            __syncthreads();
+            for (int w = 0; w < WAVES; ++w)
+                top = max(top, tops[w]);
+            q = quant_of(top);
+            if (threadIdx.x == 0)
+                p.out_scale[row] = q.scale;
+        }
+        for (int i = threadIdx.x; i < p.hidden; i += kLoopThreads) {
+            const float h = norm_input(p, row, i);
+            if (p.residual_out)
+                store_act(p.residual_out, row * p.residual_out_stride + i, p.dt, h);
+            const float y = h * rs * p.weight[i];
+            if (p.out)
+                store_act(p.out, row * p.out_stride + i, p.out_dt, y);
+            if (p.out_q)
+                p.out_q[row * p.out_q_stride + i] = (int8_t)quant(y, q);
+        }
+        __syncthreads();  // the sums and tops are read
     }
 }
 
@@ -334,7 +336,7 @@ constexpr int kRowMost = 16 * 1024 + 8;  // four vectors a thread would spill
 hipError_t launch_norm(const NormParams &p, hipStream_t s)
 {
     if (p.hidden < 8 || p.hidden >= kRowMost) {
-        loop_kernel<<<p.rows, kLoopThreads, 0, s>>>(p);
+        loop_kernel<<<std::min(p.rows, 512), kLoopThreads, 0, s>>>(p);  // two a CU; each takes every grid-th row
         return hipGetLastError();
     }
     switch (p.dt) {

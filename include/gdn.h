@@ -364,7 +364,7 @@ gdn_status gdn_linattn_prefill_chunked(const gdn_dims *dims, int32_t num_seqs,
  * A row whose largest |y| is below 2^-100 has out_q = 0 and out_scale = 0. A row
  * with an infinite or NaN y has out_q = 0 and out_scale = NaN.
  *
- *   rows, hidden   >= 0 rows of >= 1 elements
+ *   rows, hidden   >= 0 rows of 1 to 2^24 elements (more: OVERFLOW)
  *   dtype          of x, residual and residual_out
  *   x, residual    rows of x_stride / residual_stride elements (>= hidden), aligned to
  *                  their element size; residual may be NULL (h = x)
@@ -378,7 +378,7 @@ gdn_status gdn_linattn_prefill_chunked(const gdn_dims *dims, int32_t num_seqs,
  *   out_q          NULL, or int8 rows of out_q_stride; out_scale [rows] f32 goes with it
  *                  (both or neither)
  * At least one of out and out_q. Outputs may not overlap one another.
- * Errors: NULL, SHAPE (counts, strides, eps), UNSUPPORTED (dtype), ALIGN, LAUNCH.
+ * Errors: NULL, SHAPE (counts, strides, eps), UNSUPPORTED (dtype), OVERFLOW, ALIGN, LAUNCH.
  * ------------------------------------------------------------------------- */
 typedef struct gdn_norm_args {
     int32_t rows, hidden;
