@@ -644,9 +644,11 @@ gdn_status gdn_quant_matmul(int32_t M, int32_t N, int32_t K, const int8_t *a, in
         return GDN_ERR_SHAPE;
     if (!dtype_ok(out_dtype) || K % 16 != 0)
         return GDN_ERR_UNSUPPORTED;
-    // |a w| <= 2^14, so K products stay below 2^31; the grid's tiles are at least 16 x 16
-    // and rows are addressed with 32-bit byte offsets within a tile of 256
-    if (K > 131056 || (((int64_t)M + 15) / 16) * (((int64_t)N + 15) / 16) > kI32Max ||
+    // |a w| <= 2^14, so K products stay below 2^31; tiles of up to 256 x 256 outputs count their rows
+    // in 32 bits and launch 2^32 threads at most, 512 each; rows are addressed with 32-bit byte
+    // offsets within a tile
+    if (K > 131056 || M > kI32Max - 255 || N > kI32Max - 255 ||
+        (((int64_t)M + 255) / 256) * (((int64_t)N + 255) / 256) >= (int64_t)1 << 23 ||
         a_stride >= (int64_t)1 << 23 || w_stride >= (int64_t)1 << 23)
         return GDN_ERR_OVERFLOW;
     if (M == 0 || N == 0)

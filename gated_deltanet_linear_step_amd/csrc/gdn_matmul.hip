@@ -328,11 +328,16 @@ hipError_t launch_skinny(const MatmulParams &p, hipStream_t s)
     return hipGetLastError();
 }
 
+constexpr int64_t kMostTiles = 1 << 23;
+
 // Microseconds that a CU takes for a stage (BK bytes of k) of its tiles, as measured at K = 4096: `alone` for a
-// workgroup by itself, `each` for each of several that share or follow one another on the CU.
+// workgroup by itself, `each` for each of several that share or follow one another on the CU. A launch holds fewer
+// than 2^32 threads: tiles too many for that (at 512 threads each) cost more than any other.
 double stage_cost(const MatmulParams &p, int bm, int bn, double alone, double each)
 {
     const int64_t tiles = (int64_t)((p.M + bm - 1) / bm) * ((p.N + bn - 1) / bn), per_cu = (tiles + 255) / 256;
+    if (bm < 256 && tiles >= kMostTiles)
+        return 1e30;
     return per_cu <= 1 ? alone : (double)per_cu * each;
 }
 
@@ -342,7 +347,7 @@ hipError_t launch_matmul(const MatmulParams &p, hipStream_t s)
 {
     // M x 8192 x 2048, us (skinny, tiles): M = 1 4.9 5.8, 16 5.4 6.0; M x 2048 x 4096: 1 4.3 6.0, 16 5.7 6.0. A second
     // block of 16 rows costs the skinny kernel as much again: 32 6.5 6.2, 7.5 6.2.
-    if (p.M <= kSkinnyRows)
+    if (p.M <= kSkinnyRows && (p.N + 15) / 16 < kMostTiles)
         return launch_skinny(p, s);
     // A larger tile reads each operand from the LDS fewer times, but a stage of it takes a lone workgroup longer:
     // the tile whose slowest CU is done first. The smallest two deal k out to groups of waves besides (2 and 4).

@@ -406,11 +406,12 @@ gdn_status gdn_add_rms_norm(const gdn_norm_args *args, void *stream);
  *
  *     out[m][n] = (sum_k a[m][k] w[n][k]) a_scale[m] w_scale[n]
  *
- * The integer sums are exact (32 bits); the scales are applied in f32 and the result is
- * rounded once. A NaN scale makes its row or column NaN.
+ * The integer sums are exact (32 bits); the scales are applied in f32, a_scale first, and
+ * the result is rounded once. A NaN scale makes its row or column NaN.
  *
- *   M, N, K      M, N >= 0; K >= 1 a multiple of 16 (else UNSUPPORTED), at most 131056
- *                (else OVERFLOW: the sum could leave 32 bits)
+ *   M, N, K      M, N >= 0, at most 2^31 - 256 and ceil(M / 256) ceil(N / 256) below 2^23
+ *                (else OVERFLOW); K >= 1 a multiple of 16 (else UNSUPPORTED), at most
+ *                131056 (else OVERFLOW: the sum could leave 32 bits)
  *   a            [M] int8 rows of a_stride bytes (>= K)
  *   w            [N] int8 rows of w_stride bytes (>= K): a torch Linear's weight layout
  *                a, w and both strides are multiples of 16 bytes, strides below 2^23

@@ -66,6 +66,9 @@ def matmul(M=4, N=4, K=64, a=P, a_stride=64, a_scale=P, w=P, w_stride=64, w_scal
 @pytest.mark.parametrize("want,kw", [
     (SHAPE, dict(M=-1)), (SHAPE, dict(N=-1)), (SHAPE, dict(K=0)), (UNSUPPORTED, dict(K=40)), (UNSUPPORTED, dict(out_dtype=3)),
     (OVERFLOW, dict(K=131072, a_stride=131072, w_stride=131072)), (OVERFLOW, dict(M=2 ** 31 - 1, N=2 ** 31 - 1, out_stride=2 ** 31)),
+    (OVERFLOW, dict(M=2 ** 31 - 1)), (OVERFLOW, dict(N=2 ** 31 - 1, out_stride=2 ** 31)),
+    (OVERFLOW, dict(M=2 ** 31 - 256, N=257, out_stride=257)), (OVERFLOW, dict(M=2 ** 20, N=2 ** 20, out_stride=2 ** 20)),
+    (NULL, dict(M=2 ** 31 - 256, N=256, out_stride=256, out=0)), (NULL, dict(M=1, N=2 ** 31 - 256, out_stride=2 ** 31, out=0)),
     (OVERFLOW, dict(a_stride=2 ** 23)), (OVERFLOW, dict(w_stride=2 ** 23)),
     (NULL, dict(a=0)), (NULL, dict(w=0)), (NULL, dict(out=0)), (NULL, dict(a_scale=0)), (NULL, dict(w_scale=0)),
     (SHAPE, dict(a_stride=48)), (SHAPE, dict(w_stride=48)), (SHAPE, dict(out_stride=3)),
