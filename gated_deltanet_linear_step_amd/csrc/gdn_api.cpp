@@ -517,7 +517,7 @@ gdn_status gdn_linattn_decode_step(const gdn_dims *dims, int32_t batch, int32_t 
     if (!state_slots && num_slots < batch)
         return GDN_ERR_SHAPE;
     if ((int64_t)batch * tokens_per_seq > kI32Max ||
-        gdn::linattn_decode_workgroups(batch, dims->num_v_heads, dims->head_dim_k, dims->head_dim_v) > kI32Max)
+        !gdn::linattn_grid_fits(batch, dims->num_v_heads, dims->head_dim_k, dims->head_dim_v))
         return GDN_ERR_OVERFLOW;
     if (batch == 0)
         return GDN_OK;
@@ -568,7 +568,7 @@ gdn_status gdn_linattn_prefill_chunked(const gdn_dims *dims, int32_t num_seqs,
     if (st != GDN_OK)
         return st;
     if ((int64_t)total_tokens * dims->num_v_heads > kI32Max ||
-        gdn::linattn_decode_workgroups(num_seqs, dims->num_v_heads, dims->head_dim_k, dims->head_dim_v) > kI32Max)
+        !gdn::linattn_grid_fits(num_seqs, dims->num_v_heads, dims->head_dim_k, dims->head_dim_v))
         return GDN_ERR_OVERFLOW;
     if (total_tokens == 0)
         return GDN_OK;  // every sequence empty: states untouched

@@ -151,7 +151,7 @@ struct LinattnParams {
     float *seg_state, *seg_decay;
 };
 bool linattn_supported(int dk, int dv);
-int64_t linattn_decode_workgroups(int N, int Hv, int dk, int dv);
+bool linattn_grid_fits(int N, int Hv, int dk, int dv);
 hipError_t launch_linattn_decode(const LinattnParams &p, hipStream_t s);
 size_t linattn_prefill_workspace_bytes(int Hk, int Hv, int dk, int dv, int N, int64_t total_tokens);
 // cu: the offsets on the host

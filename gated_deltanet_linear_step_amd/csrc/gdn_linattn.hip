@@ -219,11 +219,11 @@ hipError_t launch_recur(const LinattnParams &p, hipStream_t s)
 
 bool linattn_supported(int dk, int dv) { return decode_supported(dk, dv); }
 
-// Workgroups of the recurrence for the smallest split it uses: the host checks that
-// the grid stays within 31 bits.
-int64_t linattn_decode_workgroups(int N, int Hv, int dk, int dv)
+// Whether a launch over the sequences' heads holds fewer than 2^32 threads: the recurrence with two rows to a lane
+// group (with one it has few workgroups); the chunk kernels have no more for the same states.
+bool linattn_grid_fits(int N, int Hv, int dk, int dv)
 {
-    return (int64_t)N * Hv * ((dv + recur_rows(dk, 1) - 1) / recur_rows(dk, 1));
+    return (int64_t)N * Hv * ((dv + recur_rows(dk, 2) - 1) / recur_rows(dk, 2)) * 64 * kRecurWaves < (int64_t)1 << 32;
 }
 
 hipError_t launch_linattn_decode(const LinattnParams &p, hipStream_t s) { return launch_recur(p, s); }
@@ -294,30 +294,28 @@ Cut choose_cut(const int32_t *cu, int N, int Hv, int dv, int64_t total)
 
 // Entering states: a sequence's slot s (state after its segment s, entered with zero
 // from s = 1 on) becomes the state after segment s. HBM bound, one float4 a thread; the
-// loads of later segments do not wait for the running sum.
-__global__ __launch_bounds__(256) void scan_kernel(const LinattnParams p, int vecs)
+// loads of later segments do not wait for the running sum. The grid covers `seqs` sequences at a time.
+__global__ __launch_bounds__(256) void scan_kernel(const LinattnParams p, int vecs, int seqs)
 {
-    const int blocks = (vecs + 255) / 256;
-    const int part = blockIdx.x % blocks, h = blockIdx.x / blocks % p.hc.Hv, seq = blockIdx.x / blocks / p.hc.Hv;
-    const int at = part * 256 + threadIdx.x;
+    const int blocks = vecs / 256;  // vecs = dk dv / 4 is a multiple of 256 for every head shape
+    const int at = blockIdx.x % blocks * 256 + threadIdx.x, h = blockIdx.x / blocks % p.hc.Hv;
     const Cut cut{p.seg_tokens, p.seg_first_tokens};
-    const int segs = cut.segments(p.cu[seq + 1] - p.cu[seq]);
-    if (segs < 3)
-        return;
-    const int slot0 = linattn::slots_before(p.cu, cut, seq);
-    if (at >= vecs)
-        return;
-    const int64_t step = (int64_t)p.hc.Hv * vecs;
-    const int64_t slot = (int64_t)slot0 * p.hc.Hv + h;
-    float4 *x = reinterpret_cast<float4 *>(p.seg_state) + slot * vecs + at;
-    const float *d = p.seg_decay + slot;
-    float4 run = *x;
+    for (int64_t seq = blockIdx.x / blocks / p.hc.Hv; seq < p.N; seq += seqs) {
+        const int segs = cut.segments(p.cu[seq + 1] - p.cu[seq]);
+        if (segs < 3)
+            continue;
+        const int64_t step = (int64_t)p.hc.Hv * vecs;
+        const int64_t slot = (int64_t)linattn::slots_before(p.cu, cut, (int)seq) * p.hc.Hv + h;
+        float4 *x = reinterpret_cast<float4 *>(p.seg_state) + slot * vecs + at;
+        const float *d = p.seg_decay + slot;
+        float4 run = *x;
 #pragma unroll 4
-    for (int s = 1; s < segs - 1; ++s) {
-        const float4 add = x[s * step];
-        const float a = expf(d[(int64_t)s * p.hc.Hv]);
-        run = make_float4(fmaf(a, run.x, add.x), fmaf(a, run.y, add.y), fmaf(a, run.z, add.z), fmaf(a, run.w, add.w));
-        x[s * step] = run;
+        for (int s = 1; s < segs - 1; ++s) {
+            const float4 add = x[s * step];
+            const float a = expf(d[(int64_t)s * p.hc.Hv]);
+            run = make_float4(fmaf(a, run.x, add.x), fmaf(a, run.y, add.y), fmaf(a, run.z, add.z), fmaf(a, run.w, add.w));
+            x[s * step] = run;
+        }
     }
 }
 
@@ -356,8 +354,10 @@ hipError_t launch_linattn_prefill(const LinattnParams &given, const int32_t *cu,
     if (e != hipSuccess || c.last == 0)
         return e;
     if (c.between > 0) {
-        const int vecs = p.hc.dk * p.hc.dv / 4;
-        scan_kernel<<<(unsigned)((int64_t)p.N * p.hc.Hv * ((vecs + 255) / 256)), 256, 0, s>>>(p, vecs);
+        // (few sequences have states between segments; a grid of 2^20 workgroups is plenty)
+        const int vecs = p.hc.dk * p.hc.dv / 4, per_seq = p.hc.Hv * (vecs / 256);
+        const int seqs = std::min(p.N, std::max(1, (1 << 20) / per_seq));
+        scan_kernel<<<(unsigned)((int64_t)seqs * per_seq), 256, 0, s>>>(p, vecs, seqs);
         e = hipGetLastError();
         if (e != hipSuccess)
             return e;

@@ -295,7 +295,7 @@ constexpr double kLowest = -1e4;
 // the first segment is walked with its outputs in the first launch; that takes twice as long as the others' states.)
 struct Cut {
     int L, L0;
-    __host__ __device__ int segments(int len) const { return len <= L ? (len > 0 ? 1 : 0) : 1 + (len - L0 + L - 1) / L; }
+    __host__ __device__ int segments(int len) const { return len <= L ? (len > 0 ? 1 : 0) : 2 + (len - L0 - 1) / L; }
 };
 
 __device__ __forceinline__ float lane_value(float x, int lane)

@@ -124,6 +124,7 @@ def decode(d=None, inp=None, batch=2, T=1, state=P, slots=0, num_slots=2, out_dt
     (ALIGN, dict(inp=inputs(q=vp(P + 2)))), (ALIGN, dict(inp=inputs(v_stride=1026))), (ALIGN, dict(inp=inputs(g=vp(P + 2)))),
     (ALIGN, dict(d=dims(flags=ops.HEAD_DECAY), inp=inputs(decay_param=vp(P + 1)))), (ALIGN, dict(state=P + 8)),
     (OVERFLOW, dict(batch=2 ** 30, T=4, num_slots=2 ** 30)), (OVERFLOW, dict(batch=2 ** 27, num_slots=2 ** 27)),
+    (OVERFLOW, dict(batch=2 ** 20, num_slots=2 ** 20)),
     (OK, dict(batch=0)), (OK, dict(batch=0, inp=inputs(q=None, k=None, v=None), out=0)),
 ])
 def test_decode_refusals(want, kw):
@@ -142,6 +143,7 @@ def prefill(d=None, inp=None, cu=(0, 100, 230), total=230, state=P, out_dtype=0,
     (SHAPE, dict(total=-1)), (NULL, dict(cu_dev=0)), (WORKSPACE, dict(ws=0)), (WORKSPACE, dict(nbytes=0)),
     (ALIGN, dict(ws=P + 128)), (UNSUPPORTED, dict(d=dims(flags=ops.STREAM_STATE))), (NULL, dict(inp=inputs(v=None))),
     (OVERFLOW, dict(d=dims(Hk=2, Hv=2048), cu=(0, 2 ** 21), total=2 ** 21, inp=inputs(v_stride=2048 * 128))),
+    (OVERFLOW, dict(cu=(0,) * 2 ** 20 + (5,), total=5)), (WORKSPACE, dict(cu=(0,) * (2 ** 20 - 1) + (5,), total=5, ws=0)),
     (OVERFLOW, dict(inp=inputs(q_stride=2 ** 24))), (ALIGN, dict(out=P + 8)), (OK, dict(cu=(0, 0, 0), total=0)), (OK, dict(cu=(0,), total=0)), (SHAPE, dict(cu=(0,), total=3)),
     (OK, dict(cu=(0, 0), total=0, inp=inputs(q=None, k=None, v=None, g=None), out=0, ws=0)),
 ])
