@@ -418,7 +418,7 @@ struct Walk {
     }
 
     // Walks the segment's chunks from the state at `in` (NULL: zero) and stores the state after them at
-    // `out_state`; OUT: with the tokens' outputs. Returns the segment's summed log decay. in, out_state and
+    // `out_state` (unless NULL); OUT: with the tokens' outputs. Returns the segment's summed log decay. in, out_state and
     // dvh are those of the workgroup's DV rows, the first of which is row dvh of the head.
     template <bool OUT>
     static __device__ __forceinline__ double run(Lds &l, const LinattnParams &p, const Segment sg, int h, int dvh,
@@ -814,6 +814,8 @@ struct Walk {
                 __syncthreads();
             }
         }
+        if (!out_state)
+            return total;
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
@@ -840,9 +842,11 @@ __global__ __launch_bounds__((Geo<DK, DV, QT, F32OUT>::THREADS), (Walk<DK, DV, Q
     const int64_t size = (int64_t)DK * p.hc.dv, skip = (int64_t)DK * dvh;
     float *state = p.state + ((int64_t)sg.seq * p.hc.Hv + h) * size + skip;
     const int64_t slot = (int64_t)(sg.slot0 + sg.seg) * p.hc.Hv + h;
-    float *after = sg.seg == sg.segs - 1 ? state : p.seg_state + slot * size + skip;
+    const bool last = sg.seg == sg.segs - 1;
+    float *after = last ? state : p.seg_state + slot * size + skip;
     if constexpr (SECOND) {
-        Wk::template run<true>(l, p, sg, h, dvh, p.seg_state + (slot - p.hc.Hv) * size + skip, after);
+        // (the states between segments are read in this launch, not written)
+        Wk::template run<true>(l, p, sg, h, dvh, p.seg_state + (slot - p.hc.Hv) * size + skip, last ? state : nullptr);
     } else if (sg.seg == 0) {
         Wk::template run<true>(l, p, sg, h, dvh, state, after);
     } else {

@@ -317,6 +317,26 @@ def test_prefill_of_short_sequences(lens):
 
 
 @pytest.mark.gpu
+def test_prefill_leaves_the_states_between_segments_as_the_running_sum_left_them():
+    # more segments than the card holds at a time, and calls that agree bit for bit
+    Hk, Hv, d, n = 4, 8, 128, 20000
+    gen = torch.Generator().manual_seed(3)
+    q, k, v = (torch.randn(n, H * d, generator=gen).to(DEV) * d ** -0.5 for H in (Hk, Hk, Hv))
+    g = torch.full((n, Hv), -1e-3, device=DEV)
+    cu = torch.tensor([0, n], dtype=torch.int32)
+    heads = dict(Hk=Hk, Hv=Hv, dk=d, dv=d)
+    need = ops.linattn_prefill_workspace_bytes(num_seqs=1, total_tokens=n, **heads)
+    first = None
+    for _ in range(4):
+        ws = torch.zeros(need, dtype=torch.uint8, device=DEV)
+        state = torch.ones(1, Hv, d, d, device=DEV)
+        o = ops.linattn_prefill_chunked(q, k, v, state, cu.to(DEV), cu_seqlens_host=cu, g=g, workspace=ws,
+                                        head_map=ops.MAP_GROUPED, **heads)
+        first = first or (o, state, ws)
+        assert torch.equal(o, first[0]) and torch.equal(state, first[1]) and torch.equal(ws, first[2])
+
+
+@pytest.mark.gpu
 def test_growing_states():
     """Log decays above 0 are no decay, but the formula holds for them too."""
     Hk, Hv, d, n = 1, 2, 64, 150
