@@ -87,6 +87,10 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG, WAVES) void tile_kernel(const 
     // epilogue: a wave's 32 rows of its BN / WGN columns, in f32
     constexpr int EP = BN / WGN * 4 + 16, EPI = WGM * WGN * 32 * EP;
     __shared__ __align__(64) unsigned char lds[2 * STAGE > EPI ? 2 * STAGE : EPI];
+    // the tile's scales of a and w, fetched behind the first stages: after the products a round trip to memory for
+    // them would stand alone
+    __shared__ __align__(16) float scales[BM + BN];
+    static_assert(BM + BN <= THREADS && 64 % (BN / WGN / 8) == 0, "a scale for a thread, whole rows for a wave's stores");
 
     const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), kg = wave / (WGM * WGN);
@@ -175,6 +179,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG, WAVES) void tile_kernel(const 
 #pragma unroll
         for (int part = 0; part < KS; ++part)
             fetch(d * KB, regs[d], part);
+    const float scale = tid < BM ? p.a_scale[min(m0 + tid, p.M - 1)] : p.w_scale[min(n0 + min(tid - BM, BN - 1), p.N - 1)];
 #pragma unroll
     for (int part = 0; part < KS; ++part)
         stage(lds, regs[0], part);
@@ -193,6 +198,11 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG, WAVES) void tile_kernel(const 
             step(buf, d, 0, false, regs[d + 1]);
             buf ^= 1;
         }
+
+    if (tid < BM + BN)
+        scales[tid] = scale;
+    if constexpr (KG == 1)
+        __syncthreads();
 
     // With KG > 1 the other groups of waves hand their sums over, behind the epilogue's part of the LDS
     if constexpr (KG > 1) {
@@ -215,13 +225,11 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG, WAVES) void tile_kernel(const 
     const int er = lane / PER, ec = lane % PER * 8;
     const int nb = n0 + wn * TN * 32, valid = p.N - nb - ec;
     float sw[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        sw[e] = e < valid ? p.w_scale[nb + ec + e] : 0.f;
+    __builtin_memcpy(sw, &scales[BM + wn * TN * 32 + ec], sizeof(sw));
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
         const int mb = m0 + (wm * TM + i) * 32;
-        const float sa = mb + l32 < p.M ? p.a_scale[mb + l32] : 0.f;
+        const float sa = scales[(wm * TM + i) * 32 + l32];
 #pragma unroll
         for (int j = 0; j < TN; ++j)
 #pragma unroll
@@ -276,6 +284,13 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(const MatmulP
     for (int j = 0; j < NT; ++j)
         wr[j] = p.w + (int64_t)min(n0 + 16 * j + li, p.N - 1) * p.w_stride;
     const int8_t *ar = p.a + (int64_t)min(li, p.M - 1) * p.a_stride;
+    // the scales of the tile that this wave adds up at the end, fetched with the first operands
+    const int n = n0 + 16 * min(wave, NT - 1) + 4 * lg;
+    const float sa = p.a_scale[min(li, p.M - 1)];
+    float sw[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        sw[e] = p.w_scale[min(n + e, p.N - 1)];
     i32x4 acc[NT] = {};
     for (int k0 = wave * 64 * STEPS; k0 < p.K; k0 += kSkinnyWaves * 64 * STEPS) {
         i32x4 fw[STEPS][NT], fa[STEPS];
@@ -306,13 +321,12 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(const MatmulP
 #pragma unroll
         for (int w = 1; w < kSkinnyWaves; ++w)
             sum += part[w][wave][lane];
-        const int n = n0 + 16 * wave + 4 * lg, valid = min(p.N - n, 4);
+        const int valid = min(p.N - n, 4);
         if (li < p.M && valid > 0) {
-            const float sa = p.a_scale[li];
             float y[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                y[e] = (float)sum[e] * sa * p.w_scale[n + min(e, valid - 1)];
+                y[e] = (float)sum[e] * sa * sw[e];
             store_row<4>(p.out, (int64_t)li * p.out_stride + n, p.out_dt, y, valid);
         }
     }
