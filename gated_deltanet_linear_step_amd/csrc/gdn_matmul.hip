@@ -11,11 +11,11 @@
 //  * tile_kernel -- M above kSkinnyRows: BM x BN outputs a workgroup through LDS,
 //    128 bytes of k (a stage) at a time, double buffered, with two or three more stages on
 //    their way in registers. Bound by the LDS: a stage of 256 x 256 moves 192 KB out of
-//    it and 64 KB in for 2048 clocks of products. 4096^3: 66 us, 2071 TOPS (a library's
-//    int8 product reaches 2078 at 8192^3); 8192 x 8192 x 2048: 154 us, where storing the
+//    it and 64 KB in for 2048 clocks of products. 4096^3: 67 us, 2050 TOPS (a library's
+//    int8 product reaches 2078 at 8192^3); 8192 x 8192 x 2048: 152 us, where storing the
 //    128 MB of bf16 outputs adds about 20 us that no product covers.
 //  * skinny_kernel -- a few rows: bound by the weights, which stream through once
-//    (1 x 8192 x 2048: 4.9 us).
+//    (1 x 8192 x 2048: 4.7 us).
 
 #include "gdn_device.h"
 #include "gdn_kernels.h"
@@ -359,17 +359,17 @@ double stage_cost(const MatmulParams &p, int bm, int bn, double alone, double ea
 
 hipError_t launch_matmul(const MatmulParams &p, hipStream_t s)
 {
-    // M x 8192 x 2048, us (skinny, tiles): M = 1 4.9 5.8, 16 5.4 6.0; M x 2048 x 4096: 1 4.3 6.0, 16 5.7 6.0. A second
-    // block of 16 rows costs the skinny kernel as much again: 32 6.5 6.2, 7.5 6.2.
+    // M x 8192 x 2048, us (skinny, tiles): M = 1 4.8 5.5, 16 5.3 5.7; M x 2048 x 4096: 1 4.3 6.0, 16 5.6 5.9. A second
+    // block of 16 rows costs the skinny kernel as much again: 32 6.5 5.9, 7.5 6.1.
     if (p.M <= kSkinnyRows && (p.N + 15) / 16 < kMostTiles)
         return launch_skinny(p, s);
     // A larger tile reads each operand from the LDS fewer times, but a stage of it takes a lone workgroup longer:
     // the tile whose slowest CU is done first. The smallest two deal k out to groups of waves besides (2 and 4).
     // M x N x K, us (256 x 256, 128 x 128, 64 x 128, 64 x 64, 64 x 32, 32 x 32):
-    //   4096 x 4096 x 4096  66  81  99  122  -  -        100 x 8192 x 2048  27  13  9.6  7.9  8.5  12
-    //   2048 x 4096 x 2048  31  26  30  36   -  -         64 x 8192 x 2048  -   -   -    7.7  6.5  7.3
-    //   1001 x 2050 x 4112  50  24  30  29   30 36       128 x 2048 x 4096  46  20  15   11   8.2  6.6
-    //   1001 x 2048 x 4096  47  21  17  20   23 29        64 x 2048 x 4096  -   -   -    11   7.9  6.2
+    //   4096 x 4096 x 4096  67  81  100 121  -  -        100 x 8192 x 2048  26  12  9.0  7.2  8.0  11
+    //   2048 x 4096 x 2048  31  24  28  34   -  -         64 x 8192 x 2048  25  12  8.9  7.1  6.0  7.0
+    //   1001 x 2050 x 4112  50  23  27  28   29 36       128 x 2048 x 4096  45  19  14   11   8.0  6.4
+    //   1001 x 2048 x 4096  46  20  15  18   21 29        64 x 2048 x 4096  43  19  14   11   7.7  6.1
     const struct {
         double cost;
         hipError_t (*launch)(const MatmulParams &, hipStream_t);
