@@ -757,6 +757,8 @@ def linattn_prefill_chunked(q, k, v, state, cu_seqlens, *, Hk, Hv, dk, dv, head_
 
 
 def _rows(name, t, rows, hidden, dtypes):
+    if max(rows, hidden) > 2 ** 31 - 1:
+        raise ValueError(f"{name}: counts must fit 32 bits")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
     if t.dim() != 2 or tuple(t.shape) != (rows, hidden) or (hidden > 1 and t.stride(1) != 1):

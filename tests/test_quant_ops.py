@@ -274,6 +274,12 @@ def test_matmul_binding_refusals():
     assert ops.add_rms_norm(x, torch.ones(64, device=DEV), quantize=True)["out_q"].shape == (0, 64)
     with pytest.raises(ValueError):
         ops.add_rms_norm(x, torch.ones(63, device=DEV))
+    # counts past 32 bits are not cut off
+    many = x.new_zeros(1, 64).expand(2 ** 32 + 5, 64)
+    with pytest.raises(ValueError, match="32 bits"):
+        ops.prepare_add_rms_norm(many, torch.ones(64, device=DEV), out=many)
+    with pytest.raises(ValueError, match="32 bits"):
+        ops.prepare_quant_matmul(a[:1].expand(2 ** 32 + 5, 64), sa, w, sw, torch.empty(4, 8, device=DEV))
 
 
 # ---- a layer of them -----------------------------------------------------------
