@@ -236,8 +236,8 @@ using linattn::Cut;
 
 // Segments are a multiple of 64 tokens (whole chunks of 64 or 32), at least kMinSegment, and not more in a call than
 // about kSegments over all heads (and a head's parts of 128 dv rows): every one but a sequence's last costs a pass
-// over its keys and values and its state written and read twice. Two workgroups run on each of the 256 CUs.
-constexpr int kMinSegment = 256, kSegments = 1024, kResident = 512;
+// over its keys and values and its state written and read twice.
+constexpr int kMinSegment = 128, kSegments = 1024;
 constexpr int kShortest = 8;  // sequences up to this long go token by token
 
 int parts_of(int dv) { return dv > 128 ? dv / 128 : 1; }
@@ -258,32 +258,49 @@ int64_t segment_slots(int Hv, int dv, int64_t total)
 
 struct Counts {
     int64_t first, between, last;
+    int longest_single;
 };
 Counts count_segments(const int32_t *cu, int N, Cut cut)
 {
-    Counts c{N, 0, 0};  // an empty sequence counts for a first segment, which ends at once
+    Counts c{N, 0, 0, 0};  // an empty sequence counts for a first segment, which ends at once
     for (int i = 0; i < N; ++i) {
-        const int segs = cut.segments(cu[i + 1] - cu[i]);
+        const int len = cu[i + 1] - cu[i], segs = cut.segments(len);
+        if (segs == 1)
+            c.longest_single = std::max(c.longest_single, len);
         c.between += segs > 2 ? segs - 2 : 0;
         c.last += segs > 1;
     }
     return c;
 }
 
-// The segment length whose launches end first, as rounds of resident workgroups: a few lengths from the least one on
-// (a few only, and for few sequences: the host walks their offsets for each).
+// The segment length whose launches end first, of a few lengths from the least one on. In units of a token's time in a
+// segment without outputs (29 ns at 128 x 128; with outputs twice that), as measured: a launch takes its longest
+// segment times its rounds, a state between segments 1.55, the second launch and the running sum 250. The host walks the
+// offsets for each length: with many sequences, which fill the card by themselves, one is taken unseen.
+// us with segments of 128, 256, 512: 4096 tokens x 32 heads 104 82 83, 2048 x 32 56 52 74, 1024 x 16 33 44 71,
+// 4096 x 8 45 49 -; 700 tokens x 16 heads of 256 x 256: 52 86 -.
+constexpr int kFewSequences = 64, kManySequencesSegment = 256;
+// Rounds of n workgroups on 256 CUs that hold two each; two that share a CU take 1.4 times as long as one alone.
+double rounds(int64_t n)
+{
+    const int64_t rest = n % 512;
+    return n / 512 * 1.4 + (rest == 0 ? 0.0 : rest <= 256 ? 1.0 : 1.4);
+}
 Cut choose_cut(const int32_t *cu, int N, int Hv, int dv, int64_t total)
 {
-    const int least = least_segment(Hv, dv, total);
+    int least = least_segment(Hv, dv, total);
+    if (N > kFewSequences)
+        least = std::max(least, kManySequencesSegment);
     const int64_t heads = (int64_t)Hv * parts_of(dv);
     Cut best{};
-    int64_t best_cost = 0;
-    for (int i = 0; i < (N <= 64 ? 8 : 1); ++i) {
+    double best_cost = 0;
+    for (int i = 0; i < (N <= kFewSequences ? 8 : 1); ++i) {
         const int L = least + 64 * i * ((least + 511) / 512);
         const Cut cut{L, (L / 2 + 63) / 64 * 64};
         const Counts c = count_segments(cu, N, cut);
-        auto rounds = [&](int64_t segs) { return (segs * heads + kResident - 1) / kResident; };
-        const int64_t cost = L * (rounds(c.first + c.between) + 2 * rounds(c.between + c.last));
+        const double longest = std::max(c.last ? (double)L : 0.0, 2.0 * c.longest_single);
+        const double cost = longest * rounds((c.first + c.between) * heads) + 2.0 * L * rounds((c.between + c.last) * heads) +
+                            1.55 * (double)(c.between * heads) + (c.last ? 250 : 0);
         if (i == 0 || cost < best_cost) {
             best = cut;
             best_cost = cost;
@@ -309,12 +326,23 @@ __global__ __launch_bounds__(256) void scan_kernel(const LinattnParams p, int ve
         float4 *x = reinterpret_cast<float4 *>(p.seg_state) + slot * vecs + at;
         const float *d = p.seg_decay + slot;
         float4 run = *x;
-#pragma unroll 4
-        for (int s = 1; s < segs - 1; ++s) {
-            const float4 add = x[s * step];
-            const float a = expf(d[(int64_t)s * p.hc.Hv]);
-            run = make_float4(fmaf(a, run.x, add.x), fmaf(a, run.y, add.y), fmaf(a, run.z, add.z), fmaf(a, run.w, add.w));
-            x[s * step] = run;
+        // eight segments' loads at a time, in front of the stores
+        for (int s0 = 1; s0 < segs - 1; s0 += 8) {
+            float4 add[8];
+            float a[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int s = min(s0 + i, segs - 2);
+                add[i] = x[s * step];
+                a[i] = d[(int64_t)s * p.hc.Hv];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float e = expf(a[i]);
+                run = make_float4(fmaf(e, run.x, add[i].x), fmaf(e, run.y, add[i].y), fmaf(e, run.z, add[i].z), fmaf(e, run.w, add[i].w));
+                if (s0 + i < segs - 1)
+                    x[(s0 + i) * step] = run;
+            }
         }
     }
 }

@@ -292,7 +292,8 @@ def test_prefill_lengths(lens, Hk, Hv, dtype):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("lens,Hv", [([257] * 7, 4), ([256, 257, 255, 600, 0, 1025], 2), ([9000], 16), ([3] * 70 + [900] + [0] * 5 + [700], 2)])
+@pytest.mark.parametrize("lens,Hv", [([257] * 7, 4), ([256, 257, 255, 600, 0, 1025], 2), ([9000], 16), ([3] * 70 + [900] + [0] * 5 + [700], 2),
+                                     ([129] * 9, 4), ([129, 128, 127, 193, 320, 321], 2), ([300] * 70, 2), ([12000], 1)])
 def test_prefill_segments_keep_to_the_workspace(lens, Hv):
     """Sequences just past and far past one segment, among many short ones: states within the bound, two runs alike bit
     for bit, and no byte outside the workspace that the query asks for."""
