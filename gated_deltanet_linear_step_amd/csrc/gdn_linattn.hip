@@ -21,6 +21,7 @@
 #include "gdn_linattn_chunk.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace gdn {
 namespace {
@@ -326,24 +327,30 @@ __global__ __launch_bounds__(256) void scan_kernel(const LinattnParams p, int ve
         float4 *x = reinterpret_cast<float4 *>(p.seg_state) + slot * vecs + at;
         const float *d = p.seg_decay + slot;
         float4 run = *x;
-        // eight segments' loads at a time, in front of the stores
-        for (int s0 = 1; s0 < segs - 1; s0 += 8) {
-            float4 add[8];
-            float a[8];
+        // eight segments' loads at a time, in front of their stores; the rest by fours (more would be loads for nothing)
+        auto batch = [&](int s0, auto count) {
+            constexpr int n = decltype(count)::value;
+            float4 add[n];
+            float a[n];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < n; ++i) {
                 const int s = min(s0 + i, segs - 2);
                 add[i] = x[s * step];
                 a[i] = d[(int64_t)s * p.hc.Hv];
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < n; ++i) {
                 const float e = expf(a[i]);
                 run = make_float4(fmaf(e, run.x, add[i].x), fmaf(e, run.y, add[i].y), fmaf(e, run.z, add[i].z), fmaf(e, run.w, add[i].w));
                 if (s0 + i < segs - 1)
                     x[(s0 + i) * step] = run;
             }
-        }
+        };
+        int s = 1;
+        for (; s + 8 < segs; s += 8)
+            batch(s, std::integral_constant<int, 8>());
+        for (; s + 1 < segs; s += 4)
+            batch(s, std::integral_constant<int, 4>());
     }
 }
 
