@@ -40,7 +40,7 @@
 // LDS pitches are an odd number of 16-byte blocks: 16 rows of a column, or 16
 // 32-byte row pieces of a transposing read, fall into different banks.
 //
-// 4096 tokens, 32 heads of 128 x 128, bf16: 89 us (launches of 31, 11 and 47); 8 sequences of 30,208 tokens in all: 326.
+// 4096 tokens, 32 heads of 128 x 128, bf16: 85 us (launches of 31, 11 and 45); 8 sequences of 30,208 tokens in all: 328.
 // Bound by matrix and vector instructions: the two chunks that a CU works on at a time take 13.4 K clocks, their 1552
 // products 6.2 K of them; the rest is splitting into parts, decays and LDS reads.
 #pragma once
