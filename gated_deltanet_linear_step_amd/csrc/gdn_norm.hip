@@ -114,16 +114,22 @@ __device__ __forceinline__ void store_vec8(void *p, int64_t idx, int dt, const f
         store_vec8_t<DT_F16>(p, idx, x);
 }
 
-// V vectors of 8 to each of NT threads: rows of 8 up to 8 V NT elements (and the tail). Loads are never
+// V vectors of 8 to each of a workgroup's threads, MOST of them or, where that is 256, whole waves up to it: rows of
+// 8 up to 8 V elements a thread (and the tail). Loads are never
 // conditional -- a thread without a vector loads the last one, and counts it in no sum and no maximum (its owner may
 // have stored residual_out over it by then) -- so that all of a row's are in flight together.
-template <int DT, int V, int NT, bool RES>
-__global__ __launch_bounds__(NT) void row_kernel(const NormParams p)
+template <int DT, int V, int MOST, bool RES>
+__global__ __launch_bounds__(MOST) void row_kernel(const NormParams p)
 {
-    constexpr int WAVES = NT / 64;
+    constexpr int WAVES = MOST / 64;
     __shared__ float sums[2][WAVES];
     __shared__ uint32_t tops[2][WAVES];
-    const int tid = threadIdx.x, wave = tid >> 6;
+    const int tid = threadIdx.x, wave = tid >> 6, NT = MOST == 256 ? blockDim.x : MOST;
+    // the slots of waves that this row has no use for
+    if (MOST == 256 && tid < WAVES && tid >= NT / 64) {
+        sums[0][tid] = sums[1][tid] = 0.f;
+        tops[0][tid] = tops[1][tid] = 0u;
+    }
     const int whole = p.hidden / 8, tail = p.hidden % 8;
     const bool tails = tid < tail;
     const int ti = whole * 8 + tid, tc = min(ti, p.hidden - 1);  // this thread's element of the tail
@@ -303,15 +309,19 @@ __global__ __launch_bounds__(kLoopThreads) void loop_kernel(const NormParams p)
     }
 }
 
-template <int DT, int V, int NT>
+template <int DT, int V, int MOST>
 hipError_t launch_rows_t(const NormParams &p, hipStream_t s)
 {
+    // Up to four waves, as many as the row fills (4096 x 2560 bf16 13.9 us, 15.3 with four; 4096 x 1000 5.5, 6.6);
+    // more are eight or sixteen (five to seven share the four SIMDs unevenly: 4096 x 5120 32.4 us with eight, 35.0 with
+    // five).
+    const int NT = MOST > 256 ? MOST : 64 * ((p.hidden / 8 + 64 * V - 1) / (64 * V));
     // as many workgroups as the card holds at 2048 threads a CU; each takes every grid-th row
     const int grid = std::min(p.rows, 256 * (2048 / NT));
     if (p.residual)
-        row_kernel<DT, V, NT, true><<<grid, NT, 0, s>>>(p);
+        row_kernel<DT, V, MOST, true><<<grid, NT, 0, s>>>(p);
     else
-        row_kernel<DT, V, NT, false><<<grid, NT, 0, s>>>(p);
+        row_kernel<DT, V, MOST, false><<<grid, NT, 0, s>>>(p);
     return hipGetLastError();
 }
 

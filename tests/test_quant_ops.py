@@ -126,7 +126,8 @@ def norm_inputs(rows, hidden, dtype, seed, stride=None):
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
 @pytest.mark.parametrize("rows,hidden", [(1, 1), (3, 7), (2, 64), (5, 513), (4, 1000), (2, 1024), (3, 2048), (2, 2056),
-                                         (1300, 5), (600, 16400), (7, 4096), (2, 5003), (2, 8192), (2, 8200), (1, 16384), (2, 20001), (1, 40008)])
+                                         (1300, 5), (600, 16400), (4200, 1000),
+                                         (3000, 1500), (7, 4096), (2, 5003), (2, 8192), (2, 8200), (1, 16384), (2, 20001), (1, 40008)])
 def test_norm_sizes(rows, hidden, dtype):
     x, r, w = norm_inputs(rows, hidden, dtype, rows + hidden)
     check_norm(ops.add_rms_norm(x, w, residual=r, quantize=True, out_dtype=dtype), x, r, w)
