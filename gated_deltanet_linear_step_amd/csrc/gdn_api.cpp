@@ -13,7 +13,7 @@
 #include <limits>
 #include <mutex>
 
-#include "gdn_kernels.h"
+#include "gdn_ops.h"
 
 namespace {
 

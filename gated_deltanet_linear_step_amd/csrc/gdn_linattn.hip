@@ -17,7 +17,7 @@
 // 5.0, the last-level cache holds part of the states); one sequence of 48 heads: 3.7 us.
 
 #include "gdn_device.h"
-#include "gdn_kernels.h"
+#include "gdn_ops.h"
 #include "gdn_linattn_chunk.h"
 
 #include <algorithm>

@@ -46,7 +46,7 @@
 #pragma once
 
 #include "gdn_device.h"
-#include "gdn_kernels.h"
+#include "gdn_ops.h"
 
 namespace gdn {
 namespace linattn {

@@ -18,7 +18,7 @@
 //    (1 x 8192 x 2048: 4.7 us).
 
 #include "gdn_device.h"
-#include "gdn_kernels.h"
+#include "gdn_ops.h"
 
 namespace gdn {
 namespace {

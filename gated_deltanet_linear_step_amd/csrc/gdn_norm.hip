@@ -19,7 +19,7 @@
 // one round trip to memory.
 
 #include "gdn_device.h"
-#include "gdn_kernels.h"
+#include "gdn_ops.h"
 
 #include <algorithm>
 
