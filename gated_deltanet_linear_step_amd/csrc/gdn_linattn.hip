@@ -278,8 +278,8 @@ Counts count_segments(const int32_t *cu, int N, Cut cut)
 // segment without outputs (29 ns at 128 x 128; with outputs twice that), as measured: a launch takes its longest
 // segment times its rounds, a state between segments 1.55, the second launch and the running sum 250. The host walks the
 // offsets for each length: with many sequences, which fill the card by themselves, one is taken unseen.
-// us with segments of 128, 256, 512: 4096 tokens x 32 heads 104 82 83, 2048 x 32 56 52 74, 1024 x 16 33 44 71,
-// 4096 x 8 45 49 -; 700 tokens x 16 heads of 256 x 256: 52 86 -.
+// us with segments of 128, 256, 512: 4096 tokens x 32 heads 108 85 90, 2048 x 32 58 57 83, 1024 x 16 34 48 79,
+// 4096 x 8 43 52 81; 700 tokens x 16 heads of 256 x 256: 55 71 107.
 constexpr int kFewSequences = 64, kManySequencesSegment = 256;
 // Rounds of n workgroups on 256 CUs that hold two each; two that share a CU take 1.4 times as long as one alone.
 double rounds(int64_t n)
@@ -374,7 +374,7 @@ hipError_t launch_linattn_prefill(const LinattnParams &given, const int32_t *cu,
 {
     LinattnParams p = given;
     // A chunk costs the same however few tokens are in it. 8 sequences x 32 heads of 128 x 128, us (recurrence,
-    // chunks): 4 tokens 10 14, 8 13.5 13.8, 16 20 14; 64 sequences: 8 68 77, 16 100 78.
+    // chunks): 4 tokens 10.4 14.5, 8 13.5 14.4, 16 20 14.4; 64 sequences: 8 68 77, 16 101 78.
     if (p.T <= kShortest)
         return launch_recur(p, s);
     const Cut cut = choose_cut(cu, p.N, p.hc.Hv, p.hc.dv, p.total);

@@ -18,12 +18,15 @@
 // A call whose sequences all have one segment is the first launch alone.
 //
 // Products are on v_mfma_f32_16x16x32_bf16. An operand that is not bf16 is a sum of
-// bf16 parts: f16 two (exact), f32 three (exact). Parts are cut off, not rounded, so
-// that no part overflows; what three leave of an f32 is zero, two leave 2^-16. Products
-// of parts whose orders add up to more than LIM are left out. The state's update keeps
-// 2^-24 (three parts of the decayed V, LIM 2) whatever the types: states are f32. The
-// outputs keep as much for f32 outputs; for 16-bit ones P and the state are taken as
-// two parts, 2^-16, two hundred times finer than the output's own rounding.
+// bf16 parts: f16 two, and f32 -- inputs, the state, P and the decayed V -- three, which
+// leave nothing (of f32 values below 2^-109, less than 2^-133, where bf16 ends). The
+// leading part is cut off, not rounded, so that it cannot overflow: it leaves less than
+// 2^-7 of its power of two. The second is rounded and leaves at most 2^-16, of either sign.
+// Products of parts whose orders, counted from 0, add up to more than 2 are left out:
+// with bf16 inputs there are none; of two f32 factors two of up to 2^-23 each, 2^-22
+// of the product at most; of f32 and f16 one of them. So scores, outputs and states are
+// f32 sums of products exact to 2^-22 or better whatever the output's type: 16-bit
+// outputs are the f32 ones, rounded once.
 //
 // Layouts. A 16x16x32 operand's lane (li, lg) = (lane % 16, lane / 16) holds eight
 // k-values of row li; the accumulator's lane holds column li of rows 4 lg + r.
@@ -40,9 +43,10 @@
 // LDS pitches are an odd number of 16-byte blocks: 16 rows of a column, or 16
 // 32-byte row pieces of a transposing read, fall into different banks.
 //
-// 4096 tokens, 32 heads of 128 x 128, bf16: 85 us (launches of 31, 11 and 45); 8 sequences of 30,208 tokens in all: 328.
-// Bound by matrix and vector instructions: the two chunks that a CU works on at a time take 13.4 K clocks, their 1552
-// products 6.2 K of them; the rest is splitting into parts, decays and LDS reads.
+// 4096 tokens, 32 heads of 128 x 128, bf16: 90 us; 8 sequences of 30,208 tokens in all: 366 (with P and the state in two
+// parts in the outputs of 16 bits 84 and 323, but 2^-15 of a term off, always towards zero).
+// Bound by matrix and vector instructions: of the two chunks that a CU works on at a time the 1904 products take 7.6 K
+// clocks; the rest is splitting into parts, decays and LDS reads.
 #pragma once
 
 #include "gdn_device.h"
@@ -56,15 +60,16 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
+// bf16 parts of an f32 value, and the order up to which products of parts are taken
+constexpr int kParts = 3, kOrder = 2;
 // bf16 parts of an input of dtype QT
 constexpr int input_parts(int qt) { return qt == DT_BF16 ? 1 : qt == DT_F16 ? 2 : 3; }
 
 // A workgroup covers DV of a head's dv rows (all of them up to 128; two workgroups share
 // a head of 256), NT tiles of 16 to a wave: two where the registers allow it, which halve the LDS reads of K^T, Q
 // and P against one.
-template <int DK, int DV, int QT, bool F32OUT>
+template <int DK, int DV, int QT>
 struct Geo {
-    static constexpr int OP = F32OUT ? 3 : 2;  // parts of P and S in the outputs
     static constexpr int IP = input_parts(QT);
     static constexpr int NT = DV == 128 && DK <= 128 ? 2 : 1;
     static constexpr int W = DV / (16 * NT);
@@ -72,11 +77,11 @@ struct Geo {
     static constexpr int PK = DK * 2 + 16, PV = DV * 2 + 16;  // row pitches, bytes
     static constexpr int lds(int c)
     {
-        return IP * c * (2 * PK + PV) + OP * c * (2 * c + 16) + 32 * c + 32;
+        return IP * c * (2 * PK + PV) + kParts * c * (2 * c + 16) + 20 * c + c * (c - 16) / 8 + 32;
     }
     // Tokens per chunk: 64, or 32 where two workgroups then fit a CU's 160 KB and registers (4096 tokens, 32 heads,
-    // us with 64 and 32: f16 128 x 128 130 108, 96 x 96 103 84, 64 x 64, where two of 64 fit, 52 56; f32 64 x 64 89 68,
-    // 128 x 64 123 92, 96 x 96, where registers leave one workgroup, 126 133) or where 64 do not fit at all
+    // us with 64 and 32: f16 128 x 128 134 113, 96 x 96 104 88, 64 x 64 71 56; f32 64 x 64 85 66, 128 x 64 119 93, 96 x 96,
+    // where registers leave one workgroup, 126 133) or where 64 do not fit at all
     static constexpr int kLds = 160 * 1024;
     static constexpr bool PAIR = 2 * lds(64) > kLds && 2 * lds(32) <= kLds && (W <= 4 || (W <= 6 && QT != DT_F32));
     static constexpr int C = PAIR || lds(64) > kLds ? 32 : 64;
@@ -97,13 +102,24 @@ __device__ __forceinline__ uint32_t cut(float &x)
     return h;
 }
 
+// Rounds lo and hi to bf16 (to nearest even): returns their bits as one word, lo's below hi's, and leaves the rests.
+__device__ __forceinline__ uint32_t round2(float &lo, float &hi)
+{
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const uint32_t w = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+    lo -= __uint_as_float(w << 16);
+    hi -= __uint_as_float(w & 0xffff0000u);
+    return w;
+}
+
 // The upper halves of two words as one: lo's below hi's.
 __device__ __forceinline__ uint32_t pack_hi(uint32_t lo, uint32_t hi)
 {
     return __builtin_amdgcn_perm(hi, lo, 0x07060302u);
 }
 
-// Eight values as PARTS operands of eight bf16.
+// Eight values as PARTS operands of eight bf16 (the last part has what is left, which fits).
 template <int PARTS>
 __device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&out)[PARTS])
 {
@@ -118,6 +134,8 @@ __device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&out)[PARTS]
         for (int e = 0; e < 4; ++e) {
             if (s == PARTS - 1) {
                 w[e] = pack_hi(__float_as_uint(r[2 * e]), __float_as_uint(r[2 * e + 1]));
+            } else if (s > 0) {
+                w[e] = round2(r[2 * e], r[2 * e + 1]);
             } else {
                 const uint32_t lo = cut(r[2 * e]), hi = cut(r[2 * e + 1]);
                 w[e] = pack_hi(lo, hi);
@@ -376,10 +394,10 @@ __device__ __forceinline__ Segment find_segment(const int32_t *cu, int N, Cut cu
 
 template <int DK, int DV, int QT, bool F32OUT>
 struct Walk {
-    using G = Geo<DK, DV, QT, F32OUT>;
+    using G = Geo<DK, DV, QT>;
     static constexpr int IP = G::IP, C = G::C, NT = G::NT, W = G::W, THREADS = G::THREADS;
     static constexpr int PK = G::PK, PV = G::PV, PP = 2 * C + 16;
-    static constexpr int OP = G::OP, LIM = F32OUT ? 2 : 1;  // parts' orders that the outputs' products go to
+    static constexpr int OP = kParts;
     static constexpr int KT = DK / 16, KS = DK / 32, TT = C / 16, JS = C / 32;
 
     struct __align__(16) Lds {
@@ -387,11 +405,13 @@ struct Walk {
         float2 g[C];        // prefix sums of the log decays in base 2, as the sum of two f32
         // e^(G_t - G_j) of the tiles left of the diagonal, as the product of a row's and a column's factor about the
         // row tile's first token r: e^(G_t - G_r) and scale e^(G_r - G_j)
-        float row[C], col[TT - 1][C];
+        float row[C], col[8 * TT * (TT - 1)];  // row tile i's 16 i columns from col_at(i) on
         float eg[C], w[C];  // scale e^G_t and e^(G_last - G_t)
         float decay;        // e^G_last
         double last;        // G_last
     };
+
+    static constexpr int col_at(int i) { return 8 * i * (i - 1); }
 
     // waves per SIMD that the registers leave room for: those of two workgroups, where their LDS fits
     static constexpr int WAVES = 2 * sizeof(Lds) <= 160 * 1024 && W == 4 ? 2 : 1;
@@ -509,7 +529,8 @@ struct Walk {
                     l.row[lane] = trow;
 #pragma unroll
                     for (int i = 1; i < TT; ++i)
-                        l.col[i - 1][lane] = tcol[i - 1];
+                        if (lane < 16 * i)
+                            l.col[col_at(i) + lane] = tcol[i - 1];
                 }
                 l.eg[lane] = p.hc.scale * te;
                 l.w[slot_of(lane)] = tw;
@@ -582,7 +603,7 @@ struct Walk {
                             for (int x = 0; x < IP; ++x)
 #pragma unroll
                                 for (int y = 0; y < IP; ++y)
-                                    if (x + y <= LIM)
+                                    if (x + y <= kOrder)
                                         a[m] = mfma(lds8(l.k + x * C * PK + (16 * jt[m] + li) * PK + 64 * ks + 16 * lg),
                                                     lds8(l.q + y * C * PK + (16 * it[m] + li) * PK + 64 * ks + 16 * lg),
                                                     ks + x + y == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : a[m]);
@@ -619,7 +640,7 @@ struct Walk {
                             const bf16x8 k0 = lds4x2(kp + 16 * jt[0] * PK), k1 = lds4x2(kp + 16 * jt[1] * PK);
 #pragma unroll
                             for (int y = 0; y < IP; ++y)
-                                if (x + y <= LIM) {
+                                if (x + y <= kOrder) {
                                     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
                                     a[0] = mfma(k0, wave == 2 ? q[0][y] : q[1][y], ks + x + y == 0 ? zero : a[0]);
                                     a[1] = mfma(k1, q[2][y], ks + x + y == 0 ? zero : a[1]);
@@ -635,7 +656,7 @@ struct Walk {
                             for (int v = 0; v < NT; ++v)
 #pragma unroll
                                 for (int s = 0; s < OP; ++s)
-                                    if (s + y <= LIM)
+                                    if (s + y <= kOrder)
                                         O[i][v] = mfma(sp[v][s], q[i][y], ks + y + s == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : O[i][v]);
                     __builtin_amdgcn_sched_barrier(0);  // or every step's reads are issued first, into spills
                 }
@@ -647,7 +668,7 @@ struct Walk {
                     float x[4];
                     if (jt[m] < it[m]) {
                         const float row = l.row[t];
-                        const f32x4 col = *reinterpret_cast<const f32x4 *>(&l.col[it[m] - 1][j0]);
+                        const f32x4 col = *reinterpret_cast<const f32x4 *>(&l.col[col_at(it[m]) + j0]);
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
                             x[r] = a[m][r] * (row * col[r]);
@@ -665,16 +686,22 @@ struct Walk {
                     unsigned char *at = l.p + t * PP + 2 * slot_of(j0);
 #pragma unroll
                     for (int s = 0; s < OP; ++s) {
-                        uint32_t b0 = __float_as_uint(x[0]), b1 = __float_as_uint(x[1]);
-                        uint32_t b2 = __float_as_uint(x[2]), b3 = __float_as_uint(x[3]);
-                        if (s < OP - 1) {
+                        uint32_t even, odd;
+                        if (s == 1) {
+                            even = round2(x[0], x[2]);
+                            odd = round2(x[1], x[3]);
+                        } else {
+                            even = pack_hi(__float_as_uint(x[0]), __float_as_uint(x[2]));
+                            odd = pack_hi(__float_as_uint(x[1]), __float_as_uint(x[3]));
+                        }
+                        if (s == 0) {
                             cut(x[0]);
                             cut(x[1]);
                             cut(x[2]);
                             cut(x[3]);
                         }
-                        *reinterpret_cast<uint32_t *>(at + s * C * PP) = pack_hi(b0, b2);
-                        *reinterpret_cast<uint32_t *>(at + s * C * PP + 32) = pack_hi(b1, b3);
+                        *reinterpret_cast<uint32_t *>(at + s * C * PP) = even;
+                        *reinterpret_cast<uint32_t *>(at + s * C * PP + 32) = odd;
                     }
                 }
 #pragma unroll
@@ -731,7 +758,7 @@ struct Walk {
                                 for (int v = 0; v < NT; ++v)
 #pragma unroll
                                     for (int x = 0; x < IP; ++x)
-                                        if (s + x <= LIM)
+                                        if (s + x <= kOrder)
                                             O[it][v] = mfma(vt[js][v][x], pt, O[it][v]);
                             }
                 } else {
@@ -785,14 +812,14 @@ struct Walk {
             for (int js = 0; js < JS; ++js) {
                 const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&l.w[32 * js + 8 * lg]);
                 const f32x4 w1 = *reinterpret_cast<const f32x4 *>(&l.w[32 * js + 8 * lg + 4]);
-                bf16x8 vd[NT][3];
+                bf16x8 vd[NT][kParts];
 #pragma unroll
                 for (int v = 0; v < NT; ++v) {
                     float x[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         x[e] = join<IP>(vt[js][v], e) * (e < 4 ? w0[e & 3] : w1[e & 3]);
-                    split8<3>(x, vd[v]);
+                    split8<kParts>(x, vd[v]);
                 }
 #pragma unroll
                 for (int kt = 0; kt < KT; ++kt)
@@ -802,8 +829,8 @@ struct Walk {
 #pragma unroll
                         for (int v = 0; v < NT; ++v)
 #pragma unroll
-                            for (int s = 0; s < 3; ++s)
-                                if (s + y <= 2)
+                            for (int s = 0; s < kParts; ++s)
+                                if (s + y <= kOrder)
                                     S[kt][v] = mfma(k, vd[v][s], S[kt][v]);
                     }
                 __builtin_amdgcn_sched_barrier(0);
@@ -831,7 +858,7 @@ struct Walk {
 
 // Blocks: segments (the launch's first kind, then its second), then heads, then a head's parts of DV rows.
 template <int DK, int DV, int QT, bool F32OUT, bool SECOND>
-__global__ __launch_bounds__((Geo<DK, DV, QT, F32OUT>::THREADS), (Walk<DK, DV, QT, F32OUT>::WAVES)) void chunk_kernel(const LinattnParams p)
+__global__ __launch_bounds__((Geo<DK, DV, QT>::THREADS), (Walk<DK, DV, QT, F32OUT>::WAVES)) void chunk_kernel(const LinattnParams p)
 {
     using Wk = Walk<DK, DV, QT, F32OUT>;
     __shared__ typename Wk::Lds l;
@@ -863,7 +890,7 @@ __global__ __launch_bounds__((Geo<DK, DV, QT, F32OUT>::THREADS), (Walk<DK, DV, Q
 template <int DK, int DV, int QT, bool F32OUT>
 hipError_t launch_chunk(const LinattnParams &p, int64_t segments, bool second, hipStream_t s)
 {
-    constexpr int threads = Geo<DK, DV, QT, F32OUT>::THREADS;
+    constexpr int threads = Geo<DK, DV, QT>::THREADS;
     const unsigned blocks = (unsigned)(segments * p.hc.Hv * (p.hc.dv / DV));
     if (second)
         chunk_kernel<DK, DV, QT, F32OUT, true><<<blocks, threads, 0, s>>>(p);

@@ -320,7 +320,8 @@ gdn_status gdn_prefill_chunked_noalloc(const gdn_dims *dims, int32_t num_seqs,
  * the state makes what the formula makes of it not finite, and nothing else (where the
  * formula has an infinity, the prefill may have a NaN; a later exp(g) = 0 does not clear
  * either).
- * Sums are f32 or more exact. A call without tokens does nothing, whatever its
+ * Sums are f32 or more exact, whatever the output's type (of values below 2^-109 the
+ * prefill may leave out what lies below 2^-133). A call without tokens does nothing, whatever its
  * per-token pointers.
  * ------------------------------------------------------------------------- */
 

@@ -4,11 +4,11 @@ CPU, and on the GPU every output and state element against the recurrence in 64 
 Tolerance. With u = 2^-24 and the recurrence run on absolute values, A <- exp(g) A + |v| |k|^T, a term
 that has aged n tokens went through n steps of at most 6 u relative error each (exp to 2 ulp = 4 u, the
 product and the fused add u each); the chunked form applies one factor instead of n and adds at most
-20 u of constant work (operands split into three 8-bit parts leave 2^-24, products of parts below
-2^-24 are left out, and its f32 sums are shorter than the recurrence's). So a state element is off by at
+20 u of constant work (three 8-bit parts leave nothing of an f32; the products of parts left out are 2^-22 = 4 u of a
+product at most, test_linattn_accuracy; its f32 sums are shorter than the recurrence's). So a state element is off by at
 most (6 T + 20) u A, and an output by scale * ((6 T + 20) + dk + 2) u (A |q|) plus its own rounding,
-eps / 2 of its type (and half its smallest subnormal). Sixteen-bit outputs of the prefill may also carry
-intermediate operands of 16 bits (two 8-bit parts, 2^-16): 3 * 2^-16 of scale * (A |q|).
+eps / 2 of its type (and half its smallest subnormal). Sixteen-bit outputs of the prefill are allowed 3 * 2^-16 of
+scale * (A |q|) more here than they need: test_linattn_accuracy holds them to the bound without it.
 """
 import ctypes
 
