@@ -25,8 +25,6 @@ namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 // A buffer of `bytes` from a scalar base: loads past its end give 0.
 typedef __amdgpu_buffer_rsrc_t Buffer;
@@ -113,6 +111,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG, WAVES) void tile_kernel(const 
     // Loads and writes of one stage, in BK / 32 parts that go between the products of a stage: the L1 delivers 64
     // bytes a clock, so that a wave issuing a whole stage's loads at once stands still until most have left.
     constexpr int U = UA + UW, KS = BK / 32, PART = (U + KS - 1) / KS;
+    static_assert(D >= 2, "the stage that goes to the LDS is not the one being fetched");
     i32x4 regs[D][U];
     uint32_t off[U];
 #pragma unroll
@@ -161,14 +160,8 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG, WAVES) void tile_kernel(const 
 #pragma unroll
                 for (int i = 0; i < TM; ++i)
                     acc[j][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f[ks & 1][TM + j], f[ks & 1][i], acc[j][i], 0, 0, 0);
-            if (D > 1)
-                stage(lds + (buf ^ 1) * STAGE, next, ks);
+            stage(lds + (buf ^ 1) * STAGE, next, ks);
             __builtin_amdgcn_sched_barrier(0);
-        }
-        if (D == 1) {
-#pragma unroll
-            for (int part = 0; part < KS; ++part)
-                stage(lds + (buf ^ 1) * STAGE, next, part);
         }
         __syncthreads();
     };
