@@ -226,6 +226,20 @@ gdn_status check_linattn(const gdn_dims *d, const gdn_inputs *in, int64_t tokens
     return GDN_OK;
 }
 
+// What gdn_quant_matmul checks of its counts. |a w| <= 2^14, so K products stay below 2^31; tiles of up to
+// 256 x 256 outputs count their rows in 32 bits and launch 2^32 threads at most, 512 each.
+gdn_status check_matmul_counts(int32_t M, int32_t N, int32_t K)
+{
+    if (M < 0 || N < 0 || K < 1)
+        return GDN_ERR_SHAPE;
+    if (K % 16 != 0)
+        return GDN_ERR_UNSUPPORTED;
+    if (K > 131056 || M > kI32Max - 255 || N > kI32Max - 255 ||
+        (((int64_t)M + 255) / 256) * (((int64_t)N + 255) / 256) >= (int64_t)1 << 23)
+        return GDN_ERR_OVERFLOW;
+    return GDN_OK;
+}
+
 // ---- the static scratch of gdn_prefill_chunked_noalloc ----------------------
 // The prefill's workspace for callers that cannot allocate (graph capture, tight
 // serving loops): a file-scope device array, one copy per GPU, held until the
@@ -327,6 +341,22 @@ gdn_status gdn_prefill_launch_info(const gdn_dims *d, int32_t num_seqs, const in
     info->workgroups = pl.carry_workgroups;
     info->threads = pl.carry_threads;
     info->prep_workgroups = pl.prep_workgroups;
+    return GDN_OK;
+}
+
+gdn_status gdn_quant_matmul_launch_info(int32_t M, int32_t N, int32_t K, gdn_launch_info *info)
+{
+    if (!info)
+        return GDN_ERR_NULL;
+    const gdn_status st = check_matmul_counts(M, N, K);
+    if (st != GDN_OK)
+        return st;
+    *info = gdn_launch_info{};
+    if (M == 0 || N == 0)
+        return GDN_OK;  // nothing is launched
+    const gdn::MatmulPlan pl = gdn::matmul_plan(M, N);
+    info->workgroups = pl.workgroups;
+    info->threads = pl.threads;
     return GDN_OK;
 }
 
@@ -640,16 +670,13 @@ gdn_status gdn_quant_matmul(int32_t M, int32_t N, int32_t K, const int8_t *a, in
                             const float *w_scale, int32_t out_dtype, void *out, int64_t out_stride,
                             void *stream)
 {
-    if (M < 0 || N < 0 || K < 1)
-        return GDN_ERR_SHAPE;
-    if (!dtype_ok(out_dtype) || K % 16 != 0)
+    if (M >= 0 && N >= 0 && K >= 1 && !dtype_ok(out_dtype))
         return GDN_ERR_UNSUPPORTED;
-    // |a w| <= 2^14, so K products stay below 2^31; tiles of up to 256 x 256 outputs count their rows
-    // in 32 bits and launch 2^32 threads at most, 512 each; rows are addressed with 32-bit byte
-    // offsets within a tile
-    if (K > 131056 || M > kI32Max - 255 || N > kI32Max - 255 ||
-        (((int64_t)M + 255) / 256) * (((int64_t)N + 255) / 256) >= (int64_t)1 << 23 ||
-        a_stride >= (int64_t)1 << 23 || w_stride >= (int64_t)1 << 23)
+    const gdn_status st = check_matmul_counts(M, N, K);
+    if (st != GDN_OK)
+        return st;
+    // rows are addressed with 32-bit byte offsets within a tile
+    if (a_stride >= (int64_t)1 << 23 || w_stride >= (int64_t)1 << 23)
         return GDN_ERR_OVERFLOW;
     if (M == 0 || N == 0)
         return GDN_OK;

@@ -252,12 +252,14 @@ __global__ __launch_bounds__(64 * WGM * WGN * KG, WAVES) void tile_kernel(const 
 }
 
 template <int BM, int BN, int WGM, int WGN, int WAVES, int D, int KG = 1>
-hipError_t launch_tiles(const MatmulParams &p, hipStream_t s)
-{
-    const int64_t tiles = (int64_t)((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
-    tile_kernel<BM, BN, WGM, WGN, WAVES, D, KG><<<(unsigned)tiles, 64 * WGM * WGN * KG, 0, s>>>(p);
-    return hipGetLastError();
-}
+struct Tiles {
+    static constexpr int kRows = BM, kCols = BN, kThreads = 64 * WGM * WGN * KG;
+    static hipError_t launch(const MatmulParams &p, unsigned workgroups, hipStream_t s)
+    {
+        tile_kernel<BM, BN, WGM, WGN, WAVES, D, KG><<<workgroups, kThreads, 0, s>>>(p);
+        return hipGetLastError();
+    }
+};
 
 // ---- a few rows ---------------------------------------------------------------
 
@@ -325,37 +327,54 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(const MatmulP
     }
 }
 
-hipError_t launch_skinny(const MatmulParams &p, hipStream_t s)
-{
-    // two column tiles share each read of a, where that leaves a workgroup for every CU
-    if (p.N >= 256 * 32)
-        skinny_kernel<2><<<(p.N + 31) / 32, 64 * kSkinnyWaves, 0, s>>>(p);
-    else
-        skinny_kernel<1><<<(p.N + 15) / 16, 64 * kSkinnyWaves, 0, s>>>(p);
-    return hipGetLastError();
-}
+template <int NT>
+struct Skinny {
+    static constexpr int kRows = kSkinnyRows, kCols = 16 * NT, kThreads = 64 * kSkinnyWaves;
+    static hipError_t launch(const MatmulParams &p, unsigned workgroups, hipStream_t s)
+    {
+        skinny_kernel<NT><<<workgroups, kThreads, 0, s>>>(p);
+        return hipGetLastError();
+    }
+};
 
-constexpr int64_t kMostTiles = 1 << 23;
+constexpr int64_t kMostTiles = 1 << 23;  // a launch holds fewer than 2^32 threads, 512 of them a tile at most
 
 // Microseconds that a CU takes for a stage (BK bytes of k) of its tiles, as measured at K = 4096: `alone` for a
-// workgroup by itself, `each` for each of several that share or follow one another on the CU. A launch holds fewer
-// than 2^32 threads: tiles too many for that (at 512 threads each) cost more than any other.
-double stage_cost(const MatmulParams &p, int bm, int bn, double alone, double each)
+// workgroup by itself, `each` for each of several that share or follow one another on the CU.
+double stage_cost(int64_t tiles, double alone, double each)
 {
-    const int64_t tiles = (int64_t)((p.M + bm - 1) / bm) * ((p.N + bn - 1) / bn), per_cu = (tiles + 255) / 256;
-    if (bm < 256 && tiles >= kMostTiles)
-        return 1e30;
+    const int64_t per_cu = (tiles + 255) / 256;
     return per_cu <= 1 ? alone : (double)per_cu * each;
 }
 
-}  // namespace
+// A kernel of the choice: its outputs a workgroup, threads, and cost of a stage.
+struct Kernel {
+    int rows, cols, threads;
+    double alone, each;
+    hipError_t (*launch)(const MatmulParams &, unsigned, hipStream_t);
+};
+template <class T>
+constexpr Kernel kernel(double alone = 0, double each = 0)
+{
+    return Kernel{T::kRows, T::kCols, T::kThreads, alone, each, T::launch};
+}
+int64_t workgroups(const Kernel &k, int M, int N)
+{
+    return (((int64_t)M + k.rows - 1) / k.rows) * (((int64_t)N + k.cols - 1) / k.cols);
+}
 
-hipError_t launch_matmul(const MatmulParams &p, hipStream_t s)
+constexpr Kernel kSkinny[] = {kernel<Skinny<1>>(), kernel<Skinny<2>>()};
+constexpr Kernel kTiles[] = {kernel<Tiles<256, 256, 2, 4, 2, 2>>(1.42, 1.42), kernel<Tiles<128, 128, 2, 2, 2, 2>>(0.63, 0.66),
+                             kernel<Tiles<64, 128, 1, 4, 2, 2>>(0.49, 0.41),  kernel<Tiles<64, 64, 2, 2, 2, 3>>(0.33, 0.28),
+                             kernel<Tiles<64, 32, 2, 1, 1, 2, 2>>(0.22, 0.21), kernel<Tiles<32, 32, 1, 1, 1, 2, 4>>(0.15, 0.17)};
+
+const Kernel &choose(int M, int N)
 {
     // M x 8192 x 2048, us (skinny, tiles): M = 1 4.8 5.5, 16 5.3 5.7; M x 2048 x 4096: 1 4.3 6.0, 16 5.6 5.9. A second
     // block of 16 rows costs the skinny kernel as much again: 32 6.5 5.9, 7.5 6.1.
-    if (p.M <= kSkinnyRows && (p.N + 15) / 16 < kMostTiles)
-        return launch_skinny(p, s);
+    // Two column tiles share each read of a, where that leaves a workgroup for every CU.
+    if (M <= kSkinnyRows && workgroups(kSkinny[0], M, N) < kMostTiles)
+        return kSkinny[N >= 256 * 32];
     // A larger tile reads each operand from the LDS fewer times, but a stage of it takes a lone workgroup longer:
     // the tile whose slowest CU is done first. The smallest two deal k out to groups of waves besides (2 and 4).
     // M x N x K, us (256 x 256, 128 x 128, 64 x 128, 64 x 64, 64 x 32, 32 x 32):
@@ -363,20 +382,31 @@ hipError_t launch_matmul(const MatmulParams &p, hipStream_t s)
     //   2048 x 4096 x 2048  31  24  28  34   -  -         64 x 8192 x 2048  25  12  8.9  7.1  6.0  7.0
     //   1001 x 2050 x 4112  50  23  27  28   29 36       128 x 2048 x 4096  45  19  14   11   8.0  6.4
     //   1001 x 2048 x 4096  46  20  15  18   21 29        64 x 2048 x 4096  43  19  14   11   7.7  6.1
-    const struct {
-        double cost;
-        hipError_t (*launch)(const MatmulParams &, hipStream_t);
-    } tiles[] = {{stage_cost(p, 256, 256, 1.42, 1.42), launch_tiles<256, 256, 2, 4, 2, 2>},
-                 {stage_cost(p, 128, 128, 0.63, 0.66), launch_tiles<128, 128, 2, 2, 2, 2>},
-                 {stage_cost(p, 64, 128, 0.49, 0.41), launch_tiles<64, 128, 1, 4, 2, 2>},
-                 {stage_cost(p, 64, 64, 0.33, 0.28), launch_tiles<64, 64, 2, 2, 2, 3>},
-                 {stage_cost(p, 64, 32, 0.22, 0.21), launch_tiles<64, 32, 2, 1, 1, 2, 2>},
-                 {stage_cost(p, 32, 32, 0.15, 0.17), launch_tiles<32, 32, 1, 1, 1, 2, 4>}};
-    int best = 0;
-    for (int i = 1; i < 6; ++i)
-        if (tiles[i].cost < tiles[best].cost)
-            best = i;
-    return tiles[best].launch(p, s);
+    const Kernel *best = nullptr;
+    double least = 0;
+    for (const Kernel &k : kTiles) {
+        const int64_t tiles = workgroups(k, M, N);
+        const double cost = stage_cost(tiles, k.alone, k.each);
+        if (!best || (cost < least && tiles < kMostTiles)) {
+            best = &k;
+            least = cost;
+        }
+    }
+    return *best;
+}
+
+}  // namespace
+
+MatmulPlan matmul_plan(int M, int N)
+{
+    const Kernel &k = choose(M, N);
+    return MatmulPlan{(int)workgroups(k, M, N), k.threads};
+}
+
+hipError_t launch_matmul(const MatmulParams &p, hipStream_t s)
+{
+    const Kernel &k = choose(p.M, p.N);
+    return k.launch(p, (unsigned)workgroups(k, p.M, p.N), s);
 }
 
 }  // namespace gdn

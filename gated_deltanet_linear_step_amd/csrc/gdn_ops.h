@@ -66,6 +66,11 @@ struct MatmulParams {
     const float *a_scale, *w_scale;
     void *out;
 };
+// The kernel that launch_matmul takes, M, N >= 1.
+struct MatmulPlan {
+    int workgroups, threads;
+};
+MatmulPlan matmul_plan(int M, int N);
 hipError_t launch_matmul(const MatmulParams &p, hipStream_t s);
 
 }  // namespace gdn

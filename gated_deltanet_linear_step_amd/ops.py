@@ -31,7 +31,8 @@ EXPORTED = ["gdn_conv_update", "gdn_decode_step", "gdn_prefill_workspace_bytes",
             "gdn_prefill_chunked", "gdn_status_string", "gdn_version", "gdn_decode_layer",
             "gdn_decode_launch_info", "gdn_prefill_launch_info", "gdn_prefill_chunked_noalloc",
             "gdn_linattn_decode_step", "gdn_linattn_prefill_workspace_bytes",
-            "gdn_linattn_prefill_chunked", "gdn_add_rms_norm", "gdn_quant_matmul"]
+            "gdn_linattn_prefill_chunked", "gdn_add_rms_norm", "gdn_quant_matmul",
+            "gdn_quant_matmul_launch_info"]
 
 _DT = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 _VP = ctypes.c_void_p
@@ -143,6 +144,9 @@ def load() -> ctypes.CDLL:
     lib.gdn_quant_matmul.argtypes = [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _VP,
                                      ctypes.c_int64, _VP, _VP, ctypes.c_int64, _VP,
                                      ctypes.c_int32, _VP, ctypes.c_int64, _VP]
+    lib.gdn_quant_matmul_launch_info.restype = ctypes.c_int
+    lib.gdn_quant_matmul_launch_info.argtypes = [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                                 ctypes.POINTER(LaunchInfo)]
     _LIB = lib
     return lib
 
@@ -310,6 +314,14 @@ def prefill_launch_info(lengths, *, Hk, Hv, dk, dv, compute_units, head_map=MAP_
     _check(load().gdn_prefill_launch_info(ctypes.byref(dims), len(lengths), arr, cu[-1],
                                           compute_units, ctypes.byref(info)),
            "gdn_prefill_launch_info")
+    return info.as_dict()
+
+
+def quant_matmul_launch_info(M, N, K) -> dict:
+    """The kernel gdn_quant_matmul would run: its workgroups and threads per workgroup."""
+    info = LaunchInfo()
+    _check(load().gdn_quant_matmul_launch_info(M, N, K, ctypes.byref(info)),
+           "gdn_quant_matmul_launch_info")
     return info.as_dict()
 
 

@@ -431,7 +431,7 @@ gdn_status gdn_quant_matmul(int32_t M, int32_t N, int32_t K, const int8_t *a, in
  * follows from its shape and from the device, as the ferrum-kernels tests page
  * checks for its own kernels (`chunk_k_gram_specialization_requires_repeated_
  * k128_heads`, `simd_delta_specialization_is_shape_and_device_capability_driven`).
- * These two calls report the choice the corresponding entry point makes, from the
+ * These calls report the choice the corresponding entry point makes, from the
  * same code; they make no HIP call and launch nothing.
  * ------------------------------------------------------------------------- */
 typedef struct gdn_launch_info {
@@ -444,7 +444,8 @@ typedef struct gdn_launch_info {
                                   slice), 1 carry (one wave per slice); 2 the f32 carry
                                   of the head shapes other than 128 x 128 */
     int32_t slices_per_workgroup; /* prefill: 16-row dv slices per carry workgroup */
-    int32_t workgroups;        /* grid of the decode kernel, or of the prefill carry */
+    int32_t workgroups;        /* grid of the decode kernel, of the prefill carry, or of the
+                                  int8 product (which has this and threads alone) */
     int32_t threads;           /* threads per workgroup of that kernel */
     int32_t prep_workgroups;   /* prefill: grid of the per-chunk preparation kernel */
 } gdn_launch_info;
@@ -461,6 +462,10 @@ gdn_status gdn_decode_launch_info(const gdn_dims *dims, int32_t batch, int32_t t
 gdn_status gdn_prefill_launch_info(const gdn_dims *dims, int32_t num_seqs,
                                    const int32_t *cu_seqlens_host, int32_t total_tokens,
                                    int32_t compute_units, gdn_launch_info *info);
+
+/* The kernel gdn_quant_matmul runs for these counts (none: workgroups 0). Errors: NULL, and
+ * SHAPE, UNSUPPORTED, OVERFLOW as the entry point reports them for M, N, K. */
+gdn_status gdn_quant_matmul_launch_info(int32_t M, int32_t N, int32_t K, gdn_launch_info *info);
 
 /* Static, NUL-terminated description of a status code. */
 const char *gdn_status_string(gdn_status status);
