@@ -595,7 +595,8 @@ def prepare_prefill_chunked(q, k, v, state, cu_seqlens_dev, cu_seqlens_host, out
 # ---- decayed linear attention, residual RMS norm with 8-bit output, int8 product ----
 # These calls run on the tensors' own device, whatever the current one is. What they
 # allocate (outputs, workspaces, offset copies) is allocated on the stream they run on,
-# so its memory is not handed out again before the kernels have read it.
+# so its memory is not handed out again before the kernels have read it. As for torch's own
+# operators, tensors of another stream are ready, and kept until the call has run, by the caller.
 
 def _device_of(**tensors):
     """The one GPU that every given tensor is on."""
