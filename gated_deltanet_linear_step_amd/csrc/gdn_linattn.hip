@@ -275,7 +275,8 @@ Counts count_segments(const int32_t *cu, int N, Cut cut)
 }
 
 // The segment length whose launches end first, of a few lengths from the least one on. In units of a token's time in a
-// segment without outputs (29 ns at 128 x 128; with outputs twice that), as measured: a launch takes its longest
+// segment without outputs (29 ns at 128 x 128; with outputs twice that), as measured for bf16 heads of 128 x 128 and an estimate
+// for others, where a CU may hold one workgroup and a state fewer bytes: a launch takes its longest
 // segment times its rounds, a state between segments 1.55, the second launch and the running sum 250. The host walks the
 // offsets for each length: with many sequences, which fill the card by themselves, one is taken unseen.
 // us with segments of 128, 256, 512: 4096 tokens x 32 heads 108 85 90, 2048 x 32 58 57 83, 1024 x 16 34 48 79,

@@ -43,10 +43,10 @@
 // LDS pitches are an odd number of 16-byte blocks: 16 rows of a column, or 16
 // 32-byte row pieces of a transposing read, fall into different banks.
 //
-// 4096 tokens, 32 heads of 128 x 128, bf16: 90 us; 8 sequences of 30,208 tokens in all: 366 (with P and the state in two
-// parts in the outputs of 16 bits 84 and 323, but 2^-15 of a term off, always towards zero).
-// Bound by matrix and vector instructions: of the two chunks that a CU works on at a time the 1904 products take 7.6 K
-// clocks; the rest is splitting into parts, decays and LDS reads.
+// 4096 tokens, 32 heads of 128 x 128, bf16: 90 us (launches of 34, 12 and 51); 8 sequences of 30,208 tokens in all:
+// 364-382 (with P and the state in two parts in the outputs of 16 bits 84 and 323, but 2^-15 of a term off, always towards
+// zero). 4096 tokens in f16 113, in f32 173. Bound by matrix and vector instructions: the 1920 products of the two
+// chunks that a CU works on at a time take 7.7 K clocks; the rest is splitting into parts, decays and LDS reads.
 #pragma once
 
 #include "gdn_device.h"

@@ -11,8 +11,8 @@
 //  * tile_kernel -- M above kSkinnyRows: BM x BN outputs a workgroup through LDS,
 //    128 bytes of k (a stage) at a time, double buffered, with two or three more stages on
 //    their way in registers. Bound by the LDS: a stage of 256 x 256 moves 192 KB out of
-//    it and 64 KB in for 2048 clocks of products. 4096^3: 67 us, 2050 TOPS (a library's
-//    int8 product reaches 2078 at 8192^3); 8192 x 8192 x 2048: 152 us, where storing the
+//    it and 64 KB in for 2048 clocks of products. 4096^3: 67-69 us, 1980-2050 TOPS (a
+//    library's int8 product reaches 2078 at 8192^3); 8192 x 8192 x 2048: 148-160 us, where storing the
 //    128 MB of bf16 outputs adds about 20 us that no product covers.
 //  * skinny_kernel -- a few rows: bound by the weights, which stream through once
 //    (1 x 8192 x 2048: 4.7 us).

@@ -12,11 +12,13 @@
 // the next row's loads in flight while the current one is reduced. Vectors need no
 // alignment beyond the element's (the hardware splits them), so odd widths and
 // strides take the same path; a width's last hidden % 8 elements go one to a thread.
-// loop_kernel takes wider rows (and those of less than 8) in passes over memory.
+// loop_kernel takes wider rows (and those of less than 8) in passes over memory, an element to a lane.
 // Sums and maxima are f32, in a fixed order: lanes, DPP tree, waves.
-// 8192 x 4096 bf16, residual in and out, 16- and 8-bit rows out: 57 us, 5.3 TB/s (a large
-// copy reaches 5.0). 1537 x 5003 f16: 9.1 us, 3.4 TB/s; 64 x 2048: 3.3 us, a launch and
-// one round trip to memory.
+// 8192 x 4096 bf16, residual in and out, 16- and 8-bit rows out: 56-58 us, 5.2 TB/s (a large
+// copy reaches 5.0). 1537 x 5003 f16: 9.3-9.8 us, 3.1-3.3 TB/s; 64 x 2048: 3.5 us, a launch and
+// one round trip to memory. loop_kernel, 2048 x 20480 bf16 with residual and 8-bit rows: 358 us,
+// 0.8 TB/s: bound by its single-element loads and their conversions, three times over the row. It is kept
+// that simple because the widths of model layers are row_kernel's.
 
 #include "gdn_device.h"
 #include "gdn_ops.h"
