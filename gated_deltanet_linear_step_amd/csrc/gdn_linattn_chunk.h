@@ -145,12 +145,13 @@ __device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&out)[PARTS]
     }
 }
 
+// The value of parts, from the last on: the first two alone may be a rounding above f32's largest number.
 template <int PARTS>
 __device__ __forceinline__ float join(const bf16x8 (&p)[PARTS], int e)
 {
-    float x = (float)p[0][e];
+    float x = (float)p[PARTS - 1][e];
 #pragma unroll
-    for (int s = 1; s < PARTS; ++s)
+    for (int s = PARTS - 2; s >= 0; --s)
         x += (float)p[s][e];
     return x;
 }

@@ -77,3 +77,22 @@ def test_16_bit_outputs_are_the_f32_ones_rounded(dk, dv, dtype):
     for out_dtype in (B16, F16):
         out, state16, _ = run_prefill(c, lens, Hk, Hv, dk, dv, ops.MAP_TILED, "rate", out_dtype)
         assert torch.equal(out, wide.to(out_dtype)) and torch.equal(state, state16)
+
+
+@pytest.mark.parametrize("dtype", [B16, F32])
+@pytest.mark.parametrize("power", [127, -100])
+def test_values_near_the_ends_of_f32(dtype, power):
+    """v and the state up to f32's largest numbers (no part of an operand may overflow), and far below 1."""
+    Hk, Hv, d, lens = 1, 2, 64, [130, 20]
+    gen = torch.Generator().manual_seed(9)
+    c = make(sum(lens), Hk, Hv, d, d, dtype, 9, slots=2)
+    q, k, v = (x.float() for x in views(c["mixed"], Hk, Hv, d, d))
+    sign = torch.randint(0, 2, v.shape, generator=gen) * 2 - 1
+    top = 2.0 ** power * (2 - torch.rand(v.shape, generator=gen) * 2.0 ** -9)  # up to the largest number
+    top[torch.rand(v.shape, generator=gen) < 0.2] = 2.0 ** power
+    c["mixed"] = torch.cat([q * 2.0 ** -10, k * 2.0 ** -8, sign * torch.clamp(top, max=torch.finfo(dtype).max)], 1).to(dtype)
+    assert torch.isfinite(c["mixed"].float()).all()
+    c["state"] = c["state"].sign() * 2.0 ** (power - 4) * (1 + torch.rand(c["state"].shape, generator=gen))
+    for out_dtype in (F32, B16):
+        out, state, cu = run_prefill(c, lens, Hk, Hv, d, d, ops.MAP_GROUPED, "token", out_dtype)
+        check_rows(c, lens, Hk, d, out, state, cu)
