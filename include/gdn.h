@@ -316,7 +316,9 @@ gdn_status gdn_prefill_chunked_noalloc(const gdn_dims *dims, int32_t num_seqs,
  *          f32; without it in->g [tokens][Hv] f32. Both 4-byte aligned. The other
  *          gate fields, z and norm_weight are ignored.
  *
- * -inf stands for exp(g) = 0: the state is forgotten. A NaN or infinity in q, k, v or
+ * -inf stands for exp(g) = 0: the state is forgotten. Log decays above 0 let the state
+ * grow; in the prefill exp of their sum over any run of 64 tokens must stay finite, also
+ * where the state is 0. A NaN or infinity in q, k, v or
  * the state makes what the formula makes of it not finite, and nothing else (where the
  * formula has an infinity, the prefill may have a NaN; a later exp(g) = 0 does not clear
  * either).
