@@ -317,14 +317,14 @@ gdn_status gdn_prefill_chunked_noalloc(const gdn_dims *dims, int32_t num_seqs,
  *          gate fields, z and norm_weight are ignored.
  *
  * -inf stands for exp(g) = 0: the state is forgotten. Log decays above 0 let the state
- * grow; in the prefill exp of their sum over any run of 64 tokens must stay finite, also
- * where the state is 0. A NaN or infinity in q, k, v or
- * the state makes what the formula makes of it not finite, and nothing else (where the
- * formula has an infinity, the prefill may have a NaN; a later exp(g) = 0 does not clear
- * either).
+ * grow; in the prefill exp of their sum over any run of a sequence's tokens must stay
+ * finite, also where the state is 0.
+ * A NaN or infinity in q, k, v or the state makes what the formula makes of it not
+ * finite, and nothing else (where the formula has an infinity, the prefill may have a
+ * NaN; a later exp(g) = 0 does not clear either).
  * Sums are f32 or more exact, whatever the output's type (of values below 2^-109 the
- * prefill may leave out what lies below 2^-133). A call without tokens does nothing, whatever its
- * per-token pointers.
+ * prefill may leave out what lies below 2^-133). A call without tokens does nothing,
+ * whatever its per-token pointers.
  * ------------------------------------------------------------------------- */
 
 /* gdn_linattn_decode_step -- B sequences of T tokens each; arguments, slots and
