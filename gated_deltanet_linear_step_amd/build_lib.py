@@ -18,7 +18,8 @@ LIB = os.path.join(HERE, "libgdn.so")
 SOURCES = ["gdn_api.cpp", "gdn_conv.hip", "gdn_decode.hip", "gdn_prefill.hip",
            "gdn_prefill_generic.hip", "gdn_linattn.hip",
            "gdn_linattn_bf16.hip", "gdn_linattn_f16.hip", "gdn_linattn_f32.hip", "gdn_norm.hip",
-           "gdn_matmul.hip"]
+           "gdn_matmul.hip", "gdn_attn_api.cpp", "gdn_rope.hip", "gdn_pages.hip", "gdn_attn.hip",
+           "gdn_attn_bf16.hip", "gdn_attn_f16.hip"]
 ARCH = os.environ.get("GDN_OFFLOAD_ARCH", "gfx950")
 
 

@@ -13,21 +13,15 @@
 #include <limits>
 #include <mutex>
 
+#include "gdn_checks.h"
 #include "gdn_ops.h"
 
 namespace {
 
+using namespace gdn::checks;
+
 constexpr uint32_t kPrefillFlags = GDN_L2NORM_QK | GDN_RAW_GATES | GDN_GATED_NORM;
 constexpr uint32_t kDecodeFlags = kPrefillFlags | GDN_STREAM_STATE;
-constexpr int64_t kI32Max = std::numeric_limits<int32_t>::max();
-
-bool dtype_ok(int32_t dt) { return dt == GDN_F32 || dt == GDN_F16 || dt == GDN_BF16; }
-int64_t dtype_size(int32_t dt) { return dt == GDN_F32 ? 4 : 2; }
-
-bool aligned(const void *p, int64_t bytes)
-{
-    return (reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(bytes)) == 0;
-}
 
 // Checks shared by the decode step and the prefill: dims, flags and the inputs
 // the flags require. On success fills the kernel-side copies.
@@ -118,29 +112,6 @@ gdn_status check_common(const gdn_dims *d, const gdn_inputs *in, int32_t out_dty
     ai.z = in->z;
     ai.z_dt = in->z_dtype;
     ai.norm_w = in->norm_weight;
-    return GDN_OK;
-}
-
-gdn_status launch_status(hipError_t e) { return e == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH; }
-
-// Validates host cu_seqlens; fills the chunk counts (chunks of `clen` tokens) the
-// prefill grid needs.
-gdn_status check_cu(const int32_t *cu, int32_t n, int32_t total, int clen, int64_t *chunks,
-                    int64_t *max_chunks)
-{
-    if (cu[0] != 0 || cu[n] != total)
-        return GDN_ERR_SHAPE;
-    int64_t c = 0, mx = 0;
-    for (int32_t i = 0; i < n; ++i) {
-        if (cu[i + 1] < cu[i])
-            return GDN_ERR_SHAPE;
-        const int64_t ci = ((int64_t)cu[i + 1] - cu[i] + clen - 1) / clen;
-        c += ci;
-        if (ci > mx)
-            mx = ci;
-    }
-    *chunks = c;
-    *max_chunks = mx;
     return GDN_OK;
 }
 

@@ -1,0 +1,107 @@
+// gdn_attn.h -- kernel parameter blocks and launchers of the softmax attention layer's operators: rotary positions,
+// attention over prompts and in decode steps, and the pages of their cache.
+#pragma once
+
+#include "gdn_kernels.h"
+
+namespace gdn {
+
+// Rotary positions (gdn_rope.hip). Strides in elements.
+struct RopeParams {
+    int tokens, Hq, Hkv, D, rot, layout, dt;
+    float magnitude;
+    const int32_t *positions;
+    const double *w;
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    void *q_out, *k_out, *k_pages, *v_pages;  // NULL: not stored
+    int64_t q_out_stride, k_out_stride, page_stride;
+    int64_t num_slots;
+    int page_shift;
+    const int32_t *slots;
+};
+hipError_t launch_rope(const RopeParams &p, hipStream_t s);
+
+// Keys and values of an attention call: packed rows, or pools of pages [Hkv][page size][D].
+struct KvSource {
+    const void *k, *v;
+    int64_t k_stride, v_stride;  // elements from row to row, or from page to page
+    int page_shift, num_pages;   // log2 of the page size; page_shift < 0: packed rows
+    const int32_t *table;
+    int64_t table_stride;
+};
+
+// What the attention kernels share. Partial results go to `part` where a query's keys are
+// split: [token][head][slot] rows of D f32, with (maximum, sum) pairs in `stat`.
+struct AttnParams {
+    int Hq, Hkv, D, dt;
+    float scale;
+    const void *q;
+    int64_t q_stride;
+    void *out;
+    int64_t out_stride;
+    float *lse;
+    KvSource kv;
+    float *part;
+    float2 *stat;
+    int slots;  // partial results of a query; 0: the outputs are written at once
+};
+
+// Blocks of queries against runs of keys (gdn_attn_prefill.hip). Sequences: packed and causal by cu_q and cu_k (device);
+// or, cu_q NULL, N of T queries each, causal against lens[s] keys of table row s (lens on the device, at most max_keys
+// count), or, lens NULL too, N = 1 against max_keys keys that every query sees.
+struct AttnPrefillParams {
+    AttnParams a;
+    int N, T, total;  // sequences, queries of each without cu_q, queries in all
+    const int32_t *cu_q, *cu_k, *lens;
+    int max_keys;
+    int splits, first_slot;  // runs of keys of a block of queries, and the slot of the first run
+};
+bool attn_supported(int D);
+// Runs of keys that a call is split into
+int attn_prefill_splits(int Hq, int Hkv, int64_t total, int64_t max_keys);
+// Workgroups for each run of keys
+int64_t attn_prefill_blocks(int Hq, int Hkv, int N, int64_t total, bool packed);
+hipError_t launch_attn_prefill(const AttnPrefillParams &p, hipStream_t s);
+hipError_t launch_attn_prefill_bf16(const AttnPrefillParams &p, unsigned grid, hipStream_t s);
+hipError_t launch_attn_prefill_f16(const AttnPrefillParams &p, unsigned grid, hipStream_t s);
+
+// A few queries of each sequence against its own pages (gdn_attn_decode.hip).
+struct AttnDecodeParams {
+    AttnParams a;
+    int B, T;
+    const int32_t *lens;
+    int max_len;
+    int splits, split_keys, first_slot;  // runs of split_keys keys each
+};
+int64_t attn_decode_blocks(int Hq, int Hkv, int D, int B, int T);  // workgroups for each run of keys
+void attn_decode_splits(int Hq, int Hkv, int D, int B, int T, int max_len, int *splits, int *split_keys);
+hipError_t launch_attn_decode(const AttnDecodeParams &p, hipStream_t s);
+
+// Joins the partial results of `rows` rows (queries times heads) into outputs.
+hipError_t launch_attn_join(const AttnParams &p, int64_t rows, hipStream_t s);
+
+// Pages of a cache (gdn_pages.hip).
+struct PageParams {
+    int32_t *table;
+    int64_t table_stride;
+    int rows, width;
+    int32_t *refs;
+    int num_pages, page_size;
+    unsigned char *data;
+    int num_planes;
+    int64_t plane_stride, page_stride, page_bytes;
+    int n;
+    const int32_t *row, *src, *len;  // requests: rows (fork: dst), fork's sources, lengths or entries to keep
+    int32_t *status;
+    int32_t *page_map, *used;
+    int32_t *workspace;
+};
+constexpr int kPageRequests = 1024;
+size_t pages_workspace_bytes(int num_pages);
+hipError_t launch_pages_free(const PageParams &p, hipStream_t s);
+hipError_t launch_pages_reserve(const PageParams &p, hipStream_t s);
+hipError_t launch_pages_fork(const PageParams &p, hipStream_t s);
+hipError_t launch_pages_compact(const PageParams &p, hipStream_t s);
+
+}  // namespace gdn

@@ -1,0 +1,98 @@
+// gdn_attn_device.h -- what the attention kernels of gfx950 share: 16-bit types and their matrix instructions,
+// transposing LDS reads, 16-byte copies to the LDS, page lookups and the softmax in base 2.
+#pragma once
+
+#include "gdn_device.h"
+#include "gdn_attn.h"
+
+namespace gdn {
+namespace attn {
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) void lds_void;
+
+// exp2 of a masked score, and the running maximum before any key
+constexpr float kNone = -__builtin_inff();
+
+template <int DT>
+struct Type16;
+template <>
+struct Type16<DT_BF16> {
+    typedef __bf16 T8 __attribute__((ext_vector_type(8)));
+    typedef __bf16 T2 __attribute__((ext_vector_type(2)));
+    static constexpr uint32_t kExponents = 0x7f807f80u, kLow = 0x00800080u;
+    __device__ __forceinline__ static f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(T8, a), __builtin_bit_cast(T8, b), c, 0, 0, 0);
+    }
+    __device__ __forceinline__ static f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(T8, a), __builtin_bit_cast(T8, b), c, 0, 0, 0);
+    }
+};
+template <>
+struct Type16<DT_F16> {
+    typedef _Float16 T8 __attribute__((ext_vector_type(8)));
+    typedef _Float16 T2 __attribute__((ext_vector_type(2)));
+    static constexpr uint32_t kExponents = 0x7c007c00u, kLow = 0x04000400u;
+    __device__ __forceinline__ static f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(T8, a), __builtin_bit_cast(T8, b), c, 0, 0, 0);
+    }
+    __device__ __forceinline__ static f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(T8, a), __builtin_bit_cast(T8, b), c, 0, 0, 0);
+    }
+};
+
+// Two f32 rounded to the type, lo's bits below hi's
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), typename Type16<DT>::T2));
+}
+
+// The top bits of the halves of w that are infinite or NaN
+template <int DT>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w)
+{
+    return ((w & Type16<DT>::kExponents) + Type16<DT>::kLow) & 0x80008000u;
+}
+
+// w with the halves that are infinite or NaN made 0
+template <int DT>
+__device__ __forceinline__ uint32_t finite_part(uint32_t w)
+{
+    const uint32_t bad = not_finite<DT>(w) >> 15;
+    return w & ~(bad * 0xffffu);
+}
+
+template <int DT>
+__device__ __forceinline__ float to_f32(uint32_t h)
+{
+    return DT == DT_BF16 ? bf16_bits_to_f32(h) : f16_bits_to_f32(h);
+}
+
+// Maximum and sum over a lane and the one 32 away (the swap leaves the lower half's values in one word, the upper half's
+// in the other)
+__device__ __forceinline__ float half_max(float x)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_sum(float x)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+__device__ __forceinline__ float exp2_f(float x) { return __builtin_amdgcn_exp2f(x); }
+
+}  // namespace attn
+}  // namespace gdn

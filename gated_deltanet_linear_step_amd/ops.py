@@ -26,13 +26,18 @@ MAP_GROUPED, MAP_TILED = 0, 1
 DECAY_LOG_RATE, DECAY_NEGATIVE_RATE = 0, 1
 L2NORM_QK, RAW_GATES, GATED_NORM, STREAM_STATE, HEAD_DECAY = 1, 2, 4, 8, 16
 CHUNK = 64
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_BANDS = 0, 1, 2, 3
 
 EXPORTED = ["gdn_conv_update", "gdn_decode_step", "gdn_prefill_workspace_bytes",
             "gdn_prefill_chunked", "gdn_status_string", "gdn_version", "gdn_decode_layer",
             "gdn_decode_launch_info", "gdn_prefill_launch_info", "gdn_prefill_chunked_noalloc",
             "gdn_linattn_decode_step", "gdn_linattn_prefill_workspace_bytes",
             "gdn_linattn_prefill_chunked", "gdn_add_rms_norm", "gdn_quant_matmul",
-            "gdn_quant_matmul_launch_info"]
+            "gdn_quant_matmul_launch_info", "gdn_rope", "gdn_rope_frequencies",
+            "gdn_attention_prefill_workspace_bytes", "gdn_attention_prefill",
+            "gdn_attention_decode_workspace_bytes", "gdn_attention_decode", "gdn_pages_free",
+            "gdn_pages_reserve", "gdn_pages_workspace_bytes", "gdn_pages_fork", "gdn_pages_compact"]
 
 _DT = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 _VP = ctypes.c_void_p
@@ -78,6 +83,34 @@ class NormArgs(ctypes.Structure):
                 ("weight", _VP), ("eps", ctypes.c_float), ("out_dtype", ctypes.c_int32),
                 ("out", _VP), ("out_stride", ctypes.c_int64),
                 ("out_q", _VP), ("out_q_stride", ctypes.c_int64), ("out_scale", _VP)]
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("tokens", "q_heads", "kv_heads", "head_dim", "rotary_dim",
+                                              "layout", "dtype")] + \
+        [("magnitude", ctypes.c_float), ("positions", _VP), ("inv_freq", _VP),
+         ("q", _VP), ("q_stride", ctypes.c_int64), ("q_out", _VP), ("q_out_stride", ctypes.c_int64),
+         ("k", _VP), ("k_stride", ctypes.c_int64), ("k_out", _VP), ("k_out_stride", ctypes.c_int64),
+         ("v", _VP), ("v_stride", ctypes.c_int64), ("k_pages", _VP), ("v_pages", _VP),
+         ("page_stride", ctypes.c_int64), ("num_pages", ctypes.c_int32),
+         ("page_size", ctypes.c_int32), ("slots", _VP)]
+
+
+class AttentionArgs(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("q", _VP), ("q_stride", ctypes.c_int64), ("out", _VP), ("out_stride", ctypes.c_int64),
+                ("lse", _VP), ("k", _VP), ("v", _VP), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("table", _VP), ("table_stride", ctypes.c_int64)]
+
+
+class PageArgs(ctypes.Structure):
+    _fields_ = [("table", _VP), ("table_stride", ctypes.c_int64), ("rows", ctypes.c_int32),
+                ("width", ctypes.c_int32), ("refs", _VP), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("data", _VP), ("num_planes", ctypes.c_int32),
+                ("plane_stride", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("page_bytes", ctypes.c_int64)]
 
 
 class GdnError(RuntimeError):
@@ -147,6 +180,25 @@ def load() -> ctypes.CDLL:
     lib.gdn_quant_matmul_launch_info.restype = ctypes.c_int
     lib.gdn_quant_matmul_launch_info.argtypes = [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                                  ctypes.POINTER(LaunchInfo)]
+    i32, ptr = ctypes.c_int32, ctypes.POINTER
+    for name, restype, argtypes in (
+            ("gdn_rope", ctypes.c_int, [ptr(RopeArgs), _VP]),
+            ("gdn_rope_frequencies", ctypes.c_int,
+             [i32, ctypes.c_double, i32] + [ctypes.c_double] * 4 + [_VP, _VP]),
+            ("gdn_attention_prefill_workspace_bytes", ctypes.c_size_t, [i32] * 5),
+            ("gdn_attention_prefill", ctypes.c_int,
+             [ptr(AttentionArgs), i32, _VP, _VP, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
+            ("gdn_attention_decode_workspace_bytes", ctypes.c_size_t, [i32] * 7),
+            ("gdn_attention_decode", ctypes.c_int,
+             [ptr(AttentionArgs), i32, i32, _VP, i32, _VP, i32, _VP, ctypes.c_size_t, _VP]),
+            ("gdn_pages_free", ctypes.c_int, [ptr(PageArgs), i32, _VP, _VP, _VP]),
+            ("gdn_pages_reserve", ctypes.c_int, [ptr(PageArgs), i32, _VP, _VP, _VP, _VP]),
+            ("gdn_pages_workspace_bytes", ctypes.c_size_t, [i32]),
+            ("gdn_pages_fork", ctypes.c_int,
+             [ptr(PageArgs), i32, _VP, _VP, _VP, _VP, _VP, ctypes.c_size_t, _VP]),
+            ("gdn_pages_compact", ctypes.c_int, [ptr(PageArgs), _VP, _VP, _VP, ctypes.c_size_t, _VP])):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = restype, argtypes
     _LIB = lib
     return lib
 
@@ -862,3 +914,389 @@ def quant_matmul(a, a_scale, w, w_scale, *, out=None, out_dtype=torch.bfloat16, 
             out = torch.empty((a.shape[0], w.shape[0]), dtype=out_dtype, device=a.device)
         prepare_quant_matmul(a, a_scale, w, w_scale, out).launch()
     return out
+
+
+# ---- softmax attention layers: rotary positions, attention, the pages of the cache ----
+
+def rope_frequencies(rotary_dim, theta=10000.0, *, scaling=ROPE_PLAIN, factor=1.0, original_length=0.0,
+                     beta_fast=32.0, beta_slow=1.0):
+    """The frequencies of gdn_rope_frequencies: (inv_freq [rotary_dim / 2] f64 on the host, magnitude)."""
+    inv_freq = torch.empty(max(int(rotary_dim) // 2, 1), dtype=torch.float64)
+    magnitude = ctypes.c_float()
+    st = load().gdn_rope_frequencies(rotary_dim, theta, scaling, factor, original_length, beta_fast,
+                                     beta_slow, ctypes.c_void_p(inv_freq.data_ptr()), ctypes.byref(magnitude))
+    _check(st, "gdn_rope_frequencies")
+    return inv_freq, magnitude.value
+
+
+def _i32(name, t, *shape):
+    """A contiguous int32 tensor of the shape; None in it is any size."""
+    if t.dtype != torch.int32 or t.dim() != len(shape) or not t.is_contiguous() or \
+            any(want is not None and n != want for n, want in zip(t.shape, shape)):
+        raise ValueError(f"{name} must be contiguous int32 {['any' if n is None else n for n in shape]}, "
+                         f"got {t.dtype} {list(t.shape)}")
+    return t
+
+
+def _head_rows(name, t, rows, heads, dim, dtype):
+    """Row stride of t [rows][heads][dim], whose rows may be strided."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or tuple(t.shape) != (rows, heads, dim):
+        raise ValueError(f"{name} must be [{rows}][{heads}][{dim}], got {list(t.shape)}")
+    if t.numel() > 0 and ((dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != dim)):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return t.stride(0) if rows > 1 else heads * dim
+
+
+def _page_pool(name, t, heads, dim, dtype):
+    """Page stride of the pool t [pages][heads][page_size][dim], whose pages may be strided."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 4 or t.shape[1] != heads or t.shape[3] != dim:
+        raise ValueError(f"{name} must be [pages][{heads}][page_size][{dim}], got {list(t.shape)}")
+    page = heads * t.shape[2] * dim
+    if t.numel() > 0 and not t[0].is_contiguous():
+        raise ValueError(f"{name}: a page must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else page
+
+
+def prepare_rope(positions, inv_freq, *, q=None, q_out=None, k=None, k_out=None, v=None, k_pages=None,
+                 v_pages=None, slots=None, layout=ROPE_HALF, magnitude=1.0, stream=None) -> DeviceCall:
+    """rope into the caller's buffers, checked and marshalled once: q_out and k_out like q and k (their
+    own buffers allowed), or for k and v page pools [pages][kv_heads][page_size][head_dim] with
+    slots [tokens] int32."""
+    device = _device_of(positions=positions, inv_freq=inv_freq, q=q, q_out=q_out, k=k, k_out=k_out, v=v,
+                        k_pages=k_pages, v_pages=v_pages, slots=slots)
+    given = q if q is not None else k
+    if given is None:
+        raise ValueError("give q, k or both")
+    if given.dim() != 3:
+        raise ValueError("q and k must be [tokens][heads][head_dim]")
+    tokens, _, dim = given.shape
+    _i32("positions", positions, tokens)
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be contiguous float64 [rotary_dim / 2]")
+    if magnitude == 0:
+        raise ValueError("magnitude must not be 0")
+    args = RopeArgs(tokens=tokens, head_dim=dim, rotary_dim=2 * inv_freq.numel(), layout=layout, dtype=_dt(given),
+                    magnitude=magnitude, positions=_ptr(positions), inv_freq=_ptr(inv_freq))
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        args.q_heads = q.shape[1]
+        args.q, args.q_stride = _ptr(q), _head_rows("q", q, tokens, args.q_heads, dim, given.dtype)
+        args.q_out, args.q_out_stride = _ptr(q_out), _head_rows("q_out", q_out, tokens, args.q_heads, dim, given.dtype)
+    paged = [t is not None for t in (k_pages, v_pages, slots, v)]
+    if any(paged) and (not all(paged) or k is None or k_out is not None):
+        raise ValueError("k_pages, v_pages, slots, k and v go together, without k_out")
+    if not any(paged) and (k is None) != (k_out is None):
+        raise ValueError("k goes to k_out or to pages")
+    if k is not None:
+        args.kv_heads = k.shape[1] if k.dim() == 3 else 0
+        args.k, args.k_stride = _ptr(k), _head_rows("k", k, tokens, args.kv_heads, dim, given.dtype)
+    if k_out is not None:
+        args.k_out, args.k_out_stride = _ptr(k_out), _head_rows("k_out", k_out, tokens, args.kv_heads, dim, given.dtype)
+    if k_pages is not None:
+        args.v, args.v_stride = _ptr(v), _head_rows("v", v, tokens, args.kv_heads, dim, given.dtype)
+        args.k_pages, args.v_pages = _ptr(k_pages), _ptr(v_pages)
+        args.page_stride = _page_pool("k_pages", k_pages, args.kv_heads, dim, given.dtype)
+        if _page_pool("v_pages", v_pages, args.kv_heads, dim, given.dtype) != args.page_stride or \
+                k_pages.shape != v_pages.shape:
+            raise ValueError("k_pages and v_pages must have one shape and stride")
+        args.num_pages, args.page_size = k_pages.shape[0], k_pages.shape[2]
+        args.slots = _ptr(_i32("slots", slots, tokens))
+    return DeviceCall(load().gdn_rope, (ctypes.byref(args), _RunOn(device, stream).handle), "gdn_rope",
+                      [args, positions, inv_freq, q, q_out, k, k_out, v, k_pages, v_pages, slots], device,
+                      (q_out, k_out))
+
+
+def rope(positions, inv_freq, *, q=None, k=None, v=None, k_pages=None, v_pages=None, slots=None,
+         layout=ROPE_HALF, magnitude=1.0, stream=None):
+    """One call of gdn_rope: turns the first 2 * len(inv_freq) elements of each head of q and k
+    [tokens][heads][head_dim] (views of a mixed row allowed) by their positions [tokens] int32. With
+    pages, k and v are stored in the slots and only q is returned; else new (q, k), None for one
+    not given."""
+    with _RunOn(_device_of(positions=positions), stream):
+        q_out = None if q is None else torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        k_out = None if k is None or k_pages is not None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        prepare_rope(positions, inv_freq, q=q, q_out=q_out, k=k, k_out=k_out, v=v, k_pages=k_pages,
+                     v_pages=v_pages, slots=slots, layout=layout, magnitude=magnitude).launch()
+    return q_out if k_pages is not None else (q_out, k_out)
+
+
+def _attention_args(q, k, v, out, lse, table, scale):
+    """AttentionArgs of queries q [rows][q_heads][head_dim] and packed rows or, with a table, page pools."""
+    if q.dim() != 3 or k.dim() != (3 if table is None else 4) or k.shape[-1] != q.shape[2]:
+        raise ValueError("q must be [rows][q_heads][head_dim], k and v [keys][kv_heads][head_dim] or "
+                         "[pages][kv_heads][page_size][head_dim] with a table")
+    rows, Hq, dim = q.shape
+    Hkv = k.shape[1]
+    args = AttentionArgs(q_heads=Hq, kv_heads=Hkv, head_dim=dim, dtype=_dt(q), scale=scale, q=_ptr(q),
+                         q_stride=_head_rows("q", q, rows, Hq, dim, q.dtype), out=_ptr(out),
+                         out_stride=_head_rows("out", out, rows, Hq, dim, q.dtype), k=_ptr(k), v=_ptr(v))
+    if lse is not None:
+        if lse.dtype != torch.float32 or not lse.is_contiguous() or tuple(lse.shape) != (rows, Hq):
+            raise ValueError(f"lse must be contiguous float32 [{rows}][{Hq}]")
+        args.lse = _ptr(lse)
+    if k.shape != v.shape:
+        raise ValueError("k and v must have one shape")
+    if table is None:
+        args.k_stride = _head_rows("k", k, k.shape[0], Hkv, dim, q.dtype)
+        args.v_stride = _head_rows("v", v, k.shape[0], Hkv, dim, q.dtype)
+    else:
+        args.k_stride = _page_pool("k", k, Hkv, dim, q.dtype)
+        args.v_stride = _page_pool("v", v, Hkv, dim, q.dtype)
+        args.num_pages, args.page_size = k.shape[0], k.shape[2]
+        if table.dtype != torch.int32 or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
+            raise ValueError("table must be int32 [sequences][entries] with contiguous rows")
+        args.table = _ptr(table)
+        args.table_stride = table.stride(0) if table.shape[0] > 1 else table.shape[1]
+        if args.table_stride < table.shape[1]:
+            raise ValueError("table: rows overlap")
+    return args
+
+
+def _workspace(workspace):
+    if workspace is None:
+        return None, 0
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return _ptr(workspace), workspace.numel() * workspace.element_size()
+
+
+def attention_prefill_workspace_bytes(*, Hq, Hkv, head_dim, num_seqs, total_tokens):
+    """Workspace gdn_attention_prefill needs for total_tokens queries."""
+    return int(load().gdn_attention_prefill_workspace_bytes(Hq, Hkv, head_dim, num_seqs, total_tokens))
+
+
+def prepare_attention_prefill(q, k, v, cu_q, cu_q_host, out, workspace, *, cu_k=None, cu_k_host=None,
+                              table=None, lse=None, scale=0.0, stream=None) -> DeviceCall:
+    """attention_prefill with its arguments checked and marshalled once: the offsets as int32 [N+1]
+    tensors on the GPU and on the host, the workspace a contiguous uint8 tensor (None where none is needed)."""
+    device = _device_of(q=q, k=k, v=v, cu_q=cu_q, out=out, workspace=workspace, cu_k=cu_k, table=table, lse=lse)
+    if (cu_k is None) != (cu_k_host is None):
+        raise ValueError("cu_k and cu_k_host go together")
+    for name, t, host in (("cu_q", cu_q, cu_q_host), ("cu_k", cu_k, cu_k_host)):
+        if t is None:
+            continue
+        _i32(name, t, None)
+        _i32(name + "_host", host, t.numel())
+        if host.device.type != "cpu" or t.numel() != cu_q.numel() or t.numel() < 1:
+            raise ValueError(f"{name}_host must hold {name}'s offsets on the host, one more than sequences")
+    args = _attention_args(q, k, v, out, lse, table, scale)
+    N = cu_q.numel() - 1
+    cu_keys = cu_q_host if cu_k_host is None else cu_k_host
+    if q.shape[0] < int(cu_q_host[-1]):
+        raise ValueError(f"q must hold {int(cu_q_host[-1])} rows")
+    if table is None and k.shape[0] < int(cu_keys[-1]):
+        raise ValueError(f"k and v must hold {int(cu_keys[-1])} rows")
+    if table is not None:
+        longest = int(cu_keys.diff().max()) if N > 0 else 0
+        if table.shape[0] != N or table.shape[1] * k.shape[2] < longest:
+            raise ValueError(f"table must hold {N} rows of pages for {longest} tokens")
+    ws, ws_bytes = _workspace(workspace)
+    call = (ctypes.byref(args), N, ctypes.c_void_p(cu_q_host.data_ptr()), _ptr(cu_q),
+            None if cu_k is None else ctypes.c_void_p(cu_k_host.data_ptr()), _ptr(cu_k), ws, ws_bytes,
+            _RunOn(device, stream).handle)
+    return DeviceCall(load().gdn_attention_prefill, call, "gdn_attention_prefill",
+                      [args, q, k, v, cu_q, cu_q_host, out, workspace, cu_k, cu_k_host, table, lse], device, out)
+
+
+def attention_prefill(q, k, v, cu_seqlens, *, cu_k=None, table=None, out=None, lse=None, scale=0.0,
+                      workspace=None, cu_seqlens_host=None, cu_k_host=None, stream=None):
+    """One call of gdn_attention_prefill: causal attention of packed prompts, q [tokens][q_heads][head_dim]
+    (f16 or bf16, views of a mixed row allowed), cu_seqlens integer [N+1] on either side. k and v are packed
+    rows [keys][kv_heads][head_dim], or page pools [pages][kv_heads][page_size][head_dim] with a table
+    [N][entries] int32; cu_k are the offsets of the keys where they are not those of the queries (the
+    queries are then the last ones of the keys). lse [tokens][q_heads] f32 receives the log-sums. Returns
+    out [tokens][q_heads][head_dim]."""
+    with _RunOn(_device_of(q=q), stream):
+        host = _cu_host(cu_seqlens if cu_seqlens_host is None else cu_seqlens_host)
+        dev = _cu_device(cu_seqlens, q.device)
+        k_host = k_dev = None
+        if cu_k is not None:
+            k_host = _cu_host(cu_k if cu_k_host is None else cu_k_host)
+            k_dev = _cu_device(cu_k, q.device)
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if workspace is None and q.dim() == 3 and k.dim() > 2:
+            need = attention_prefill_workspace_bytes(Hq=q.shape[1], Hkv=k.shape[1], head_dim=q.shape[2],
+                                                     num_seqs=host.numel() - 1, total_tokens=int(host[-1]))
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        prepare_attention_prefill(q, k, v, dev, host, out, workspace, cu_k=k_dev, cu_k_host=k_host, table=table,
+                                  lse=lse, scale=scale).launch()
+    return out
+
+
+def attention_decode_workspace_bytes(*, Hq, Hkv, head_dim, batch, tokens_per_seq=1, max_len, prefix_len=0):
+    """Workspace gdn_attention_decode needs."""
+    return int(load().gdn_attention_decode_workspace_bytes(Hq, Hkv, head_dim, batch, tokens_per_seq, max_len,
+                                                           prefix_len))
+
+
+def prepare_attention_decode(q, k_pages, v_pages, table, lens, out, workspace, *, batch, max_len,
+                             tokens_per_seq=1, prefix_table=None, prefix_len=0, lse=None, scale=0.0,
+                             stream=None) -> DeviceCall:
+    """attention_decode with its arguments checked and marshalled once; the workspace a contiguous uint8
+    tensor (None where none is needed). lens and the tables are read when the call runs."""
+    device = _device_of(q=q, k_pages=k_pages, v_pages=v_pages, table=table, lens=lens, out=out,
+                        workspace=workspace, prefix_table=prefix_table, lse=lse)
+    if table is None:
+        raise ValueError("the keys of a decode step are on pages: give a table")
+    args = _attention_args(q, k_pages, v_pages, out, lse, table, scale)
+    if q.shape[0] != batch * tokens_per_seq:
+        raise ValueError(f"q must hold {batch * tokens_per_seq} rows")
+    _i32("lens", lens, batch)
+    if table.shape[0] < batch or table.shape[1] * k_pages.shape[2] < max_len:
+        raise ValueError(f"table must hold {batch} rows of pages for {max_len} tokens")
+    if (prefix_table is None) != (prefix_len == 0):
+        raise ValueError("prefix_table and prefix_len go together")
+    if prefix_table is not None:
+        _i32("prefix_table", prefix_table, None)
+        if prefix_table.numel() * k_pages.shape[2] < prefix_len:
+            raise ValueError(f"prefix_table must hold pages for {prefix_len} tokens")
+    ws, ws_bytes = _workspace(workspace)
+    call = (ctypes.byref(args), batch, tokens_per_seq, _ptr(lens), max_len, _ptr(prefix_table), prefix_len, ws,
+            ws_bytes, _RunOn(device, stream).handle)
+    return DeviceCall(load().gdn_attention_decode, call, "gdn_attention_decode",
+                      [args, q, k_pages, v_pages, table, lens, out, workspace, prefix_table, lse], device, out)
+
+
+def attention_decode(q, k_pages, v_pages, table, lens, *, batch, max_len, tokens_per_seq=1, prefix_table=None,
+                     prefix_len=0, out=None, lse=None, scale=0.0, workspace=None, stream=None):
+    """One call of gdn_attention_decode: tokens_per_seq new queries of each sequence, q [B*T][q_heads]
+    [head_dim], against a prefix that the batch shares (prefix_len tokens on the pages prefix_table) and each
+    sequence's own lens[b] tokens (int32, on the GPU, the new ones among them, at most max_len) on the pages
+    table[b]. Returns out [B*T][q_heads][head_dim]."""
+    with _RunOn(_device_of(q=q), stream):
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if workspace is None and q.dim() == 3 and k_pages.dim() == 4:
+            need = attention_decode_workspace_bytes(Hq=q.shape[1], Hkv=k_pages.shape[1], head_dim=q.shape[2],
+                                                    batch=batch, tokens_per_seq=tokens_per_seq, max_len=max_len,
+                                                    prefix_len=prefix_len)
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        prepare_attention_decode(q, k_pages, v_pages, table, lens, out, workspace, batch=batch, max_len=max_len,
+                                 tokens_per_seq=tokens_per_seq, prefix_table=prefix_table, prefix_len=prefix_len,
+                                 lse=lse, scale=scale).launch()
+    return out
+
+
+def _page_args(table, refs, page_size=1, pool=None):
+    if table.dtype != torch.int32 or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1) or \
+            (table.shape[0] > 1 and table.stride(0) < table.shape[1]):
+        raise ValueError("table must be int32 [rows][entries] with contiguous rows")
+    _i32("refs", refs, None)
+    args = PageArgs(table=_ptr(table), table_stride=table.stride(0) if table.shape[0] > 1 else table.shape[1],
+                    rows=table.shape[0], width=table.shape[1], refs=_ptr(refs), num_pages=refs.numel(),
+                    page_size=page_size)
+    if pool is not None:
+        if pool.dim() < 2 or pool.shape[1] != refs.numel():
+            raise ValueError(f"pool must be [planes][{refs.numel()}][...]")
+        size = pool.element_size()
+        args.data, args.num_planes = _ptr(pool), pool.shape[0]
+        page = 1
+        for n in pool.shape[2:]:
+            page *= n
+        args.page_bytes = page * size
+        args.page_stride = pool.stride(1) * size if pool.shape[1] > 1 else args.page_bytes
+        args.plane_stride = pool.stride(0) * size if pool.shape[0] > 1 else pool.shape[1] * args.page_stride
+        if pool.numel() > 0 and not pool[0, 0].is_contiguous():
+            raise ValueError("pool: a page must be contiguous")
+    return args
+
+
+def prepare_pages_free(table, refs, rows, *, keep=None, stream=None) -> DeviceCall:
+    """pages_free with its arguments checked and marshalled once."""
+    device = _device_of(table=table, refs=refs, rows=rows, keep=keep)
+    args = _page_args(table, refs)
+    n = _i32("rows", rows, None).numel()
+    if keep is not None:
+        _i32("keep", keep, n)
+    return DeviceCall(load().gdn_pages_free, (ctypes.byref(args), n, _ptr(rows), _ptr(keep),
+                                              _RunOn(device, stream).handle), "gdn_pages_free",
+                      [args, table, refs, rows, keep], device, None)
+
+
+def pages_free(table, refs, rows, *, keep=None, stream=None):
+    """One call of gdn_pages_free: the rows rows [n] int32 of table [rows][entries] int32 give their pages back,
+    all or those from entry keep[i] on; refs [pages] int32."""
+    with _RunOn(_device_of(table=table), stream):
+        prepare_pages_free(table, refs, rows, keep=keep).launch()
+
+
+def prepare_pages_reserve(table, refs, rows, lens, status, *, page_size, stream=None) -> DeviceCall:
+    """pages_reserve into the caller's status [n] int32, checked and marshalled once."""
+    device = _device_of(table=table, refs=refs, rows=rows, lens=lens, status=status)
+    args = _page_args(table, refs, page_size)
+    n = _i32("rows", rows, None).numel()
+    _i32("lens", lens, n)
+    _i32("status", status, n)
+    return DeviceCall(load().gdn_pages_reserve, (ctypes.byref(args), n, _ptr(rows), _ptr(lens), _ptr(status),
+                                                 _RunOn(device, stream).handle), "gdn_pages_reserve",
+                      [args, table, refs, rows, lens, status], device, status)
+
+
+def pages_reserve(table, refs, rows, lens, *, page_size, stream=None):
+    """One call of gdn_pages_reserve: row rows[i] gets pages for its first lens[i] tokens where it has none.
+    Returns status [n] int32: 0 done, 1 too few pages, 2 refused."""
+    with _RunOn(_device_of(table=table), stream):
+        status = torch.empty(rows.shape, dtype=torch.int32, device=table.device)
+        prepare_pages_reserve(table, refs, rows, lens, status, page_size=page_size).launch()
+    return status
+
+
+def pages_workspace_bytes(num_pages):
+    """Workspace gdn_pages_fork and gdn_pages_compact need."""
+    return int(load().gdn_pages_workspace_bytes(num_pages))
+
+
+def prepare_pages_fork(pool, table, refs, src, dst, lens, status, workspace, *, page_size,
+                       stream=None) -> DeviceCall:
+    """pages_fork into the caller's status [n] int32, checked and marshalled once."""
+    device = _device_of(pool=pool, table=table, refs=refs, src=src, dst=dst, lens=lens, status=status,
+                        workspace=workspace)
+    args = _page_args(table, refs, page_size, pool)
+    n = _i32("src", src, None).numel()
+    for name, t in (("dst", dst), ("lens", lens), ("status", status)):
+        _i32(name, t, n)
+    ws, ws_bytes = _workspace(workspace)
+    return DeviceCall(load().gdn_pages_fork, (ctypes.byref(args), n, _ptr(src), _ptr(dst), _ptr(lens), _ptr(status),
+                                              ws, ws_bytes, _RunOn(device, stream).handle), "gdn_pages_fork",
+                      [args, pool, table, refs, src, dst, lens, status, workspace], device, status)
+
+
+def pages_fork(pool, table, refs, src, dst, lens, *, page_size, workspace=None, stream=None):
+    """One call of gdn_pages_fork: the empty row dst[i] becomes the first lens[i] tokens of row src[i], full pages
+    shared, a last one copied on every plane of pool [planes][pages][...]. Returns status [n] int32."""
+    with _RunOn(_device_of(table=table), stream):
+        status = torch.empty(src.shape, dtype=torch.int32, device=table.device)
+        if workspace is None:
+            workspace = torch.empty(pages_workspace_bytes(refs.numel()), dtype=torch.uint8, device=table.device)
+        prepare_pages_fork(pool, table, refs, src, dst, lens, status, workspace, page_size=page_size).launch()
+    return status
+
+
+def prepare_pages_compact(pool, table, refs, page_map, used, workspace, *, stream=None) -> DeviceCall:
+    """pages_compact into the caller's page_map [pages] and used [1] int32, checked and marshalled once."""
+    device = _device_of(pool=pool, table=table, refs=refs, page_map=page_map, used=used, workspace=workspace)
+    args = _page_args(table, refs, 1, pool)
+    _i32("page_map", page_map, refs.numel())
+    _i32("used", used, 1)
+    ws, ws_bytes = _workspace(workspace)
+    return DeviceCall(load().gdn_pages_compact, (ctypes.byref(args), _ptr(page_map), _ptr(used), ws, ws_bytes,
+                                                 _RunOn(device, stream).handle), "gdn_pages_compact",
+                      [args, pool, table, refs, page_map, used, workspace], device, (page_map, used))
+
+
+def pages_compact(pool, table, refs, *, workspace=None, stream=None):
+    """One call of gdn_pages_compact: the pages in use move to the front of pool [planes][pages][...], table and
+    refs follow. Returns (page_map [pages] int32: where each page went, used [1] int32: how many are in use)."""
+    with _RunOn(_device_of(table=table), stream):
+        page_map = torch.empty(refs.shape, dtype=torch.int32, device=table.device)
+        used = torch.empty(1, dtype=torch.int32, device=table.device)
+        if workspace is None:
+            workspace = torch.empty(pages_workspace_bytes(refs.numel()), dtype=torch.uint8, device=table.device)
+        prepare_pages_compact(pool, table, refs, page_map, used, workspace).launch()
+    return page_map, used

@@ -16,7 +16,9 @@
  * Beside it: linear attention with a decay per head (the same state without the
  * delta rule), and what feeds a layer in 8 bits -- the RMS norm with the residual's
  * addition and an 8-bit output, and the product of 8-bit integers that projects
- * it to the mixed q, k, v row.
+ * it to the mixed q, k, v row. And the softmax attention layers that stand between such
+ * layers: rotary positions, attention over packed prompts and in decode steps over a
+ * paged cache with a shared prefix, and the operations on that cache's pages.
  *
  * Conventions shared by every entry point
  *  - Every array pointer is a DEVICE pointer unless its comment says "host".
@@ -427,6 +429,231 @@ gdn_status gdn_quant_matmul(int32_t M, int32_t N, int32_t K, const int8_t *a, in
                             const float *a_scale, const int8_t *w, int64_t w_stride,
                             const float *w_scale, int32_t out_dtype, void *out,
                             int64_t out_stride, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * gdn_rope -- rotary positions: a pair (a, b) of a head's first rotary_dim elements, at
+ * position p and with frequency w of the pair, becomes
+ *
+ *     (a c - b s, b c + a s),   c = magnitude cos(p w),   s = magnitude sin(p w)
+ *
+ * and the head's other elements stay. The angle is formed and reduced in 64 bits, the
+ * pair is turned in f32, each output is rounded once. q, k, or both; with page pools
+ * the turned k and v go to the cache's pages instead of rows.
+ *
+ *   tokens         >= 0 rows
+ *   q_heads, kv_heads, head_dim   head_dim 2 to 1024; rotary_dim even, 2 to head_dim
+ *   layout         GDN_ROPE_HALF pairs (i, i + rotary_dim / 2), GDN_ROPE_INTERLEAVED
+ *                  (2 i, 2 i + 1)
+ *   dtype          of every row and page
+ *   positions      [tokens] int32, from 0 on (any other value turns as the formula has it)
+ *   inv_freq       [rotary_dim / 2] f64, radians a token, finite
+ *   magnitude      0 selects 1
+ *   q, q_out       rows of q_heads * head_dim elements with strides q_stride, q_out_stride;
+ *                  q_out may be q itself (same pointer and stride), else may not overlap
+ *                  an input. Both NULL: no q.
+ *   k, k_out       the same for k (kv_heads); k_out only without pages. k NULL: no k.
+ *   k_pages, v_pages  NULL, or page pools (gdn_attention_args): row t of the turned k and
+ *                  of v (rows of v_stride) goes to slot slots[t] = page * page_size + token
+ *                  in page. A slot outside [0, num_pages * page_size) is not stored. Slots
+ *                  of a call differ; of two tokens with one slot either may be stored.
+ *   page_size      a power of two from 16 to 1024; num_pages * page_size below 2^31
+ *   page_stride    elements from page to page, >= kv_heads * page_size * head_dim
+ * Pointers are aligned to their element (positions, slots 4, inv_freq 8 bytes).
+ * Errors: NULL, SHAPE, UNSUPPORTED (dtype, layout, head or rotary dims, page size),
+ * OVERFLOW, ALIGN, LAUNCH.
+ * ------------------------------------------------------------------------- */
+typedef enum gdn_rope_layout { GDN_ROPE_HALF = 0, GDN_ROPE_INTERLEAVED = 1 } gdn_rope_layout;
+typedef struct gdn_rope_args {
+    int32_t tokens, q_heads, kv_heads, head_dim, rotary_dim;
+    int32_t layout, dtype;
+    float magnitude;
+    const int32_t *positions;
+    const double *inv_freq;
+    const void *q;
+    int64_t q_stride;
+    void *q_out;
+    int64_t q_out_stride;
+    const void *k;
+    int64_t k_stride;
+    void *k_out;
+    int64_t k_out_stride;
+    const void *v;
+    int64_t v_stride;
+    void *k_pages, *v_pages;
+    int64_t page_stride;
+    int32_t num_pages, page_size;
+    const int32_t *slots;
+} gdn_rope_args;
+gdn_status gdn_rope(const gdn_rope_args *args, void *stream);
+
+/* gdn_rope_frequencies -- fills inv_freq (HOST, [rotary_dim / 2] f64) and magnitude (HOST)
+ * for gdn_rope: theta^(-2 i / rotary_dim), stretched for contexts `factor` (>= 1) times as long:
+ *   GDN_ROPE_PLAIN    as it is
+ *   GDN_ROPE_LINEAR   divided by factor
+ *   GDN_ROPE_BASE     theta times factor^(r / (r - 2)) (r = rotary_dim >= 4): the slowest pair
+ *                     is divided by factor, the fastest stays
+ *   GDN_ROPE_BANDS    pairs that turn beta_fast times or more in original_length tokens stay,
+ *                     those that turn beta_slow times or less are divided by factor, between
+ *                     them the two are mixed in proportion to the pair's index; magnitude
+ *                     0.1 ln(factor) + 1 (1 with the other kinds)
+ * The index at which a pair turns n times is r ln(original_length / (2 pi n)) / (2 ln theta),
+ * rounded down for beta_fast and up for beta_slow and kept within [0, r - 1].
+ * Makes no HIP call. Errors: NULL, SHAPE (theta <= 1, factor < 1, original_length < 1,
+ * 0 < beta_slow <= beta_fast not held), UNSUPPORTED (kind, rotary_dim). */
+typedef enum gdn_rope_scaling {
+    GDN_ROPE_PLAIN = 0,
+    GDN_ROPE_LINEAR = 1,
+    GDN_ROPE_BASE = 2,
+    GDN_ROPE_BANDS = 3
+} gdn_rope_scaling;
+gdn_status gdn_rope_frequencies(int32_t rotary_dim, double theta, int32_t scaling, double factor,
+                                double original_length, double beta_fast, double beta_slow,
+                                double *inv_freq, float *magnitude);
+
+/* ---------------------------------------------------------------------------
+ * Softmax attention of grouped heads: query head h reads key head h / (q_heads / kv_heads),
+ *
+ *     o_i = sum_j p_ij v_j,   p_ij = exp(scale q_i k_j) / sum_j exp(scale q_i k_j)
+ *
+ * over the keys j that query i sees. Scores, their maximum and sum and the outputs are
+ * f32 sums; p enters the product with v rounded to the 16 bits of v (relative to the
+ * row's largest), and o is rounded once.
+ * A query that sees no key, or whose scores are all -inf, has o = 0 and lse = -inf.
+ * Infinities and NaN in keys, values or queries that a query does not see do not reach
+ * it; in those it sees they make what the formula makes of them not finite (where that
+ * is an infinity, a NaN may stand).
+ *
+ *   q_heads, kv_heads   q_heads a multiple of kv_heads, both >= 1
+ *   head_dim       64, 96, 128 or 256
+ *   dtype          of q, k, v and out: f16 or bf16
+ *   scale          0 selects head_dim^(-1/2)
+ *   q, out         rows of q_heads * head_dim elements with strides q_stride, out_stride
+ *   lse            NULL, or [rows][q_heads] f32: ln sum_j exp(scale q_i k_j)
+ *   k, v           page_size 0: packed rows of kv_heads * head_dim elements, k_stride and
+ *                  v_stride elements apart. Else pools of pages [kv_heads][page_size]
+ *                  [head_dim], k_stride and v_stride elements from page to page
+ *   page_size      0, or a power of two from 16 to 1024
+ *   num_pages      pages of the pools
+ *   table          [sequences][table_stride] int32: page of token n of a sequence is entry
+ *                  n / page_size. Keys of an entry outside [0, num_pages) are not seen.
+ * q, k, v, out and their strides are multiples of 16 bytes, lse, table 4 bytes.
+ * out may not overlap an input.
+ * ------------------------------------------------------------------------- */
+typedef struct gdn_attention_args {
+    int32_t q_heads, kv_heads, head_dim, dtype;
+    float scale;
+    const void *q;
+    int64_t q_stride;
+    void *out;
+    int64_t out_stride;
+    float *lse;
+    const void *k, *v;
+    int64_t k_stride, v_stride;
+    int32_t page_size, num_pages;
+    const int32_t *table;
+    int64_t table_stride;
+} gdn_attention_args;
+
+/* gdn_attention_prefill -- prompts packed one after another, causal: sequence s has the
+ * queries [cu_q[s], cu_q[s + 1]) and cu_k[s + 1] - cu_k[s] keys, of which its last query
+ * sees all, the one before all but one, and so on. Packed keys are the rows
+ * [cu_k[s], cu_k[s + 1]); on pages they are the first tokens of table row s. More queries
+ * than keys: the first ones see none.
+ *   cu_q, cu_k     [num_seqs + 1] int32, ascending from 0, on the host and on the device
+ *                  with the same values; both cu_k NULL: cu_q
+ *   workspace      of the bytes that the query gives for these counts, aligned to 256; NULL
+ *                  where it gives 0. Scratch: calls that may overlap in time (other streams,
+ *                  two captured graphs) need one each.
+ * Rows behind cu_q[num_seqs] are not touched.
+ * Errors: NULL, SHAPE (counts, strides, offsets; table rows shorter than a sequence),
+ * UNSUPPORTED, OVERFLOW (a row stride of 2^24 elements or more, more than 2^31 - 1 rows times
+ * heads), ALIGN, WORKSPACE, LAUNCH. */
+size_t gdn_attention_prefill_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                             int32_t num_seqs, int32_t total_tokens);
+gdn_status gdn_attention_prefill(const gdn_attention_args *args, int32_t num_seqs,
+                                 const int32_t *cu_q_host, const int32_t *cu_q_dev,
+                                 const int32_t *cu_k_host, const int32_t *cu_k_dev,
+                                 void *workspace, size_t workspace_bytes, void *stream);
+
+/* gdn_attention_decode -- tokens_per_seq (T) new tokens of each of `batch` sequences, whose
+ * keys are on pages (page_size 0 UNSUPPORTED): first prefix_len keys that the whole batch
+ * shares, read and multiplied once for all, then the sequence's own, lens[b] tokens (the T
+ * new ones among them) of table row b. Query t sees the prefix and the first
+ * lens[b] - T + 1 + t own keys.
+ *   q, out, lse    row b * T + t
+ *   lens           [batch] int32 on the device; of more than max_len tokens the first
+ *                  max_len are there, below 0 counts as 0
+ *   max_len        an upper bound of lens that sizes the grid and the workspace
+ *   prefix_table   [ceil(prefix_len / page_size)] int32 pages of the prefix; NULL where
+ *                  prefix_len is 0
+ *   workspace      as above
+ * Errors: as gdn_attention_prefill's. */
+size_t gdn_attention_decode_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                            int32_t batch, int32_t tokens_per_seq, int32_t max_len,
+                                            int32_t prefix_len);
+gdn_status gdn_attention_decode(const gdn_attention_args *args, int32_t batch,
+                                int32_t tokens_per_seq, const int32_t *lens, int32_t max_len,
+                                const int32_t *prefix_table, int32_t prefix_len, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The pages of a cache. A table row lists the pages of one sequence in order, -1 where
+ * there is none; refs counts the rows' references to each page, and a page with none is
+ * free. Free pages are handed out lowest first, in the order of the requests and of a row's
+ * entries. Pages of a row are its first entries.
+ *
+ *   table          [rows][table_stride] int32, width entries of each row in use
+ *   refs           [num_pages] int32
+ *   page_size      tokens a page holds, >= 1
+ *   data           the pages of every layer's keys and values: num_planes planes of
+ *                  num_pages pages of page_bytes, page and plane strides in bytes; all
+ *                  multiples of 16, data too (page_bytes at most 2^30)
+ * A request for a row outside [0, rows), to change a row that an earlier request of the
+ * call names too, or on rows that do not hold what it needs is refused: its status is 2 and
+ * nothing of it is done. Entries outside [0, num_pages) count as none.
+ * Calls on one table and refs are ordered by the caller; n is at most 1024 (else OVERFLOW).
+ * Errors: NULL, SHAPE, OVERFLOW, ALIGN, WORKSPACE, LAUNCH.
+ * ------------------------------------------------------------------------- */
+typedef struct gdn_page_args {
+    int32_t *table;
+    int64_t table_stride;
+    int32_t rows, width;
+    int32_t *refs;
+    int32_t num_pages, page_size;
+    void *data;
+    int32_t num_planes;
+    int64_t plane_stride, page_stride, page_bytes;
+} gdn_page_args;
+
+/* gdn_pages_free -- releases the entries keep[i] and later (all, keep NULL) of row rows[i]:
+ * their pages' refs go down by one, the entries become -1. A row named twice is released
+ * once, from the lower of its keep on. data is not used. */
+gdn_status gdn_pages_free(const gdn_page_args *args, int32_t n, const int32_t *rows,
+                          const int32_t *keep, void *stream);
+
+/* gdn_pages_reserve -- gives row rows[i] a page for each of the first ceil(lens[i] /
+ * page_size) entries that has none. status[i]: 0 done, 1 pages are needed, but too few were
+ * left for it and the requests before it (nothing of it done), 2 refused (also lens[i] below
+ * 0 or past the row). data is not used. */
+gdn_status gdn_pages_reserve(const gdn_page_args *args, int32_t n, const int32_t *rows,
+                             const int32_t *lens, int32_t *status, void *stream);
+
+/* gdn_pages_fork -- row dst[i], which holds no page, becomes the first lens[i] tokens of
+ * row src[i]: full pages are shared (refs up by one), a last page filled in part is copied
+ * to a free one, on every plane. status as gdn_pages_reserve's; refused also where the
+ * source lacks a page of them or is a dst of the call. One source may be forked many times.
+ * workspace: gdn_pages_workspace_bytes(num_pages), aligned to 256. */
+size_t gdn_pages_workspace_bytes(int32_t num_pages);
+gdn_status gdn_pages_fork(const gdn_page_args *args, int32_t n, const int32_t *src,
+                          const int32_t *dst, const int32_t *lens, int32_t *status,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
+/* gdn_pages_compact -- moves the pages in use together: with U of them, the i-th page in use
+ * at U or later goes to the i-th free page below U, on every plane; table and refs follow
+ * (the whole width of every row). page_map [num_pages]: where each page went, itself where
+ * it did not move. used [1]: U. page_size is not used. workspace as gdn_pages_fork's. */
+gdn_status gdn_pages_compact(const gdn_page_args *args, int32_t *page_map, int32_t *used,
+                             void *workspace, size_t workspace_bytes, void *stream);
 
 /* ---------------------------------------------------------------------------
  * Kernel selection, for inspection and host-side tests. Which kernel a call runs
