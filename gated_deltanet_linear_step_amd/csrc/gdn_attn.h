@@ -56,6 +56,7 @@ struct AttnPrefillParams {
     const int32_t *cu_q, *cu_k, *lens;
     int max_keys;
     int splits, first_slot;  // runs of keys of a block of queries, and the slot of the first run
+    bool one_round;          // all workgroups are on the device at once (set by the launcher)
 };
 bool attn_supported(int D);
 // Runs of keys that a call is split into

@@ -63,6 +63,7 @@ __global__ void join_kernel(const AttnParams p)
 }
 
 constexpr int kBlock = 128;  // rows of a workgroup of the prefill kernel
+constexpr int kCus = 256;
 
 }  // namespace
 
@@ -83,9 +84,13 @@ int64_t attn_prefill_blocks(int Hq, int Hkv, int N, int64_t total, bool packed)
     return (packed ? total * G / kBlock + N : N * ((total / std::max(N, 1) * G + kBlock - 1) / kBlock)) * Hkv;
 }
 
-hipError_t launch_attn_prefill(const AttnPrefillParams &p, hipStream_t s)
+hipError_t launch_attn_prefill(const AttnPrefillParams &given, hipStream_t s)
 {
+    AttnPrefillParams p = given;
     const int64_t blocks = attn_prefill_blocks(p.a.Hq, p.a.Hkv, p.N, p.total, p.cu_q != nullptr) * p.splits;
+    // without the blocks that stay empty: one a sequence
+    const int64_t empty = p.cu_q ? (int64_t)p.N * p.a.Hkv * p.splits : 0;
+    p.one_round = blocks - empty <= 2 * kCus;
     return p.a.dt == DT_BF16 ? launch_attn_prefill_bf16(p, (unsigned)blocks, s) : launch_attn_prefill_f16(p, (unsigned)blocks, s);
 }
 

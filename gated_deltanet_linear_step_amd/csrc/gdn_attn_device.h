@@ -15,6 +15,7 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) void lds_void;
 
 // exp2 of a masked score, and the running maximum before any key
@@ -77,6 +78,32 @@ template <int DT>
 __device__ __forceinline__ float to_f32(uint32_t h)
 {
     return DT == DT_BF16 ? bf16_bits_to_f32(h) : f16_bits_to_f32(h);
+}
+
+// 16 bytes at an LDS address, and a transposing read: a lane's four elements are column i (of lane i of 16) of the four rows
+// whose 16 columns, in groups of four, the lanes point at
+__device__ __forceinline__ u32x4 lds_read16(uint32_t at) { return *(const lds_u32x4 *)(uintptr_t)at; }
+__device__ __forceinline__ u32x2 lds_read_tr(uint32_t at)
+{
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)at));
+}
+
+// A value of which the compiler knows nothing: what is computed from it late is not kept in registers from early on
+__device__ __forceinline__ int opaque(int x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// Copies 16 bytes a lane from base + off to the LDS, lane l's to byte `to` + 16 l, without waiting. Written out because
+// the compiler lets every transposing LDS read wait for all such copies, those to another buffer too: whoever
+// reads what was copied waits for it (vmcnt) itself. (m0 is the compiler's only as an operand set right before its use.)
+__device__ __forceinline__ void copy16(const unsigned char *base, uint32_t off, uint32_t to)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(to), "v"(off), "s"(base)
+                 : "memory");
 }
 
 // Maximum and sum over a lane and the one 32 away (the swap leaves the lower half's values in one word, the upper half's

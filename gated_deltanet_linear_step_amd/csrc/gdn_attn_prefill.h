@@ -41,6 +41,17 @@ struct Geo {
         return D == 64 ? 2 * ((row >> 1) & 3) : D == 96 ? 2 * ((row >> 2) & 1) : 2 * (row & 7);
     }
     __device__ __forceinline__ static int v_at(int row, int b) { return row * PITCH + 16 * (b ^ v_swizzle(row)); }
+    // Blocks 2 c + x of a row, and 4 c + x of V, from where blocks x lie: the permutation is an exclusive or of a few bits
+    __device__ __forceinline__ static uint32_t k_next(uint32_t at, int c)
+    {
+        constexpr int M = D == 64 ? 4 : D == 96 ? 2 : 8;
+        return (at ^ (32 * (c % M))) + 32 * M * (c / M);
+    }
+    __device__ __forceinline__ static uint32_t v_next(uint32_t at, int c)
+    {
+        constexpr int M = D == 64 ? 2 : D == 96 ? 1 : 4;
+        return (at ^ (64 * (c % M))) + 64 * M * (c / M);
+    }
 };
 
 // First block of 128 rows that the sequences before cu[s] leave to sequence s (some blocks stay empty)
@@ -64,7 +75,10 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
     // Work: a key head, a run of keys, a block of rows; the last blocks, which see most keys, first
     const int kvh = blockIdx.x % p.a.Hkv, rest = blockIdx.x / p.a.Hkv;
     const int split = rest % p.splits;
-    int block = gridDim.x / (p.a.Hkv * p.splits) - 1 - rest / p.splits;
+    const int blocks_all = gridDim.x / (p.a.Hkv * p.splits);
+    int block = rest / p.splits;
+    // (of one round of workgroups, two on a CU, the second half goes the other way, so that a CU has one of either kind)
+    block = p.one_round && block >= blocks_all / 2 ? block - blocks_all / 2 : blocks_all - 1 - block;
     int seq = 0, row0, len, nk;
     int64_t key0 = 0;
     if (p.cu_q) {
@@ -109,16 +123,17 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
     // What a lane fetches of each tile: FETCH blocks of the wave's ROWS rows
     const unsigned char *const kb = static_cast<const unsigned char *>(p.a.kv.k), *const vb = static_cast<const unsigned char *>(p.a.kv.v);
     const int32_t *const table = p.a.kv.table + (PAGED ? seq * p.a.kv.table_stride : 0);
-    const int64_t k_row = 2 * (PAGED ? (int64_t)D : p.a.kv.k_stride), v_row = 2 * (PAGED ? (int64_t)D : p.a.kv.v_stride);
+    // bytes from row to row: below 2^25, and 16 rows are fetched from one address
+    const uint32_t k_row = 2 * (PAGED ? D : (uint32_t)p.a.kv.k_stride), v_row = 2 * (PAGED ? D : (uint32_t)p.a.kv.v_stride);
     const int64_t head_at = PAGED ? ((int64_t)kvh << p.a.kv.page_shift) * D : (int64_t)kvh * D;
-    int fetch_row[G_::FETCH], fetch_k[G_::FETCH], fetch_v[G_::FETCH];
+    uint32_t k_off[G_::FETCH], v_off[G_::FETCH];
 #pragma unroll
     for (int i = 0; i < G_::FETCH; ++i) {
         const int at = 64 * i + lane, r = at / NB, r_tile = wave * G_::ROWS + r, b = at % NB;
-        fetch_row[i] = r;
-        fetch_k[i] = G_::k_at(r_tile, b) - r_tile * G_::PITCH;
-        fetch_v[i] = G_::v_at(r_tile, b) - r_tile * G_::PITCH;
+        k_off[i] = r * k_row + G_::k_at(r_tile, b) - r_tile * G_::PITCH;
+        v_off[i] = r * v_row + G_::v_at(r_tile, b) - r_tile * G_::PITCH;
     }
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void *)lds, lds_at = lds0 + wave * G_::ROWS * G_::PITCH;
     // On pages: lane g holds the page of the g-th 16 keys of a tile, -1 where it is none
     constexpr int GROUPS = KT / 16;
     auto pages_of = [&](int tile) {
@@ -131,24 +146,33 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
         return page;
     };
     auto fetch = [&](int tile, int buf, int pages) {
-        const int k0 = tile * KT + wave * G_::ROWS;
-        int64_t k_at, v_at;
+        int k0 = tile * KT + wave * G_::ROWS;
+        const uint32_t to = lds_at + buf * G_::TILE;
+        const unsigned char *k_from, *v_from;
         if constexpr (PAGED) {
             // keys behind the last one, and those of no page, are some other rows of the pool: they are masked
             const int page = max(0, __builtin_amdgcn_readlane(pages, wave * G_::ROWS / 16));
-            const int in_page = k0 & ((1 << p.a.kv.page_shift) - 1);
-            k_at = page * p.a.kv.k_stride + head_at + (int64_t)in_page * D;
-            v_at = page * p.a.kv.v_stride + head_at + (int64_t)in_page * D;
+            const int64_t in_page = head_at + (int64_t)(k0 & ((1 << p.a.kv.page_shift) - 1)) * D;
+            k_from = kb + 2 * (page * p.a.kv.k_stride + in_page);
+            v_from = vb + 2 * (page * p.a.kv.v_stride + in_page);
         } else {
-            k_at = (key0 + k0) * p.a.kv.k_stride + head_at;
-            v_at = (key0 + k0) * p.a.kv.v_stride + head_at;
+            k0 = min(k0, nk - 1);
+            k_from = kb + 2 * ((key0 + k0) * p.a.kv.k_stride + head_at);
+            v_from = vb + 2 * ((key0 + k0) * p.a.kv.v_stride + head_at);
+            if (k0 + G_::ROWS > nk) {  // no row behind the last key
+#pragma unroll
+                for (int i = 0; i < G_::FETCH; ++i) {
+                    const uint32_t over = max(0, (64 * i + opaque(lane)) / NB - (nk - 1 - k0));
+                    copy16(k_from, k_off[i] - over * k_row, to + 1024 * i);
+                    copy16(v_from, v_off[i] - over * v_row, to + 1024 * i + 2 * G_::TILE);
+                }
+                return;
+            }
         }
 #pragma unroll
         for (int i = 0; i < G_::FETCH; ++i) {
-            const int r = PAGED ? fetch_row[i] : min(fetch_row[i], nk - 1 - k0);  // packed: no row behind the last key
-            unsigned char *to = lds + buf * G_::TILE + wave * G_::ROWS * G_::PITCH + 1024 * i;
-            __builtin_amdgcn_global_load_lds(kb + 2 * k_at + r * k_row + fetch_k[i], (lds_void *)to, 16, 0, 0);
-            __builtin_amdgcn_global_load_lds(vb + 2 * v_at + r * v_row + fetch_v[i], (lds_void *)(to + 2 * G_::TILE), 16, 0, 0);
+            copy16(k_from, k_off[i], to + 1024 * i);
+            copy16(v_from, v_off[i], to + 1024 * i + 2 * G_::TILE);
         }
     };
 
@@ -158,6 +182,10 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
 #pragma unroll
         for (int c = 0; c < KC; ++c)
             q[c] = *reinterpret_cast<const u32x4 *>(from + 32 * c);
+        // here, not in the loop, where the wait would be for the tile on its way too
+#pragma unroll
+        for (int c = 0; c < KC; ++c)
+            asm volatile("" : "+v"(q[c]));
     }
     const float scale = p.a.scale * 1.4426950408889634f;  // exponentials in base 2
     f32x16 o[TV] = {};
@@ -184,14 +212,15 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
         if (k0 >= wave_most)
             continue;
 
-        const unsigned char *kt = lds + buf * G_::TILE;
-        unsigned char *vt = lds + (2 + buf) * G_::TILE;
+        // the LDS addresses of a tile are formed as they are needed (D = 256 has no registers for them)
+        const uint32_t kt = lds0 + buf * G_::TILE, vt = lds0 + (2 + buf) * G_::TILE;
+        const uint32_t k_at = opaque(kt + G_::k_at(col, half));
         f32x16 s[TS] = {};
 #pragma unroll
         for (int t = 0; t < TS; ++t)
 #pragma unroll
             for (int c = 0; c < KC; ++c)
-                s[t] = T::mfma32(*reinterpret_cast<const u32x4 *>(kt + G_::k_at(32 * t + col, 2 * c + half)), q[c], s[t]);
+                s[t] = T::mfma32(lds_read16(G_::k_next(k_at, c) + 32 * t * G_::PITCH), q[c], s[t]);
 
         // some row of the wave does not see all of the tile
         const bool masked = k0 + KT > wave_least || k0 + KT > nk || none != 0;
@@ -232,13 +261,10 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
             }
 
         // V^T, 32 dv from 32 tv on and the 16 keys of step st, in P's order
-        const int tr_row = 4 * half + ((lane & 15) >> 2), tr_block = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+        const uint32_t v_at = opaque(vt + G_::v_at(4 * half + ((lane & 15) >> 2), 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) + 8 * (lane & 1));
         auto v_of = [&](int tv, int st) {
-            const int r = 16 * st + tr_row;
-            unsigned char *a = vt + G_::v_at(r, 4 * tv + tr_block) + 8 * (lane & 1);
-            unsigned char *b = vt + G_::v_at(r + 8, 4 * tv + tr_block) + 8 * (lane & 1);
-            const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)a));
-            const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)b));
+            const uint32_t at = G_::v_next(v_at, tv) + 16 * st * G_::PITCH;
+            const u32x2 x = lds_read_tr(at), y = lds_read_tr(at + 8 * G_::PITCH);
             return u32x4{x.x, x.y, y.x, y.y};
         };
         if (masked) {
@@ -246,7 +272,7 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
             // a row that sees one of them becomes NaN
             uint32_t bad = 0;
             for (int at = 16 * lane; at < G_::TILE; at += 1024) {
-                const u32x4 w = *reinterpret_cast<const u32x4 *>(vt + at);
+                const u32x4 w = lds_read16(vt + at);
                 bad |= not_finite<DT>(w.x) | not_finite<DT>(w.y) | not_finite<DT>(w.z) | not_finite<DT>(w.w);
             }
             if (__ballot(bad != 0) != 0) {
@@ -289,9 +315,11 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
     }
 
     sum = half_sum(sum);
-    if (wrow + col >= rows)
+    const int end_row = wrow + opaque(col);
+    if (end_row >= rows)
         return;
-    const int64_t at = (int64_t)(row0 + token) * p.a.Hq + head;
+    const int end_token = end_row / G, end_head = kvh * G + end_row - end_token * G;
+    const int64_t at = (int64_t)(row0 + end_token) * p.a.Hq + end_head;
     if (p.a.slots > 0) {
         const int64_t slot = at * p.a.slots + p.first_slot + split;
         if (half == 0)
@@ -306,7 +334,7 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
         return;
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    uint16_t *to = static_cast<uint16_t *>(p.a.out) + (int64_t)(row0 + token) * p.a.out_stride + (int64_t)head * D;
+    uint16_t *to = static_cast<uint16_t *>(p.a.out) + (int64_t)(row0 + end_token) * p.a.out_stride + (int64_t)end_head * D;
 #pragma unroll
     for (int tv = 0; tv < TV; ++tv)
 #pragma unroll
