@@ -47,7 +47,7 @@ struct AttnParams {
     int slots;  // partial results of a query; 0: the outputs are written at once
 };
 
-// Blocks of queries against runs of keys (gdn_attn_prefill.hip). Sequences: packed and causal by cu_q and cu_k (device);
+// Blocks of queries against runs of keys (gdn_attn_prefill.h). Sequences: packed and causal by cu_q and cu_k (device);
 // or, cu_q NULL, N of T queries each, causal against lens[s] keys of table row s (lens on the device, at most max_keys
 // count), or, lens NULL too, N = 1 against max_keys keys that every query sees.
 struct AttnPrefillParams {
@@ -67,7 +67,7 @@ hipError_t launch_attn_prefill(const AttnPrefillParams &p, hipStream_t s);
 hipError_t launch_attn_prefill_bf16(const AttnPrefillParams &p, unsigned grid, hipStream_t s);
 hipError_t launch_attn_prefill_f16(const AttnPrefillParams &p, unsigned grid, hipStream_t s);
 
-// A few queries of each sequence against its own pages (gdn_attn_decode.hip).
+// A few queries of each sequence against its own pages (gdn_attn_decode.h).
 struct AttnDecodeParams {
     AttnParams a;
     int B, T;
@@ -78,6 +78,8 @@ struct AttnDecodeParams {
 int64_t attn_decode_blocks(int Hq, int Hkv, int D, int B, int T);  // workgroups for each run of keys
 void attn_decode_splits(int Hq, int Hkv, int D, int B, int T, int max_len, int *splits, int *split_keys);
 hipError_t launch_attn_decode(const AttnDecodeParams &p, hipStream_t s);
+hipError_t launch_attn_decode_bf16(const AttnDecodeParams &p, unsigned grid, hipStream_t s);
+hipError_t launch_attn_decode_f16(const AttnDecodeParams &p, unsigned grid, hipStream_t s);
 
 // Joins the partial results of `rows` rows (queries times heads) into outputs.
 hipError_t launch_attn_join(const AttnParams &p, int64_t rows, hipStream_t s);

@@ -94,18 +94,43 @@ hipError_t launch_attn_prefill(const AttnPrefillParams &given, hipStream_t s)
     return p.a.dt == DT_BF16 ? launch_attn_prefill_bf16(p, (unsigned)blocks, s) : launch_attn_prefill_f16(p, (unsigned)blocks, s);
 }
 
-// Decode steps: blocks of rows like the prompts', one sequence after another
-int64_t attn_decode_blocks(int Hq, int Hkv, int D, int B, int T) { return attn_prefill_blocks(Hq, Hkv, B, (int64_t)B * T, false); }
+namespace {
+
+// Up to this many rows of a sequence and key head the decode kernel takes; more are blocks of rows like a prompt's
+constexpr int kDecodeRows = 32;
+bool few_rows(int Hq, int Hkv, int T) { return (int64_t)T * (Hq / Hkv) <= kDecodeRows; }
+
+}  // namespace
+
+int64_t attn_decode_blocks(int Hq, int Hkv, int D, int B, int T)
+{
+    return few_rows(Hq, Hkv, T) ? (int64_t)B * Hkv : attn_prefill_blocks(Hq, Hkv, B, (int64_t)B * T, false);
+}
 
 void attn_decode_splits(int Hq, int Hkv, int D, int B, int T, int max_len, int *splits, int *split_keys)
 {
-    const int64_t most = std::max(1, max_len / 256);
-    *splits = (int)std::clamp<int64_t>(1024 / attn_decode_blocks(Hq, Hkv, D, B, T), 1, std::min<int64_t>(most, 64));
-    *split_keys = 0;
+    const int64_t blocks = attn_decode_blocks(Hq, Hkv, D, B, T);
+    if (!few_rows(Hq, Hkv, T)) {
+        *splits = (int)std::clamp<int64_t>(1024 / blocks, 1, std::min<int64_t>(std::max(1, max_len / 256), 64));
+        *split_keys = 0;
+        return;
+    }
+    // Runs of a whole number of rounds of the waves, as many workgroups as keep every CU busy, at most what the lanes hold pages
+    // for
+    const int waves = D == 64 ? 4 : D == 256 ? 1 : 2, round = 32 * waves;
+    const int64_t rounds = (std::max(max_len, 1) + round - 1) / round;
+    const int64_t want = std::clamp<int64_t>(1024 / std::max<int64_t>(blocks, 1), 1, rounds);
+    const int64_t each = std::min<int64_t>((rounds + want - 1) / want, std::max(1, 1024 / round));
+    *split_keys = (int)(each * round);
+    *splits = (int)((rounds + each - 1) / each);
 }
 
 hipError_t launch_attn_decode(const AttnDecodeParams &p, hipStream_t s)
 {
+    if (few_rows(p.a.Hq, p.a.Hkv, p.T)) {
+        const unsigned grid = (unsigned)((int64_t)p.B * p.a.Hkv * p.splits);
+        return p.a.dt == DT_BF16 ? launch_attn_decode_bf16(p, grid, s) : launch_attn_decode_f16(p, grid, s);
+    }
     AttnPrefillParams f{};
     f.a = p.a;
     f.N = p.B;
