@@ -55,12 +55,15 @@ struct AttnPrefillParams {
     int N, T, total;  // sequences, queries of each without cu_q, queries in all
     const int32_t *cu_q, *cu_k, *lens;
     int max_keys;
-    int splits, first_slot;  // runs of keys of a block of queries, and the slot of the first run
+    int splits, split_tiles, first_slot;  // runs of keys of a block of queries, their tiles, and the slot of the first
     bool one_round;          // all workgroups are on the device at once (set by the launcher)
 };
 bool attn_supported(int D);
-// Runs of keys that a call is split into
-int attn_prefill_splits(int Hq, int Hkv, int64_t total, int64_t max_keys);
+// Runs of keys that a call is split into, and their length: by the offsets, or (cu_q NULL) one sequence against `keys` keys;
+// and the most that any offsets of as many queries give
+void attn_prefill_splits(int Hq, int Hkv, int D, int N, int64_t total, const int32_t *cu_q, const int32_t *cu_k, int keys, int *splits,
+                         int *split_tiles);
+int attn_prefill_most_splits(int Hq, int Hkv, int64_t total);
 // Workgroups for each run of keys
 int64_t attn_prefill_blocks(int Hq, int Hkv, int N, int64_t total, bool packed);
 hipError_t launch_attn_prefill(const AttnPrefillParams &p, hipStream_t s);
@@ -73,7 +76,7 @@ struct AttnDecodeParams {
     int B, T;
     const int32_t *lens;
     int max_len;
-    int splits, split_keys, first_slot;  // runs of split_keys keys each
+    int splits, split_keys, first_slot;  // runs of split_keys keys each (of split_keys tiles where blocks of rows take it)
 };
 int64_t attn_decode_blocks(int Hq, int Hkv, int D, int B, int T);  // workgroups for each run of keys
 void attn_decode_splits(int Hq, int Hkv, int D, int B, int T, int max_len, int *splits, int *split_keys);

@@ -15,66 +15,133 @@ namespace {
 
 using namespace attn;
 
-// A workgroup per row (query and head); D / 4 lanes share a run's outputs, the workgroup's other lanes take other runs.
+// Four of a row's outputs, from element d on
 template <int DT>
-__global__ void join_kernel(const AttnParams p)
+__device__ __forceinline__ void store_joined(const AttnParams &p, int64_t row, int d, f32x4 o, float most, float total)
 {
-    __shared__ float4 sums[256];
-    __shared__ float totals[256];
-    const int lanes = p.D / 4, groups = blockDim.x / lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
-    const int64_t row = blockIdx.x, first = row * p.slots;
-    float most = kNone;
-    for (int s = 0; s < p.slots; ++s)
-        most = fmaxf(most, p.stat[first + s].y == 0.f ? kNone : p.stat[first + s].x);
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float total = 0.f;
-    if (group < groups)
-        for (int s = group; s < p.slots; s += groups) {
-            const float2 st = p.stat[first + s];
-            if (st.y == 0.f)
-                continue;
-            const float f = exp2_f(st.x - most);
-            const float4 v = *reinterpret_cast<const float4 *>(p.part + (first + s) * p.D + 4 * lane);
-            total += f * st.y;
-            o.x += f * v.x;
-            o.y += f * v.y;
-            o.z += f * v.z;
-            o.w += f * v.w;
-        }
-    sums[threadIdx.x] = o;
-    totals[threadIdx.x] = total;
-    __syncthreads();
-    if (group != 0)
-        return;
-    for (int g = 1; g < groups; ++g) {
-        const float4 v = sums[g * lanes + lane];
-        total += totals[g * lanes + lane];
-        o.x += v.x;
-        o.y += v.y;
-        o.z += v.z;
-        o.w += v.w;
-    }
     const float inv = total == 0.f ? 0.f : 1.f / total;
     const int64_t token = row / p.Hq, head = row - token * p.Hq;
-    uint16_t *to = static_cast<uint16_t *>(p.out) + token * p.out_stride + head * p.D + 4 * lane;
+    uint16_t *to = static_cast<uint16_t *>(p.out) + token * p.out_stride + head * p.D + d;
     *reinterpret_cast<u32x2 *>(to) = u32x2{pack2<DT>(o.x * inv, o.y * inv), pack2<DT>(o.z * inv, o.w * inv)};
-    if (p.lse && lane == 0)
+    if (p.lse && d == 0)
         p.lse[row] = total == 0.f ? kNone : (most + __log2f(total)) * 0.69314718055994531f;
+}
+
+// A few runs: D / 4 lanes join a row (a query and head) run after run, 256 lanes as many rows as they are for.
+template <int DT>
+__global__ __launch_bounds__(256) void join_few_kernel(const AttnParams p, int64_t rows)
+{
+    const int lanes = p.D / 4, group = threadIdx.x / lanes, d = 4 * (threadIdx.x % lanes), groups = 256 / lanes;
+    const int64_t row = (int64_t)blockIdx.x * groups + group, first = row * p.slots;
+    if (group >= groups || row >= rows)
+        return;
+    float most = kNone;
+    for (int s = 0; s < p.slots; ++s) {
+        const float2 st = p.stat[first + s];
+        most = fmaxf(most, st.y == 0.f ? kNone : st.x);
+    }
+    f32x4 o = {};
+    float total = 0.f;
+    for (int s = 0; s < p.slots; ++s) {
+        const float2 st = p.stat[first + s];
+        if (st.y == 0.f)
+            continue;
+        const float f = exp2_f(st.x - most);
+        total += f * st.y;
+        o += f * *reinterpret_cast<const f32x4 *>(p.part + (first + s) * p.D + d);
+    }
+    store_joined<DT>(p, row, d, o, most, total);
+}
+
+constexpr int kJoinThreads = 256, kJoinWidth = 32, kJoinRuns = kJoinThreads / (kJoinWidth / 4);
+
+// A workgroup joins 32 of a row's (a query and head) D outputs: 8 lanes share a run's, 32 runs are read at a time.
+template <int DT>
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(const AttnParams p)
+{
+    __shared__ float4 sums[kJoinThreads];
+    __shared__ float tops[kJoinThreads / 64], totals[kJoinThreads];
+    const int parts = p.D / kJoinWidth, lane = threadIdx.x % 8, group = threadIdx.x / 8;
+    const int64_t row = blockIdx.x / parts, first = row * p.slots;
+    const int d = blockIdx.x % parts * kJoinWidth + 4 * lane;
+    float most = kNone;
+    for (int s = threadIdx.x; s < p.slots; s += kJoinThreads) {
+        const float2 st = p.stat[first + s];
+        most = fmaxf(most, st.y == 0.f ? kNone : st.x);
+    }
+#pragma unroll
+    for (int x = 32; x; x >>= 1)
+        most = fmaxf(most, __shfl_xor(most, x, 64));
+    if ((threadIdx.x & 63) == 0)
+        tops[threadIdx.x >> 6] = most;
+    __syncthreads();
+    most = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+    f32x4 o = {};
+    float total = 0.f;
+    for (int s = group; s < p.slots; s += kJoinRuns) {
+        const float2 st = p.stat[first + s];
+        if (st.y == 0.f)
+            continue;
+        const float f = exp2_f(st.x - most);
+        total += f * st.y;
+        o += f * *reinterpret_cast<const f32x4 *>(p.part + (first + s) * p.D + d);
+    }
+    // the wave's eight runs, then the four waves
+#pragma unroll
+    for (int x = 8; x < 64; x *= 2) {
+        total += __shfl_xor(total, x, 64);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            o[i] += __shfl_xor(o[i], x, 64);
+    }
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) < 8) {
+        sums[8 * wave + lane] = make_float4(o.x, o.y, o.z, o.w);
+        totals[8 * wave + lane] = total;
+    }
+    __syncthreads();
+    if (threadIdx.x >= 8)
+        return;
+#pragma unroll
+    for (int w = 1; w < kJoinThreads / 64; ++w) {
+        const float4 v = sums[8 * w + lane];
+        total += totals[8 * w + lane];
+        o += f32x4{v.x, v.y, v.z, v.w};
+    }
+    store_joined<DT>(p, row, d, o, most, total);
 }
 
 constexpr int kBlock = 128;  // rows of a workgroup of the prefill kernel
 constexpr int kCus = 256;
+constexpr int kFewRuns = 32;
 
 }  // namespace
 
 bool attn_supported(int D) { return D == 64 || D == 96 || D == 128 || D == 256; }
 
-int attn_prefill_splits(int Hq, int Hkv, int64_t total, int64_t max_keys)
+int attn_prefill_most_splits(int Hq, int Hkv, int64_t total)
 {
-    // at least this many workgroups where there are keys enough: two for each CU
     const int64_t G = Hq / Hkv, blocks = std::max<int64_t>(1, (total * G + kBlock - 1) / kBlock) * Hkv;
-    const int64_t most = std::max<int64_t>(1, max_keys / 256);
-    return (int)std::clamp<int64_t>(512 / blocks, 1, std::min<int64_t>(most, 32));
+    return blocks >= kCus ? 1 : (int)std::min<int64_t>(1024 / blocks, 32);
+}
+
+void attn_prefill_splits(int Hq, int Hkv, int D, int N, int64_t total, const int32_t *cu_q, const int32_t *cu_k, int keys, int *splits,
+                         int *split_tiles)
+{
+    // Where the blocks of rows are fewer than the CUs, runs of keys of one length, so many that two workgroups for each CU
+    // have one; a run is at least four tiles.
+    const int most = attn_prefill_most_splits(Hq, Hkv, total), KT = D <= 128 ? 64 : 32;
+    const int64_t G = Hq / Hkv;
+    int64_t all = 0, longest = 0;
+    for (int s = 0; s < N; ++s) {
+        const int64_t len = cu_q ? cu_q[s + 1] - cu_q[s] : total, nk = cu_q ? cu_k[s + 1] - cu_k[s] : keys;
+        const int64_t tiles = (nk + KT - 1) / KT, blocks = (len * G + kBlock - 1) / kBlock;
+        all += tiles * blocks * Hkv;  // (of queries that see all keys: few queries against many keys are what is split)
+        longest = std::max(longest, blocks > 0 ? tiles : 0);
+    }
+    const int64_t each = std::max<int64_t>({(all + 2 * kCus - 1) / (2 * kCus), 4, (longest + most - 1) / most});
+    *splits = (int)std::max<int64_t>(1, most == 1 ? 1 : (longest + each - 1) / each);
+    *split_tiles = *splits == 1 ? 1 << 30 : (int)each;
 }
 
 int64_t attn_prefill_blocks(int Hq, int Hkv, int N, int64_t total, bool packed)
@@ -111,15 +178,17 @@ void attn_decode_splits(int Hq, int Hkv, int D, int B, int T, int max_len, int *
 {
     const int64_t blocks = attn_decode_blocks(Hq, Hkv, D, B, T);
     if (!few_rows(Hq, Hkv, T)) {
-        *splits = (int)std::clamp<int64_t>(1024 / blocks, 1, std::min<int64_t>(std::max(1, max_len / 256), 64));
-        *split_keys = 0;
+        const int KT = D <= 128 ? 64 : 32;
+        const int64_t tiles = (std::max(max_len, 1) + KT - 1) / KT, want = std::clamp<int64_t>(2 * kCus / blocks, 1, 64);
+        *split_keys = (int)std::max<int64_t>((tiles + want - 1) / want, 4);
+        *splits = (int)((tiles + *split_keys - 1) / *split_keys);
         return;
     }
     // Runs of a whole number of rounds of the waves, as many workgroups as keep every CU busy, at most what the lanes hold pages
     // for
-    const int waves = D == 64 ? 4 : D == 256 ? 1 : 2, round = 32 * waves;
+    constexpr int round = 32 * 4;
     const int64_t rounds = (std::max(max_len, 1) + round - 1) / round;
-    const int64_t want = std::clamp<int64_t>(1024 / std::max<int64_t>(blocks, 1), 1, rounds);
+    const int64_t want = std::clamp<int64_t>((D == 256 ? 256 : 512) / std::max<int64_t>(blocks, 1), 1, rounds);
     const int64_t each = std::min<int64_t>((rounds + want - 1) / want, std::max(1, 1024 / round));
     *split_keys = (int)(each * round);
     *splits = (int)((rounds + each - 1) / each);
@@ -139,17 +208,27 @@ hipError_t launch_attn_decode(const AttnDecodeParams &p, hipStream_t s)
     f.lens = p.lens;
     f.max_keys = p.max_len;
     f.splits = p.splits;
+    f.split_tiles = p.split_keys;
     f.first_slot = p.first_slot;
     return launch_attn_prefill(f, s);
 }
 
 hipError_t launch_attn_join(const AttnParams &p, int64_t rows, hipStream_t s)
 {
-    const int threads = p.slots <= 8 ? 64 : 256;
+    if (p.slots <= kFewRuns) {
+        const int groups = 256 / (p.D / 4);
+        const unsigned grid = (unsigned)((rows + groups - 1) / groups);
+        if (p.dt == DT_BF16)
+            join_few_kernel<DT_BF16><<<grid, 256, 0, s>>>(p, rows);
+        else
+            join_few_kernel<DT_F16><<<grid, 256, 0, s>>>(p, rows);
+        return hipGetLastError();
+    }
+    const unsigned grid = (unsigned)(rows * (p.D / kJoinWidth));
     if (p.dt == DT_BF16)
-        join_kernel<DT_BF16><<<(unsigned)rows, threads, 0, s>>>(p);
+        join_kernel<DT_BF16><<<grid, kJoinThreads, 0, s>>>(p);
     else
-        join_kernel<DT_F16><<<(unsigned)rows, threads, 0, s>>>(p);
+        join_kernel<DT_F16><<<grid, kJoinThreads, 0, s>>>(p);
     return hipGetLastError();
 }
 

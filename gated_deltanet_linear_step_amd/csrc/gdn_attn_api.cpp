@@ -100,13 +100,13 @@ void carve(gdn::AttnParams &p, int64_t rows, int slots, void *workspace)
 
 // How a decode step is split: runs of the prefix's keys, then of each sequence's own
 struct DecodeSplit {
-    int prefix, own, own_keys;
+    int prefix, prefix_tiles, own, own_keys;
 };
 DecodeSplit decode_split(int Hq, int Hkv, int D, int B, int T, int max_len, int prefix_len)
 {
-    DecodeSplit s{0, 0, 0};
+    DecodeSplit s{};
     if (prefix_len > 0)
-        s.prefix = gdn::attn_prefill_splits(Hq, Hkv, (int64_t)B * T, prefix_len);
+        gdn::attn_prefill_splits(Hq, Hkv, D, 1, (int64_t)B * T, nullptr, nullptr, prefix_len, &s.prefix, &s.prefix_tiles);
     gdn::attn_decode_splits(Hq, Hkv, D, B, T, max_len, &s.own, &s.own_keys);
     return s;
 }
@@ -274,7 +274,7 @@ size_t gdn_attention_prefill_workspace_bytes(int32_t q_heads, int32_t kv_heads, 
 {
     if (!heads_ok(q_heads, kv_heads, head_dim) || num_seqs < 0 || total_tokens < 1)
         return 0;
-    return split_bytes((int64_t)total_tokens * q_heads, gdn::attn_prefill_splits(q_heads, kv_heads, total_tokens, kI32Max), head_dim);
+    return split_bytes((int64_t)total_tokens * q_heads, gdn::attn_prefill_most_splits(q_heads, kv_heads, total_tokens), head_dim);
 }
 
 gdn_status gdn_attention_prefill(const gdn_attention_args *args, int32_t num_seqs, const int32_t *cu_q_host,
@@ -307,7 +307,7 @@ gdn_status gdn_attention_prefill(const gdn_attention_args *args, int32_t num_seq
     p.total = total;
     p.cu_q = cu_q_dev;
     p.cu_k = cu_k_dev;
-    p.splits = gdn::attn_prefill_splits(p.a.Hq, p.a.Hkv, total, longest_k);
+    gdn::attn_prefill_splits(p.a.Hq, p.a.Hkv, p.a.D, num_seqs, total, cu_q_host, cu_k_host, 0, &p.splits, &p.split_tiles);
     if (gdn::attn_prefill_blocks(p.a.Hq, p.a.Hkv, num_seqs, total, true) * p.splits >= kMaxBlocks)
         return GDN_ERR_OVERFLOW;
     const int64_t rows = (int64_t)total * p.a.Hq;
@@ -385,6 +385,7 @@ gdn_status gdn_attention_decode(const gdn_attention_args *args, int32_t batch, i
         f.T = f.total = (int)queries;
         f.max_keys = prefix_len;
         f.splits = d.prefix;
+        f.split_tiles = d.prefix_tiles;
         e = gdn::launch_attn_prefill(f, s);
     }
     p.B = batch;

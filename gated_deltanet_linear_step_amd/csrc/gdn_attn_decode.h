@@ -7,8 +7,8 @@
 //
 //  * A wave walks every WAVES-th 32 keys of the run by itself, with a running maximum and sum of its own; nothing waits for
 //    another wave before the end, where the waves' results are joined through the LDS.
-//  * K and V of 32 keys go from memory straight to the wave's LDS, while the 32 before are computed: the copies of a whole
-//    run are issued without a register for them, and every wait counts exactly its own copies.
+//  * K and V of 32 keys go from memory straight to the wave's LDS, the next K while V is multiplied and the next V while K is:
+//    one buffer of each is enough, no copy needs a register, and every wait counts exactly the copies behind it.
 //  * The pages of the whole run are looked up at once, a 16-key group a lane.
 //  * S^T = K Q^T (v_mfma_f32_16x16x32): a lane holds one row's scores; as they lie, the exponentials of two 16-key tiles are the
 //    operand of O^T += V^T P^T, whose V^T comes from transposing LDS reads. Blocks of 16 bytes are permuted within
@@ -24,7 +24,7 @@ template <int D>
 struct DecodeGeo {
     static constexpr int KEYS = 32, NB = D / 8, PITCH = 2 * D;
     static constexpr int HALF = KEYS * PITCH, STAGE = 2 * HALF;         // K, then V
-    static constexpr int WAVES = D == 64 ? 4 : D == 256 ? 1 : 2;        // two stages a wave: two workgroups share a CU's LDS
+    static constexpr int WAVES = 4;                                     // 8 to 32 KB each
     static constexpr int COPIES = NB / 4;                               // of 16 bytes a lane: 16 keys of K or of V
     static constexpr int MOST_KEYS = 32 * KEYS * WAVES;                 // of a run: 64 lanes hold its pages
 };
@@ -48,7 +48,7 @@ __device__ __forceinline__ void decode_run(const AttnDecodeParams &p)
     using DG = DecodeGeo<D>;
     using T = Type16<DT>;
     constexpr int KC = D / 32, TV = D / 16, WAVES = DG::WAVES, THREADS = 64 * WAVES;
-    constexpr int STAGES = 2 * WAVES * DG::STAGE, RESULTS = WAVES * 16 * NR * D * 4;
+    constexpr int STAGES = WAVES * DG::STAGE, RESULTS = WAVES * 16 * NR * D * 4;
     __shared__ __align__(1024) unsigned char lds[STAGES > RESULTS ? STAGES : RESULTS];
     __shared__ float2 stats[WAVES][16 * NR];
 
@@ -92,22 +92,18 @@ __device__ __forceinline__ void decode_run(const AttnDecodeParams &p)
     }
     const unsigned char *const kb = static_cast<const unsigned char *>(p.a.kv.k), *const vb = static_cast<const unsigned char *>(p.a.kv.v);
     const int64_t head_at = ((int64_t)kvh << p.a.kv.page_shift) * D;
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void *)lds + 2 * wave * DG::STAGE;
-    auto fetch = [&](int step) {
-        const uint32_t to = lds0 + (step & 1) * DG::STAGE;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void *)lds + wave * DG::STAGE;
+    auto fetch = [&](int step, bool is_v) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             // keys behind the last one, and those of no page, are some other rows of the pool: they are masked
             const int page = max(0, __builtin_amdgcn_readlane(pages, 2 * step + t));
             const int in_page = (keys0 + step * DG::KEYS * WAVES + 16 * t) & ((1 << p.a.kv.page_shift) - 1);
             const int64_t at = head_at + (int64_t)in_page * D;
-            const unsigned char *k_from = kb + 2 * (page * p.a.kv.k_stride + at), *v_from = vb + 2 * (page * p.a.kv.v_stride + at);
+            const unsigned char *from = is_v ? vb + 2 * (page * p.a.kv.v_stride + at) : kb + 2 * (page * p.a.kv.k_stride + at);
 #pragma unroll
             for (int i = 0; i < DG::COPIES; ++i)
-                copy16(k_from, k_off[i], to + t * (DG::HALF / 2) + 1024 * i);
-#pragma unroll
-            for (int i = 0; i < DG::COPIES; ++i)
-                copy16(v_from, v_off[i], to + DG::HALF + t * (DG::HALF / 2) + 1024 * i);
+                copy16(from, is_v ? v_off[i] : k_off[i], lds0 + (is_v ? DG::HALF : 0) + t * (DG::HALF / 2) + 1024 * i);
         }
     };
 
@@ -127,18 +123,15 @@ __device__ __forceinline__ void decode_run(const AttnDecodeParams &p)
         top[r] = kNone;
         sum[r] = 0.f;
     }
-    if (steps > 0)
-        fetch(0);
+    const uint32_t kt = lds0, vt = lds0 + DG::HALF;
+    constexpr int HALF_COPIES = 2 * DG::COPIES;
+    if (steps > 0) {
+        fetch(0, false);
+        fetch(0, true);
+    }
     for (int step = 0; step < steps; ++step) {
         const int k0 = keys0 + step * DG::KEYS * WAVES;
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the other stage has been read
-        if (step + 1 < steps) {
-            fetch(step + 1);
-            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(4 * DG::COPIES) : "memory");
-        } else {
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        }
-        const uint32_t kt = lds0 + (step & 1) * DG::STAGE, vt = kt + DG::HALF;
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(HALF_COPIES) : "memory");  // K is here, V behind it
         int none = 0;  // 16-key groups without a page
         none |= __builtin_amdgcn_readlane(pages, 2 * step) < 0 ? 1 : 0;
         none |= __builtin_amdgcn_readlane(pages, 2 * step + 1) < 0 ? 2 : 0;
@@ -165,6 +158,10 @@ __device__ __forceinline__ void decode_run(const AttnDecodeParams &p)
                         s[r][t][i] = key < min(seen[r], end) && !(none >> t & 1) ? s[r][t][i] : kNone;
                     }
         }
+        // K has been read: the next one
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (step + 1 < steps)
+            fetch(step + 1, false);
         u32x4 pf[NR];
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
@@ -194,12 +191,17 @@ __device__ __forceinline__ void decode_run(const AttnDecodeParams &p)
                     pf[r][2 * t + i / 2] = pack2<DT>(x, y);
                 }
         }
+        if (step + 1 < steps)
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(HALF_COPIES) : "memory");  // V is here, the next K behind it
+        else
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         const int tr_row = 4 * lg + (li >> 2);
         auto v_of = [&](int j) {
             const uint32_t at = vt + G_::v_at(tr_row, 2 * j + ((li & 3) >> 1)) + 8 * (li & 1);
             const u32x2 x = lds_read_tr(at), y = lds_read_tr(at + 16 * DG::PITCH);
             return u32x4{x.x, x.y, y.x, y.y};
         };
+        bool plain = true;
         if (masked) {
             // as in the prompts' kernel: what is not finite is left out where it is not seen, and makes a NaN where it is
             uint32_t bad = 0;
@@ -234,16 +236,22 @@ __device__ __forceinline__ void decode_run(const AttnDecodeParams &p)
                             o[r][j][i] = hit[i] > 0.f ? __builtin_nanf("") : o[r][j][i];
                     }
                 }
-                continue;
+                plain = false;
             }
         }
+        if (plain) {
 #pragma unroll
-        for (int j = 0; j < TV; ++j) {
-            const u32x4 v = v_of(j);
+            for (int j = 0; j < TV; ++j) {
+                const u32x4 v = v_of(j);
 #pragma unroll
-            for (int r = 0; r < NR; ++r)
-                o[r][j] = T::mfma16(v, pf[r], o[r][j]);
+                for (int r = 0; r < NR; ++r)
+                    o[r][j] = T::mfma16(v, pf[r], o[r][j]);
+            }
         }
+        // V has been read: the next one
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (step + 1 < steps)
+            fetch(step + 1, true);
     }
 
     // The waves' results, [wave][row][D], over the stages

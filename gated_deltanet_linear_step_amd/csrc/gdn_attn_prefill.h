@@ -117,8 +117,8 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
     const int wave_least = ahead + step * (min(wrow, rows - 1) / G);
     const int wave_most = wrow < rows ? ahead + step * ((min(wrow + kRows, rows) - 1) / G) : 0;
     const int block_most = max(0, min(nk, ahead + step * ((min(m0 + kBlock, rows) - 1) / G)));
-    const int tiles = (block_most + KT - 1) / KT, per = (tiles + p.splits - 1) / p.splits;
-    const int first = min(split * per, tiles), last = min(first + per, tiles);
+    const int tiles = (block_most + KT - 1) / KT;
+    const int first = (int)min((int64_t)split * p.split_tiles, (int64_t)tiles), last = min(tiles - first, p.split_tiles) + first;
 
     // What a lane fetches of each tile: FETCH blocks of the wave's ROWS rows
     const unsigned char *const kb = static_cast<const unsigned char *>(p.a.kv.k), *const vb = static_cast<const unsigned char *>(p.a.kv.v);
@@ -134,24 +134,23 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
         v_off[i] = r * v_row + G_::v_at(r_tile, b) - r_tile * G_::PITCH;
     }
     const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void *)lds, lds_at = lds0 + wave * G_::ROWS * G_::PITCH;
-    // On pages: lane g holds the page of the g-th 16 keys of a tile, -1 where it is none
+    // On pages: lane g holds the table's entry for the g-th 16 keys of a tile. An entry is looked at an iteration after it was
+    // asked for: a wait for it would be one for the tile on its way too.
     constexpr int GROUPS = KT / 16;
-    auto pages_of = [&](int tile) {
-        int page = 0;
-        if constexpr (PAGED) {
-            const int key = min(tile * KT + 16 * (lane & (GROUPS - 1)), nk - 1);
-            page = table[key >> p.a.kv.page_shift];
-            page = page < 0 || page >= p.a.kv.num_pages ? -1 : page;
-        }
-        return page;
+    auto entries_of = [&](int tile) {
+        int entry = 0;
+        if constexpr (PAGED)
+            entry = table[min(tile * KT + 16 * (lane & (GROUPS - 1)), nk - 1) >> p.a.kv.page_shift];
+        return entry;
     };
-    auto fetch = [&](int tile, int buf, int pages) {
+    auto no_page = [&](int entry) { return entry < 0 || entry >= p.a.kv.num_pages; };
+    auto fetch = [&](int tile, int buf, int entries) {
         int k0 = tile * KT + wave * G_::ROWS;
         const uint32_t to = lds_at + buf * G_::TILE;
         const unsigned char *k_from, *v_from;
         if constexpr (PAGED) {
             // keys behind the last one, and those of no page, are some other rows of the pool: they are masked
-            const int page = max(0, __builtin_amdgcn_readlane(pages, wave * G_::ROWS / 16));
+            const int entry = __builtin_amdgcn_readlane(entries, wave * G_::ROWS / 16), page = no_page(entry) ? 0 : entry;
             const int64_t in_page = head_at + (int64_t)(k0 & ((1 << p.a.kv.page_shift) - 1)) * D;
             k_from = kb + 2 * (page * p.a.kv.k_stride + in_page);
             v_from = vb + 2 * (page * p.a.kv.v_stride + in_page);
@@ -191,11 +190,11 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
     f32x16 o[TV] = {};
     float top = kNone, sum = 0.f;
 
-    int pages = 0, next_pages = 0;
+    int entries = 0, next_entries = 0;
     if (first < last) {
-        pages = pages_of(first);
-        fetch(first, 0, pages);
-        next_pages = pages_of(min(first + 1, last - 1));
+        entries = entries_of(first);
+        next_entries = entries_of(min(first + 1, last - 1));
+        fetch(first, 0, entries);
     }
     for (int tile = first; tile < last; ++tile) {
         const int buf = (tile - first) & 1, k0 = tile * KT;
@@ -203,11 +202,14 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
         __syncthreads();                                  // and everyone's; the other buffer is no longer read
         int none = 0;  // 16-key groups of the tile that have no page
         if constexpr (PAGED)
-            none = (int)(__ballot(pages < 0) & ((1u << GROUPS) - 1));
+            none = (int)(__ballot(no_page(entries)) & ((1u << GROUPS) - 1));
         if (tile + 1 < last) {
-            pages = next_pages;
-            fetch(tile + 1, buf ^ 1, pages);
-            next_pages = pages_of(min(tile + 2, last - 1));
+            entries = next_entries;
+            if constexpr (PAGED) {
+                asm volatile("" : "+v"(entries));
+                next_entries = entries_of(min(tile + 2, last - 1));
+            }
+            fetch(tile + 1, buf ^ 1, entries);
         }
         if (k0 >= wave_most)
             continue;
@@ -324,6 +326,8 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
         const int64_t slot = at * p.a.slots + p.first_slot + split;
         if (half == 0)
             p.a.stat[slot] = make_float2(top, sum);
+        if (first >= last)
+            return;
         float *to = p.a.part + slot * D;
 #pragma unroll
         for (int tv = 0; tv < TV; ++tv)
