@@ -31,14 +31,14 @@ struct Geo {
     static constexpr int PITCH = 2 * D, TILE = KT * PITCH;
     static constexpr int ROWS = KT / kWaves;        // rows of a tile that a wave fetches, within one page
     static constexpr int FETCH = ROWS * NB / 64;    // 16-byte fetches of a lane
-    // Where block b of a row lies. K: 16 rows' blocks b cover all banks; V: the blocks 2 b, 2 b + 1 of 8 rows do.
+    // Where block b of a row lies. K: 16 rows' blocks b cover all banks; V: the blocks 4 b .. 4 b + 3 of 4 rows do.
     __device__ __forceinline__ static int k_at(int row, int b)
     {
         return row * PITCH + 16 * (D == 64 ? b ^ ((row >> 1) & 7) : D == 96 ? b ^ ((row >> 2) & 3) : b ^ (row & 15));
     }
     __device__ __forceinline__ static int v_swizzle(int row)
     {
-        return D == 64 ? 2 * ((row >> 1) & 3) : D == 96 ? 2 * ((row >> 2) & 1) : 2 * (row & 7);
+        return D == 64 ? 4 * ((row >> 1) & 1) : D == 96 ? 0 : 4 * (row & 3);
     }
     __device__ __forceinline__ static int v_at(int row, int b) { return row * PITCH + 16 * (b ^ v_swizzle(row)); }
     // Blocks 2 c + x of a row, and 4 c + x of V, from where blocks x lie: the permutation is an exclusive or of a few bits
@@ -189,6 +189,11 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
     const float scale = p.a.scale * 1.4426950408889634f;  // exponentials in base 2
     f32x16 o[TV] = {};
     float top = kNone, sum = 0.f;
+
+    // Of the two waves of a SIMD one goes first wherever both could: equals would use the matrix unit at the same time, and
+    // then the vector unit, and neither beside the other
+    if (__builtin_amdgcn_s_getreg(4 | 3 << 11) & 1)  // the wave's slot
+        __builtin_amdgcn_s_setprio(1);
 
     int entries = 0, next_entries = 0;
     if (first < last) {
