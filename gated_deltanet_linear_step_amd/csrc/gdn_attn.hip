@@ -27,30 +27,55 @@ __device__ __forceinline__ void store_joined(const AttnParams &p, int64_t row, i
         p.lse[row] = total == 0.f ? kNone : (most + __log2f(total)) * 0.69314718055994531f;
 }
 
-// A few runs: D / 4 lanes join a row (a query and head) run after run, 256 lanes as many rows as they are for.
-template <int DT>
+// Up to 64 runs: a wave joins a row (a query and head). A lane looks at one run's maximum and sum; then D / 4 lanes
+// share a run's outputs, D <= 128 several runs side by side, all loads of eight turns in flight together.
+template <int DT, int D>
 __global__ __launch_bounds__(256) void join_few_kernel(const AttnParams p, int64_t rows)
 {
-    const int lanes = p.D / 4, group = threadIdx.x / lanes, d = 4 * (threadIdx.x % lanes), groups = 256 / lanes;
-    const int64_t row = (int64_t)blockIdx.x * groups + group, first = row * p.slots;
-    if (group >= groups || row >= rows)
+    constexpr int LANES = D / 4, GROUPS = 64 / LANES, TURNS = 8;
+    const int lane = threadIdx.x & 63, group = lane / LANES, d = 4 * (lane % LANES);
+    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), first = row * p.slots;
+    if (row >= rows)
         return;
-    float most = kNone;
-    for (int s = 0; s < p.slots; ++s) {
-        const float2 st = p.stat[first + s];
-        most = fmaxf(most, st.y == 0.f ? kNone : st.x);
-    }
+    const float2 st = lane < p.slots ? p.stat[first + lane] : make_float2(kNone, 0.f);
+    float most = st.y == 0.f ? kNone : st.x;
+#pragma unroll
+    for (int x = 32; x; x >>= 1)
+        most = fmaxf(most, __shfl_xor(most, x, 64));
+    const float f = st.y == 0.f ? 0.f : exp2_f(st.x - most);
+    float total = f * st.y;
+#pragma unroll
+    for (int x = 32; x; x >>= 1)
+        total += __shfl_xor(total, x, 64);
     f32x4 o = {};
-    float total = 0.f;
-    for (int s = 0; s < p.slots; ++s) {
-        const float2 st = p.stat[first + s];
-        if (st.y == 0.f)
-            continue;
-        const float f = exp2_f(st.x - most);
-        total += f * st.y;
-        o += f * *reinterpret_cast<const f32x4 *>(p.part + (first + s) * p.D + d);
+    for (int s0 = 0; s0 < p.slots; s0 += GROUPS * TURNS) {
+        f32x4 v[TURNS];
+        float w[TURNS];
+#pragma unroll
+        for (int i = 0; i < TURNS; ++i) {
+            const int s = s0 + i * GROUPS + group;
+            w[i] = __shfl(f, s & 63, 64);
+            if (group >= GROUPS || s >= p.slots)
+                w[i] = 0.f;
+            // a run without keys left its outputs as they were: the first run's are read again, and left out
+            v[i] = *reinterpret_cast<const f32x4 *>(p.part + (first + (w[i] == 0.f ? 0 : s)) * D + d);
+        }
+#pragma unroll
+        for (int i = 0; i < TURNS; ++i)
+            o += w[i] == 0.f ? f32x4{} : w[i] * v[i];
     }
-    store_joined<DT>(p, row, d, o, most, total);
+    if constexpr (GROUPS > 1) {
+#pragma unroll
+        for (int g = 1; g < GROUPS; g *= 2) {
+            // from the upper half of the groups (of 96 wide rows: lanes 24 on)
+            const int from = (lane + g * LANES) & 63;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                o[i] += __shfl(o[i], from, 64);
+        }
+    }
+    if (group == 0)
+        store_joined<DT>(p, row, d, o, most, total);
 }
 
 constexpr int kJoinThreads = 256, kJoinWidth = 32, kJoinRuns = kJoinThreads / (kJoinWidth / 4);
@@ -113,7 +138,18 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(const AttnParams p)
 
 constexpr int kBlock = 128;  // rows of a workgroup of the prefill kernel
 constexpr int kCus = 256;
-constexpr int kFewRuns = 32;
+
+template <int DT>
+hipError_t join_few(const AttnParams &p, int64_t rows, unsigned grid, hipStream_t s)
+{
+    switch (p.D) {
+    case 64: join_few_kernel<DT, 64><<<grid, 256, 0, s>>>(p, rows); break;
+    case 96: join_few_kernel<DT, 96><<<grid, 256, 0, s>>>(p, rows); break;
+    case 128: join_few_kernel<DT, 128><<<grid, 256, 0, s>>>(p, rows); break;
+    default: join_few_kernel<DT, 256><<<grid, 256, 0, s>>>(p, rows); break;
+    }
+    return hipGetLastError();
+}
 
 }  // namespace
 
@@ -215,14 +251,9 @@ hipError_t launch_attn_decode(const AttnDecodeParams &p, hipStream_t s)
 
 hipError_t launch_attn_join(const AttnParams &p, int64_t rows, hipStream_t s)
 {
-    if (p.slots <= kFewRuns) {
-        const int groups = 256 / (p.D / 4);
-        const unsigned grid = (unsigned)((rows + groups - 1) / groups);
-        if (p.dt == DT_BF16)
-            join_few_kernel<DT_BF16><<<grid, 256, 0, s>>>(p, rows);
-        else
-            join_few_kernel<DT_F16><<<grid, 256, 0, s>>>(p, rows);
-        return hipGetLastError();
+    if (p.slots <= 64) {
+        const unsigned grid = (unsigned)((rows + 3) / 4);
+        return p.dt == DT_BF16 ? join_few<DT_BF16>(p, rows, grid, s) : join_few<DT_F16>(p, rows, grid, s);
     }
     const unsigned grid = (unsigned)(rows * (p.D / kJoinWidth));
     if (p.dt == DT_BF16)

@@ -134,23 +134,24 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
         v_off[i] = r * v_row + G_::v_at(r_tile, b) - r_tile * G_::PITCH;
     }
     const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void *)lds, lds_at = lds0 + wave * G_::ROWS * G_::PITCH;
-    // On pages: lane g holds the table's entry for the g-th 16 keys of a tile. An entry is looked at an iteration after it was
-    // asked for: a wait for it would be one for the tile on its way too.
-    constexpr int GROUPS = KT / 16;
-    auto entries_of = [&](int tile) {
-        int entry = 0;
-        if constexpr (PAGED)
-            entry = table[min(tile * KT + 16 * (lane & (GROUPS - 1)), nk - 1) >> p.a.kv.page_shift];
-        return entry;
-    };
-    auto no_page = [&](int entry) { return entry < 0 || entry >= p.a.kv.num_pages; };
-    auto fetch = [&](int tile, int buf, int entries) {
+    // On pages: the lanes hold the table's entries for the 64 groups of 16 keys of so many tiles. They are asked for as a whole,
+    // before the first of those tiles is: a wait for an entry is one for every copy on its way too.
+    constexpr int GROUPS = KT / 16, HELD = 64 / GROUPS;
+    int entries = 0, none = 0;  // none: groups of the tile fetched last that have no page
+    auto fetch = [&](int tile, int buf) {
         int k0 = tile * KT + wave * G_::ROWS;
         const uint32_t to = lds_at + buf * G_::TILE;
         const unsigned char *k_from, *v_from;
         if constexpr (PAGED) {
+            const int held = (tile - first) % HELD * GROUPS;
+            if (held == 0) {
+                entries = table[(int)min((int64_t)tile * KT + 16 * lane, (int64_t)nk - 1) >> p.a.kv.page_shift];
+                asm volatile("" : "+v"(entries));
+            }
+            none = (int)(__ballot(entries < 0 || entries >= p.a.kv.num_pages) >> held) & ((1 << GROUPS) - 1);
             // keys behind the last one, and those of no page, are some other rows of the pool: they are masked
-            const int entry = __builtin_amdgcn_readlane(entries, wave * G_::ROWS / 16), page = no_page(entry) ? 0 : entry;
+            const int entry = __builtin_amdgcn_readlane(entries, held + wave * G_::ROWS / 16);
+            const int page = entry < 0 || entry >= p.a.kv.num_pages ? 0 : entry;
             const int64_t in_page = head_at + (int64_t)(k0 & ((1 << p.a.kv.page_shift) - 1)) * D;
             k_from = kb + 2 * (page * p.a.kv.k_stride + in_page);
             v_from = vb + 2 * (page * p.a.kv.v_stride + in_page);
@@ -195,27 +196,14 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
     if (__builtin_amdgcn_s_getreg(4 | 3 << 11) & 1)  // the wave's slot
         __builtin_amdgcn_s_setprio(1);
 
-    int entries = 0, next_entries = 0;
-    if (first < last) {
-        entries = entries_of(first);
-        next_entries = entries_of(min(first + 1, last - 1));
-        fetch(first, 0, entries);
-    }
+    if (first < last)
+        fetch(first, 0);
     for (int tile = first; tile < last; ++tile) {
-        const int buf = (tile - first) & 1, k0 = tile * KT;
+        const int buf = (tile - first) & 1, k0 = tile * KT, none_here = none;
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's part of the tile has landed
         __syncthreads();                                  // and everyone's; the other buffer is no longer read
-        int none = 0;  // 16-key groups of the tile that have no page
-        if constexpr (PAGED)
-            none = (int)(__ballot(no_page(entries)) & ((1u << GROUPS) - 1));
-        if (tile + 1 < last) {
-            entries = next_entries;
-            if constexpr (PAGED) {
-                asm volatile("" : "+v"(entries));
-                next_entries = entries_of(min(tile + 2, last - 1));
-            }
-            fetch(tile + 1, buf ^ 1, entries);
-        }
+        if (tile + 1 < last)
+            fetch(tile + 1, buf ^ 1);
         if (k0 >= wave_most)
             continue;
 
@@ -230,14 +218,14 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
                 s[t] = T::mfma32(lds_read16(G_::k_next(k_at, c) + 32 * t * G_::PITCH), q[c], s[t]);
 
         // some row of the wave does not see all of the tile
-        const bool masked = k0 + KT > wave_least || k0 + KT > nk || none != 0;
+        const bool masked = k0 + KT > wave_least || k0 + KT > nk || none_here != 0;
         if (masked) {
 #pragma unroll
             for (int t = 0; t < TS; ++t)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int key = 32 * t + 8 * (i / 4) + 4 * half + i % 4;
-                    s[t][i] = k0 + key < seen && !(none >> (key / 16) & 1) ? s[t][i] : kNone;
+                    s[t][i] = k0 + key < seen && !(none_here >> (key / 16) & 1) ? s[t][i] : kNone;
                 }
         }
         float most = s[0][0];
@@ -290,7 +278,7 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
                         const int key = 16 * st + 8 * (w / 2) + 4 * half + 2 * (w % 2);
-                        const bool page = !(none >> st & 1);
+                        const bool page = !(none_here >> st & 1);
                         sees[st][w] = (page && k0 + key < seen ? one & 0xffffu : 0u) | (page && k0 + key + 1 < seen ? one & 0xffff0000u : 0u);
                     }
 #pragma unroll
