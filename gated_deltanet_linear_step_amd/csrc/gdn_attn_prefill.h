@@ -65,8 +65,8 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
 {
     using G_ = Geo<D>;
     using T = Type16<DT>;
-    constexpr int KT = G_::KT, NB = G_::NB, KC = D / 16, TV = D / 32, TS = KT / 32;
-    __shared__ __align__(1024) unsigned char lds[4 * G_::TILE];  // K, K, V, V
+    constexpr int KT = G_::KT, NB = G_::NB, KC = D / 16, TV = D / 32, HALVES = KT / 32;
+    __shared__ __align__(1024) unsigned char lds[5 * G_::TILE];  // K twice, V three times
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = lane >> 5, col = lane & 31;
@@ -114,7 +114,6 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
     const int row = min(wrow + col, rows - 1);
     const int token = row / G, head = kvh * G + row - token * G;
     const int seen = min(nk, ahead + step * token);
-    const int wave_least = ahead + step * (min(wrow, rows - 1) / G);
     const int wave_most = wrow < rows ? ahead + step * ((min(wrow + kRows, rows) - 1) / G) : 0;
     const int block_most = max(0, min(nk, ahead + step * ((min(m0 + kBlock, rows) - 1) / G)));
     const int tiles = (block_most + KT - 1) / KT;
@@ -137,10 +136,12 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
     // On pages: the lanes hold the table's entries for the 64 groups of 16 keys of so many tiles. They are asked for as a whole,
     // before the first of those tiles is: a wait for an entry is one for every copy on its way too.
     constexpr int GROUPS = KT / 16, HELD = 64 / GROUPS;
-    int entries = 0, none = 0;  // none: groups of the tile fetched last that have no page
-    auto fetch = [&](int tile, int buf) {
+    int entries = 0;
+    // Starts the copies of a tile into K and V buffers; returns the groups of it that have no page, a bit each
+    auto fetch = [&](int tile, int k_buf, int v_buf) {
+        int none = 0;
         int k0 = tile * KT + wave * G_::ROWS;
-        const uint32_t to = lds_at + buf * G_::TILE;
+        const uint32_t k_to = lds_at + k_buf * G_::TILE, v_to = lds_at + (2 + v_buf) * G_::TILE;
         const unsigned char *k_from, *v_from;
         if constexpr (PAGED) {
             const int held = (tile - first) % HELD * GROUPS;
@@ -163,17 +164,18 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
 #pragma unroll
                 for (int i = 0; i < G_::FETCH; ++i) {
                     const uint32_t over = max(0, (64 * i + opaque(lane)) / NB - (nk - 1 - k0));
-                    copy16(k_from, k_off[i] - over * k_row, to + 1024 * i);
-                    copy16(v_from, v_off[i] - over * v_row, to + 1024 * i + 2 * G_::TILE);
+                    copy16(k_from, k_off[i] - over * k_row, k_to + 1024 * i);
+                    copy16(v_from, v_off[i] - over * v_row, v_to + 1024 * i);
                 }
-                return;
+                return none;
             }
         }
 #pragma unroll
         for (int i = 0; i < G_::FETCH; ++i) {
-            copy16(k_from, k_off[i], to + 1024 * i);
-            copy16(v_from, v_off[i], to + 1024 * i + 2 * G_::TILE);
+            copy16(k_from, k_off[i], k_to + 1024 * i);
+            copy16(v_from, v_off[i], v_to + 1024 * i);
         }
+        return none;
     };
 
     u32x4 q[KC];
@@ -191,49 +193,15 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
     f32x16 o[TV] = {};
     float top = kNone, sum = 0.f;
 
-    // Of the two waves of a SIMD one goes first wherever both could: equals would use the matrix unit at the same time, and
-    // then the vector unit, and neither beside the other
-    if (__builtin_amdgcn_s_getreg(4 | 3 << 11) & 1)  // the wave's slot
-        __builtin_amdgcn_s_setprio(1);
-
-    if (first < last)
-        fetch(first, 0);
-    for (int tile = first; tile < last; ++tile) {
-        const int buf = (tile - first) & 1, k0 = tile * KT, none_here = none;
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's part of the tile has landed
-        __syncthreads();                                  // and everyone's; the other buffer is no longer read
-        if (tile + 1 < last)
-            fetch(tile + 1, buf ^ 1);
-        if (k0 >= wave_most)
-            continue;
-
-        // the LDS addresses of a tile are formed as they are needed (D = 256 has no registers for them)
-        const uint32_t kt = lds0 + buf * G_::TILE, vt = lds0 + (2 + buf) * G_::TILE;
-        const uint32_t k_at = opaque(kt + G_::k_at(col, half));
-        f32x16 s[TS] = {};
+    auto largest = [&](const f32x16 &s) {
+        float x = fmaxf(s[0], s[1]);
 #pragma unroll
-        for (int t = 0; t < TS; ++t)
-#pragma unroll
-            for (int c = 0; c < KC; ++c)
-                s[t] = T::mfma32(lds_read16(G_::k_next(k_at, c) + 32 * t * G_::PITCH), q[c], s[t]);
-
-        // some row of the wave does not see all of the tile
-        const bool masked = k0 + KT > wave_least || k0 + KT > nk || none_here != 0;
-        if (masked) {
-#pragma unroll
-            for (int t = 0; t < TS; ++t)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int key = 32 * t + 8 * (i / 4) + 4 * half + i % 4;
-                    s[t][i] = k0 + key < seen && !(none_here >> (key / 16) & 1) ? s[t][i] : kNone;
-                }
-        }
-        float most = s[0][0];
-#pragma unroll
-        for (int t = 0; t < TS; ++t)
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                most = fmaxf(most, s[t][i]);
+        for (int i = 2; i < 16; i += 2)
+            x = fmaxf(fmaxf(x, s[i]), s[i + 1]);
+        return x;
+    };
+    // Takes the largest of 32 scores into the running maximum where it passes that by 8
+    auto rescale = [&](float most) {
         most = half_max(most) * scale;
         if (__ballot(most > top + 8.f) != 0) {
             const float up = fmaxf(top, most), f = up == kNone ? 1.f : exp2_f(top - up);
@@ -243,70 +211,199 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
             for (int t = 0; t < TV; ++t)
                 o[t] *= f;
         }
-        const float base = top == kNone ? 0.f : top;
-        u32x4 pf[KT / 16];
+        return top == kNone ? 0.f : top;
+    };
+    auto scores = [&](f32x16 &s, uint32_t kt) {
+        const uint32_t k_at = opaque(kt + G_::k_at(col, half));
+        s = f32x16{};
 #pragma unroll
-        for (int t = 0; t < TS; ++t)
+        for (int c = 0; c < KC; ++c)
+            s = T::mfma32(lds_read16(G_::k_next(k_at, c)), q[c], s);
+    };
+    // V^T, 32 dv from 32 tv on and the 16 keys of st, in P's order
+    const int v_lane = G_::v_at(4 * half + ((lane & 15) >> 2), 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) + 8 * (lane & 1);
+    auto v_of = [&](uint32_t v_at, int tv, int st) {
+        const uint32_t at = G_::v_next(v_at, tv) + 16 * st * G_::PITCH;
+        const u32x2 x = lds_read_tr(at), y = lds_read_tr(at + 8 * G_::PITCH);
+        return u32x4{x.x, x.y, y.x, y.y};
+    };
+
+    // 32 keys that every row of the block sees, with scores s and the largest of them, and values at vt. The scores `next` of
+    // the next 32 keys, which lie at next_kt, are formed while the exponentials of these are, a product and what
+    // fits beside it in turn (the scheduler would put the products first), and their largest is found beside the products with V.
+    // D = 256 has no registers for two sets of scores: the next ones are formed at the end, in the same place.
+    constexpr bool AHEAD = D <= 128;
+    float most = kNone;
+    auto attend = [&](f32x16 &s, f32x16 &next, uint32_t vt, uint32_t next_kt) {
+        const float base = rescale(most);
+        u32x4 pf[2];
+        const uint32_t v_at = opaque(vt + v_lane);
+        if constexpr (AHEAD) {
+            constexpr int READ = 3;  // products that a K operand is read ahead
+            const uint32_t k_at = opaque(next_kt + G_::k_at(col, half));
+            u32x4 kf[KC];
+            float e[16];
+#pragma unroll
+            for (int c = 0; c < READ; ++c)
+                kf[c] = lds_read16(G_::k_next(k_at, c));
+            __builtin_amdgcn_sched_barrier(0);
+            next = f32x16{};
+#pragma unroll
+            for (int c = 0; c <= KC; ++c) {
+                if (c + READ < KC)
+                    kf[c + READ] = lds_read16(G_::k_next(k_at, c + READ));
+                if (c < KC)
+                    next = T::mfma32(kf[c], q[c], next);
+                // a share of the eight pairs of exponentials, and what follows from those of the product before
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (c < KC && i * KC / 8 == c) {
+                        e[2 * i] = exp2_f(fmaf(s[2 * i], scale, -base));
+                        e[2 * i + 1] = exp2_f(fmaf(s[2 * i + 1], scale, -base));
+                    }
+                    if (i * KC / 8 + 1 == c) {
+                        sum += e[2 * i];
+                        sum += e[2 * i + 1];
+                        pf[i / 4][i % 4] = pack2<DT>(e[2 * i], e[2 * i + 1]);
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            constexpr int VREAD = 2, N = 2 * TV;
+            u32x4 vf[N];
+#pragma unroll
+            for (int i = 0; i < VREAD; ++i)
+                vf[i] = v_of(v_at, i % TV, i / TV);
+            __builtin_amdgcn_sched_barrier(0);
+            most = fmaxf(next[0], next[1]);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                if (i + VREAD < N)
+                    vf[i + VREAD] = v_of(v_at, (i + VREAD) % TV, (i + VREAD) / TV);
+                o[i % TV] = T::mfma32(vf[i], pf[i / TV], o[i % TV]);
+#pragma unroll
+                for (int x = 1; x < 8; ++x)
+                    if (i == min(x * N / 8 + 1, N - 1))
+                        most = fmaxf(fmaxf(most, next[2 * x]), next[2 * x + 1]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        } else {
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
-                const float a = exp2_f(fmaf(s[t][i], scale, -base)), b = exp2_f(fmaf(s[t][i + 1], scale, -base));
-                sum += a;
-                sum += b;
-                pf[2 * t + i / 8][i % 8 / 2] = pack2<DT>(a, b);
+                const float x = exp2_f(fmaf(s[i], scale, -base)), y = exp2_f(fmaf(s[i + 1], scale, -base));
+                sum += x;
+                sum += y;
+                pf[i / 8][i % 8 / 2] = pack2<DT>(x, y);
             }
+#pragma unroll
+            for (int st = 0; st < 2; ++st)
+#pragma unroll
+                for (int tv = 0; tv < TV; ++tv)
+                    o[tv] = T::mfma32(v_of(v_at, tv, st), pf[st], o[tv]);
+            scores(next, next_kt);
+            most = largest(next);
+        }
+    };
 
-        // V^T, 32 dv from 32 tv on and the 16 keys of step st, in P's order
-        const uint32_t v_at = opaque(vt + G_::v_at(4 * half + ((lane & 15) >> 2), 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) + 8 * (lane & 1));
-        auto v_of = [&](int tv, int st) {
-            const uint32_t at = G_::v_next(v_at, tv) + 16 * st * G_::PITCH;
-            const u32x2 x = lds_read_tr(at), y = lds_read_tr(at + 8 * G_::PITCH);
-            return u32x4{x.x, x.y, y.x, y.y};
-        };
-        if (masked) {
-            // 0 times what is not finite in a masked place must not reach a row: those values are left out, and
-            // a row that sees one of them becomes NaN
-            uint32_t bad = 0;
-            for (int at = 16 * lane; at < G_::TILE; at += 1024) {
-                const u32x4 w = lds_read16(vt + at);
-                bad |= not_finite<DT>(w.x) | not_finite<DT>(w.y) | not_finite<DT>(w.z) | not_finite<DT>(w.w);
-            }
-            if (__ballot(bad != 0) != 0) {
-                const uint32_t one = pack2<DT>(1.f, 1.f);
-                u32x4 sees[KT / 16];
+    // 32 keys from k0 on, of which a row may not see some; `none`: two bits, the groups of 16 without a page.
+    auto attend_masked = [&](int k0, int none, uint32_t kt, uint32_t vt) {
+        f32x16 s;
+        scores(s, kt);
 #pragma unroll
-                for (int st = 0; st < KT / 16; ++st)
+        for (int i = 0; i < 16; ++i) {
+            const int key = 8 * (i / 4) + 4 * half + i % 4;
+            s[i] = k0 + key < seen && !(none >> (i / 8) & 1) ? s[i] : kNone;
+        }
+        const float base = rescale(largest(s));
+        u32x4 pf[2], sees[2];
+        const uint32_t one = pack2<DT>(1.f, 1.f);
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const int key = 16 * st + 8 * (w / 2) + 4 * half + 2 * (w % 2);
-                        const bool page = !(none_here >> st & 1);
-                        sees[st][w] = (page && k0 + key < seen ? one & 0xffffu : 0u) | (page && k0 + key + 1 < seen ? one & 0xffff0000u : 0u);
-                    }
+        for (int i = 0; i < 16; i += 2) {
+            const float x = exp2_f(fmaf(s[i], scale, -base)), y = exp2_f(fmaf(s[i + 1], scale, -base));
+            sum += x;
+            sum += y;
+            pf[i / 8][i % 8 / 2] = pack2<DT>(x, y);
+            const int key = k0 + 8 * (i / 4) + 4 * half + i % 4, upto = none >> (i / 8) & 1 ? 0 : seen;
+            sees[i / 8][i % 8 / 2] = (key < upto ? one & 0xffffu : 0u) | (key + 1 < upto ? one & 0xffff0000u : 0u);
+        }
+        // 0 times what is not finite in a masked place must not reach a row: those values are left out, and
+        // a row that sees one of them becomes NaN
+        uint32_t bad = 0;
+        for (int at = 16 * lane; at < 32 * G_::PITCH; at += 1024) {
+            const u32x4 w = lds_read16(vt + at);
+            bad |= not_finite<DT>(w.x) | not_finite<DT>(w.y) | not_finite<DT>(w.z) | not_finite<DT>(w.w);
+        }
+        const uint32_t keep = __ballot(bad != 0) != 0 ? 0 : ~0u;
+        const uint32_t v_at = opaque(vt + v_lane);
 #pragma unroll
-                for (int tv = 0; tv < TV; ++tv) {
-                    f32x16 hit = {};
+        for (int tv = 0; tv < TV; ++tv) {
+            f32x16 hit = {};
 #pragma unroll
-                    for (int st = 0; st < KT / 16; ++st) {
-                        u32x4 v = v_of(tv, st), wrong;
+            for (int st = 0; st < 2; ++st) {
+                u32x4 v = v_of(v_at, tv, st), wrong;
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            wrong[w] = (not_finite<DT>(v[w]) >> 15) * 0xffffu & one;
-                            v[w] = finite_part<DT>(v[w]);
-                        }
-                        o[tv] = T::mfma32(v, pf[st], o[tv]);
-                        hit = T::mfma32(wrong, sees[st], hit);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        o[tv][i] = hit[i] > 0.f ? __builtin_nanf("") : o[tv][i];
+                for (int w = 0; w < 4; ++w) {
+                    wrong[w] = (not_finite<DT>(v[w]) >> 15) * 0xffffu;
+                    v[w] &= ~wrong[w];
+                    wrong[w] &= one;
                 }
-                continue;
+                o[tv] = T::mfma32(v, pf[st], o[tv]);
+                if (keep == 0)
+                    hit = T::mfma32(wrong, sees[st], hit);
+            }
+            if (keep == 0) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    o[tv][i] = hit[i] > 0.f ? __builtin_nanf("") : o[tv][i];
             }
         }
-#pragma unroll
-        for (int st = 0; st < KT / 16; ++st)
-#pragma unroll
-            for (int tv = 0; tv < TV; ++tv)
-                o[tv] = T::mfma32(v_of(tv, st), pf[st], o[tv]);
+    };
+
+    // K and V of a tile are here at the end of the tile before (with D = 256 of the one before that, K being read a tile ahead). At
+    // a tile's last 32 keys its K is no longer read, nor is V of the tile before: the tile after the next takes their places.
+    int none = 0, next_none = 0, v_buf = 0;
+    if (first < last) {
+        none = fetch(first, 0, 0);
+        if (first + 1 < last) {
+            next_none = fetch(first + 1, 1, 1);
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * G_::FETCH) : "memory");
+        } else {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        }
+        __syncthreads();
+    }
+    auto turn = [&](int tile) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's part of the next tile has landed
+        __syncthreads();                                  // and everyone's
+        const int after = tile + 2 < last ? fetch(tile + 2, (tile - first) & 1, v_buf == 0 ? 2 : v_buf - 1) : 0;
+        none = next_none;
+        next_none = after;
+        v_buf = v_buf == 2 ? 0 : v_buf + 1;
+    };
+    // tiles that every row of the block sees, up to a page that is none; the same for every wave
+    const int block_least = min(nk, ahead + step * (m0 / G)), full = min(last, max(0, block_least) / KT);
+    int tile = first;
+    if (tile < full && none == 0) {
+        f32x16 s[HALVES];
+        static_assert(AHEAD == (HALVES == 2), "two sets of scores, or one");
+        scores(s[0], lds0);
+        most = largest(s[0]);
+        do {
+            const uint32_t kt = lds0 + ((tile - first) & 1) * G_::TILE, vt = lds0 + (2 + v_buf) * G_::TILE;
+            if constexpr (HALVES == 2)
+                attend(s[0], s[1], vt, kt + 32 * G_::PITCH);
+            turn(tile);
+            attend(s[HALVES - 1], s[0], vt + (KT - 32) * G_::PITCH, lds0 + ((tile + 1 - first) & 1) * G_::TILE);
+            ++tile;
+        } while (tile < full && none == 0);
+    }
+    for (; tile < last; ++tile) {
+        const uint32_t kt = lds0 + ((tile - first) & 1) * G_::TILE, vt = lds0 + (2 + v_buf) * G_::TILE;
+#pragma unroll 1
+        for (int h = 0; h < HALVES; ++h)
+            if (tile * KT + 32 * h < wave_most)
+                attend_masked(tile * KT + 32 * h, none >> 2 * h, kt + 32 * h * G_::PITCH, vt + 32 * h * G_::PITCH);
+        turn(tile);
     }
 
     sum = half_sum(sum);
