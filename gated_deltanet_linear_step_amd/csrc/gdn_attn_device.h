@@ -106,6 +106,33 @@ __device__ __forceinline__ void copy16(const unsigned char *base, uint32_t off, 
                  : "memory");
 }
 
+// The same for N runs of 1024 bytes, one after another from byte `to` on: off[i] is the offset of the i-th, at least 1024 i.
+// (An instruction's own offset counts in memory and in the LDS.)
+template <int N>
+__device__ __forceinline__ void copy16_runs(const unsigned char *base, const uint32_t (&off)[N], uint32_t to)
+{
+    static_assert(N >= 2 && N <= 4, "offsets below 4096");
+    if constexpr (N == 2)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %3\n\t"
+                     "global_load_lds_dwordx4 %2, %3 offset:1024"
+                     :
+                     : "s"(to), "v"(off[0]), "v"(off[1] - 1024), "s"(base)
+                     : "memory");
+    else if constexpr (N == 3)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %4\n\t"
+                     "global_load_lds_dwordx4 %2, %4 offset:1024\n\tglobal_load_lds_dwordx4 %3, %4 offset:2048"
+                     :
+                     : "s"(to), "v"(off[0]), "v"(off[1] - 1024), "v"(off[2] - 2048), "s"(base)
+                     : "memory");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %5\n\t"
+                     "global_load_lds_dwordx4 %2, %5 offset:1024\n\tglobal_load_lds_dwordx4 %3, %5 offset:2048\n\t"
+                     "global_load_lds_dwordx4 %4, %5 offset:3072"
+                     :
+                     : "s"(to), "v"(off[0]), "v"(off[1] - 1024), "v"(off[2] - 2048), "v"(off[3] - 3072), "s"(base)
+                     : "memory");
+}
+
 // Maximum and sum over a lane and the one 32 away (the swap leaves the lower half's values in one word, the upper half's
 // in the other)
 __device__ __forceinline__ float half_max(float x)

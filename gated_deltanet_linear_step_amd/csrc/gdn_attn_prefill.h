@@ -137,45 +137,49 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
     // before the first of those tiles is: a wait for an entry is one for every copy on its way too.
     constexpr int GROUPS = KT / 16, HELD = 64 / GROUPS;
     int entries = 0;
-    // Starts the copies of a tile into K and V buffers; returns the groups of it that have no page, a bit each
-    auto fetch = [&](int tile, int k_buf, int v_buf) {
-        int none = 0;
+    // Where a wave's rows of a tile come from, found before the tile's turn
+    struct From {
+        const unsigned char *k, *v;
+        int none;  // groups of the tile that have no page, a bit each
+        int over;  // rows of the wave behind the last key (packed rows: none of them is read)
+    };
+    auto locate = [&](int tile) {
         int k0 = tile * KT + wave * G_::ROWS;
-        const uint32_t k_to = lds_at + k_buf * G_::TILE, v_to = lds_at + (2 + v_buf) * G_::TILE;
-        const unsigned char *k_from, *v_from;
+        From from{kb, vb, 0, 0};
         if constexpr (PAGED) {
             const int held = (tile - first) % HELD * GROUPS;
             if (held == 0) {
                 entries = table[(int)min((int64_t)tile * KT + 16 * lane, (int64_t)nk - 1) >> p.a.kv.page_shift];
                 asm volatile("" : "+v"(entries));
             }
-            none = (int)(__ballot(entries < 0 || entries >= p.a.kv.num_pages) >> held) & ((1 << GROUPS) - 1);
+            from.none = (int)(__ballot(entries < 0 || entries >= p.a.kv.num_pages) >> held) & ((1 << GROUPS) - 1);
             // keys behind the last one, and those of no page, are some other rows of the pool: they are masked
             const int entry = __builtin_amdgcn_readlane(entries, held + wave * G_::ROWS / 16);
             const int page = entry < 0 || entry >= p.a.kv.num_pages ? 0 : entry;
             const int64_t in_page = head_at + (int64_t)(k0 & ((1 << p.a.kv.page_shift) - 1)) * D;
-            k_from = kb + 2 * (page * p.a.kv.k_stride + in_page);
-            v_from = vb + 2 * (page * p.a.kv.v_stride + in_page);
+            from.k += 2 * (page * p.a.kv.k_stride + in_page);
+            from.v += 2 * (page * p.a.kv.v_stride + in_page);
         } else {
             k0 = min(k0, nk - 1);
-            k_from = kb + 2 * ((key0 + k0) * p.a.kv.k_stride + head_at);
-            v_from = vb + 2 * ((key0 + k0) * p.a.kv.v_stride + head_at);
-            if (k0 + G_::ROWS > nk) {  // no row behind the last key
+            from.k += 2 * ((key0 + k0) * p.a.kv.k_stride + head_at);
+            from.v += 2 * ((key0 + k0) * p.a.kv.v_stride + head_at);
+            from.over = max(0, k0 + G_::ROWS - nk);
+        }
+        return from;
+    };
+    auto fetch = [&](const From &from, int k_buf, int v_buf) {
+        const uint32_t k_to = lds_at + k_buf * G_::TILE, v_to = lds_at + (2 + v_buf) * G_::TILE;
+        if (!PAGED && from.over > 0) {
 #pragma unroll
-                for (int i = 0; i < G_::FETCH; ++i) {
-                    const uint32_t over = max(0, (64 * i + opaque(lane)) / NB - (nk - 1 - k0));
-                    copy16(k_from, k_off[i] - over * k_row, k_to + 1024 * i);
-                    copy16(v_from, v_off[i] - over * v_row, v_to + 1024 * i);
-                }
-                return none;
+            for (int i = 0; i < G_::FETCH; ++i) {
+                const uint32_t over = max(0, (64 * i + opaque(lane)) / NB - (G_::ROWS - 1 - from.over));
+                copy16(from.k, k_off[i] - over * k_row, k_to + 1024 * i);
+                copy16(from.v, v_off[i] - over * v_row, v_to + 1024 * i);
             }
+            return;
         }
-#pragma unroll
-        for (int i = 0; i < G_::FETCH; ++i) {
-            copy16(k_from, k_off[i], k_to + 1024 * i);
-            copy16(v_from, v_off[i], v_to + 1024 * i);
-        }
-        return none;
+        copy16_runs(from.k, k_off, k_to);
+        copy16_runs(from.v, v_off, v_to);
     };
 
     u32x4 q[KC];
@@ -228,30 +232,38 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
         return u32x4{x.x, x.y, y.x, y.y};
     };
 
-    // 32 keys that every row of the block sees, with scores s and the largest of them, and values at vt. The scores `next` of
-    // the next 32 keys, which lie at next_kt, are formed while the exponentials of these are, a product and what
-    // fits beside it in turn (the scheduler would put the products first), and their largest is found beside the products with V.
+    // 32 keys that every row of the block sees, with scores s and values at vt. The scores `next` of the next 32 keys, which
+    // lie at next_kt, are formed while the exponentials of these are, a product and what fits beside it in turn (the
+    // scheduler would put the products first), and their largest is found beside the products with V. LDS reads run ahead of
+    // the products, the first ones of a step (kf) of the step before.
     // D = 256 has no registers for two sets of scores: the next ones are formed at the end, in the same place.
     constexpr bool AHEAD = D <= 128;
-    float most = kNone;
-    auto attend = [&](f32x16 &s, f32x16 &next, uint32_t vt, uint32_t next_kt) {
-        const float base = rescale(most);
+    constexpr int READ = 3;  // operands read ahead
+    u32x4 kf[KC];
+    float base = 0.f;
+    auto read_k = [&](uint32_t kt) {
+        const uint32_t k_at = opaque(kt + G_::k_at(col, half));
+#pragma unroll
+        for (int c = 0; c < READ; ++c)
+            kf[c] = lds_read16(G_::k_next(k_at, c));
+    };
+    // read_on: the keys after the next are here, at then_kt. go_on: the next keys are attended to by a call of this (scores of keys
+    // that a row does not see must not move its maximum)
+    auto attend = [&](f32x16 &s, f32x16 &next, uint32_t vt, uint32_t next_kt, bool read_on, uint32_t then_kt, bool go_on) {
         u32x4 pf[2];
         const uint32_t v_at = opaque(vt + v_lane);
         if constexpr (AHEAD) {
-            constexpr int READ = 3;  // products that a K operand is read ahead
+            constexpr int N = 2 * TV;
             const uint32_t k_at = opaque(next_kt + G_::k_at(col, half));
-            u32x4 kf[KC];
+            u32x4 vf[N];
             float e[16];
-#pragma unroll
-            for (int c = 0; c < READ; ++c)
-                kf[c] = lds_read16(G_::k_next(k_at, c));
-            __builtin_amdgcn_sched_barrier(0);
             next = f32x16{};
 #pragma unroll
             for (int c = 0; c <= KC; ++c) {
                 if (c + READ < KC)
                     kf[c + READ] = lds_read16(G_::k_next(k_at, c + READ));
+                else if (c < KC)
+                    vf[c + READ - KC] = v_of(v_at, (c + READ - KC) % TV, (c + READ - KC) / TV);
                 if (c < KC)
                     next = T::mfma32(kf[c], q[c], next);
                 // a share of the eight pairs of exponentials, and what follows from those of the product before
@@ -269,17 +281,14 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
-            constexpr int VREAD = 2, N = 2 * TV;
-            u32x4 vf[N];
-#pragma unroll
-            for (int i = 0; i < VREAD; ++i)
-                vf[i] = v_of(v_at, i % TV, i / TV);
-            __builtin_amdgcn_sched_barrier(0);
-            most = fmaxf(next[0], next[1]);
+            const uint32_t then_at = opaque(then_kt + G_::k_at(col, half));
+            float most = fmaxf(next[0], next[1]);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                if (i + VREAD < N)
-                    vf[i + VREAD] = v_of(v_at, (i + VREAD) % TV, (i + VREAD) / TV);
+                if (i + READ < N)
+                    vf[i + READ] = v_of(v_at, (i + READ) % TV, (i + READ) / TV);
+                else if (read_on)
+                    kf[i + READ - N] = lds_read16(G_::k_next(then_at, i + READ - N));
                 o[i % TV] = T::mfma32(vf[i], pf[i / TV], o[i % TV]);
 #pragma unroll
                 for (int x = 1; x < 8; ++x)
@@ -287,6 +296,8 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
                         most = fmaxf(fmaxf(most, next[2 * x]), next[2 * x + 1]);
                 __builtin_amdgcn_sched_barrier(0);
             }
+            if (go_on)
+                base = rescale(most);
         } else {
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
@@ -301,7 +312,8 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
                 for (int tv = 0; tv < TV; ++tv)
                     o[tv] = T::mfma32(v_of(v_at, tv, st), pf[st], o[tv]);
             scores(next, next_kt);
-            most = largest(next);
+            if (go_on)
+                base = rescale(largest(next));
         }
     };
 
@@ -363,21 +375,32 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
     // a tile's last 32 keys its K is no longer read, nor is V of the tile before: the tile after the next takes their places.
     int none = 0, next_none = 0, v_buf = 0;
     if (first < last) {
-        none = fetch(first, 0, 0);
+        const From from = locate(first);
+        fetch(from, 0, 0);
+        none = from.none;
         if (first + 1 < last) {
-            next_none = fetch(first + 1, 1, 1);
+            const From second = locate(first + 1);
+            fetch(second, 1, 1);
+            next_none = second.none;
             asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * G_::FETCH) : "memory");
         } else {
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         }
         __syncthreads();
     }
-    auto turn = [&](int tile) {
+    // read_on: the next step's first operands are read as soon as the tile is here, at kt
+    auto turn = [&](int tile, bool read_on, uint32_t kt) {
+        From from{kb, vb, 0, 0};
+        if (tile + 2 < last)
+            from = locate(tile + 2);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's part of the next tile has landed
         __syncthreads();                                  // and everyone's
-        const int after = tile + 2 < last ? fetch(tile + 2, (tile - first) & 1, v_buf == 0 ? 2 : v_buf - 1) : 0;
+        if (read_on)
+            read_k(kt);
+        if (tile + 2 < last)
+            fetch(from, (tile - first) & 1, v_buf == 0 ? 2 : v_buf - 1);
         none = next_none;
-        next_none = after;
+        next_none = from.none;
         v_buf = v_buf == 2 ? 0 : v_buf + 1;
     };
     // tiles that every row of the block sees, up to a page that is none; the same for every wave
@@ -387,13 +410,17 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
         f32x16 s[HALVES];
         static_assert(AHEAD == (HALVES == 2), "two sets of scores, or one");
         scores(s[0], lds0);
-        most = largest(s[0]);
+        base = rescale(largest(s[0]));
+        if constexpr (AHEAD)
+            read_k(lds0 + 32 * G_::PITCH);
         do {
             const uint32_t kt = lds0 + ((tile - first) & 1) * G_::TILE, vt = lds0 + (2 + v_buf) * G_::TILE;
+            const uint32_t next_kt = lds0 + ((tile + 1 - first) & 1) * G_::TILE;
             if constexpr (HALVES == 2)
-                attend(s[0], s[1], vt, kt + 32 * G_::PITCH);
-            turn(tile);
-            attend(s[HALVES - 1], s[0], vt + (KT - 32) * G_::PITCH, lds0 + ((tile + 1 - first) & 1) * G_::TILE);
+                attend(s[0], s[1], vt, kt + 32 * G_::PITCH, false, 0, true);
+            turn(tile, AHEAD, next_kt);
+            attend(s[HALVES - 1], s[0], vt + (KT - 32) * G_::PITCH, next_kt, true, next_kt + 32 * G_::PITCH,
+                   tile + 1 < full && none == 0);
             ++tile;
         } while (tile < full && none == 0);
     }
@@ -403,7 +430,7 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
         for (int h = 0; h < HALVES; ++h)
             if (tile * KT + 32 * h < wave_most)
                 attend_masked(tile * KT + 32 * h, none >> 2 * h, kt + 32 * h * G_::PITCH, vt + 32 * h * G_::PITCH);
-        turn(tile);
+        turn(tile, false, 0);
     }
 
     sum = half_sum(sum);
