@@ -168,16 +168,33 @@ void attn_prefill_splits(int Hq, int Hkv, int D, int N, int64_t total, const int
     // have one; a run is at least four tiles.
     const int most = attn_prefill_most_splits(Hq, Hkv, total), KT = D <= 128 ? 64 : 32;
     const int64_t G = Hq / Hkv;
+    *splits = 1;
+    *split_tiles = 1 << 30;
+    if (most == 1)
+        return;
+    // (of queries that see all keys: few queries against many keys are what is split)
+    const auto over = [&](auto f) {
+        for (int s = 0; s < N; ++s) {
+            const int64_t len = cu_q ? cu_q[s + 1] - cu_q[s] : total, nk = cu_q ? cu_k[s + 1] - cu_k[s] : keys;
+            f((nk + KT - 1) / KT, (len * G + kBlock - 1) / kBlock * Hkv);
+        }
+    };
     int64_t all = 0, longest = 0;
-    for (int s = 0; s < N; ++s) {
-        const int64_t len = cu_q ? cu_q[s + 1] - cu_q[s] : total, nk = cu_q ? cu_k[s + 1] - cu_k[s] : keys;
-        const int64_t tiles = (nk + KT - 1) / KT, blocks = (len * G + kBlock - 1) / kBlock;
-        all += tiles * blocks * Hkv;  // (of queries that see all keys: few queries against many keys are what is split)
+    over([&](int64_t tiles, int64_t blocks) {
+        all += tiles * blocks;
         longest = std::max(longest, blocks > 0 ? tiles : 0);
+    });
+    int64_t each = std::max<int64_t>({(all + 2 * kCus - 1) / (2 * kCus), 4, (longest + most - 1) / most});
+    for (; each < longest; ++each) {  // one workgroup too many would take a round of its own
+        int64_t workgroups = 0;
+        over([&](int64_t tiles, int64_t blocks) { workgroups += (tiles + each - 1) / each * blocks; });
+        if (workgroups <= 2 * kCus)
+            break;
     }
-    const int64_t each = std::max<int64_t>({(all + 2 * kCus - 1) / (2 * kCus), 4, (longest + most - 1) / most});
-    *splits = (int)std::max<int64_t>(1, most == 1 ? 1 : (longest + each - 1) / each);
-    *split_tiles = *splits == 1 ? 1 << 30 : (int)each;
+    if (longest > each) {
+        *splits = (int)((longest + each - 1) / each);
+        *split_tiles = (int)each;
+    }
 }
 
 int64_t attn_prefill_blocks(int Hq, int Hkv, int N, int64_t total, bool packed)

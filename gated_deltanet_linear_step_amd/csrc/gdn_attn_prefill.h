@@ -188,10 +188,6 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
 #pragma unroll
         for (int c = 0; c < KC; ++c)
             q[c] = *reinterpret_cast<const u32x4 *>(from + 32 * c);
-        // here, not in the loop, where the wait would be for the tile on its way too
-#pragma unroll
-        for (int c = 0; c < KC; ++c)
-            asm volatile("" : "+v"(q[c]));
     }
     const float scale = p.a.scale * 1.4426950408889634f;  // exponentials in base 2
     f32x16 o[TV] = {};
@@ -382,10 +378,12 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
             const From second = locate(first + 1);
             fetch(second, 1, 1);
             next_none = second.none;
-            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * G_::FETCH) : "memory");
-        } else {
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         }
+        // the queries too: a wait for them in the loop would be one for the tile on its way
+#pragma unroll
+        for (int c = 0; c < KC; ++c)
+            asm volatile("" : "+v"(q[c]));
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
     }
     // read_on: the next step's first operands are read as soon as the tile is here, at kt
