@@ -54,31 +54,37 @@ __device__ __forceinline__ bool is_page(const PageParams &p, int page) { return 
 
 constexpr int kEach = 8, kStep = kEach * kThreads;  // pages a thread looks at, and the workgroup, at a time
 
-// Hands free pages, lowest first, to give(rank, page) for the ranks below `want`, looking from page `base` on, whose
-// first free page has rank `found`. Moves base and found behind the last pages looked at.
-template <class F>
-__device__ __forceinline__ void lowest_free(const PageParams &p, int want, int &base, int &found, int *sums, F give)
+// The pages that a thread looks at from page `base` on: bit j, whether the j-th is free
+__device__ __forceinline__ uint32_t free_pages(const PageParams &p, int base)
 {
-    for (; base < p.num_pages && found < want; base += kStep) {
-        const int at = base + kEach * threadIdx.x;
-        bool open[kEach];
-        int n = 0;
+    const int at = base + kEach * threadIdx.x;
+    int refs[kEach];
 #pragma unroll
-        for (int j = 0; j < kEach; ++j) {
-            open[j] = at + j < p.num_pages && p.refs[min(at + j, p.num_pages - 1)] <= 0;
-            n += open[j];
-        }
+    for (int j = 0; j < kEach; ++j)
+        refs[j] = p.refs[min(at + j, p.num_pages - 1)];
+    uint32_t open = 0;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j)
+        open |= at + j < p.num_pages && refs[j] <= 0 ? 1u << j : 0u;
+    return open;
+}
+
+// Hands free pages, lowest first, to give(rank, page) for the ranks below `want`; returns how many it has. `open`: what the
+// thread found from page 0 on.
+template <class F>
+__device__ __forceinline__ int lowest_free(const PageParams &p, int want, uint32_t open, int *sums, F give)
+{
+    int found = 0;
+    for (int base = 0; base < p.num_pages && found < want; base += kStep) {
+        if (base > 0)
+            open = free_pages(p, base);
         int total;
-        int rank = found + scan(n, sums, total);
-#pragma unroll
-        for (int j = 0; j < kEach; ++j)
-            if (open[j]) {
-                if (rank < want)
-                    give(rank, at + j);
-                ++rank;
-            }
+        int rank = found + scan(__popc(open), sums, total);
+        for (uint32_t left = open; left && rank < want; left &= left - 1, ++rank)
+            give(rank, base + kEach * (int)threadIdx.x + __ffs(left) - 1);
         found += total;
     }
+    return min(found, want);
 }
 
 // ---- free ---------------------------------------------------------------------
@@ -100,6 +106,41 @@ __global__ __launch_bounds__(256) void free_kernel(const PageParams p)
 
 // ---- reserve and fork ---------------------------------------------------------
 
+// Whether x is among list[0 .. n); the list is readable up to a multiple of 8
+__device__ __forceinline__ bool among(const int *list, int n, int x)
+{
+    bool found = false;
+    for (int i = 0; i < n; i += 8) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            found |= list[i + j] == x && i + j < n;
+    }
+    return found;
+}
+
+// Requests are looked after by half waves: most calls name no more of them, and rows of hundreds of entries are few loads.
+constexpr int kHalf = 32, kHalves = kThreads / kHalf;
+
+// Which lanes of the half wave have x
+__device__ __forceinline__ uint32_t half_ballot(bool x) { return (uint32_t)(__ballot(x) >> (threadIdx.x & kHalf)); }
+
+// Calls f(entry, page, in range) for a half wave's entries of a row below n, four loads at a time in flight
+template <class F>
+__device__ __forceinline__ void each_entry(const int32_t *row, int n, F f)
+{
+    const int lane = threadIdx.x & (kHalf - 1);
+    for (int e0 = 0; e0 < n; e0 += 4 * kHalf) {
+        int v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j] = row[min(e0 + kHalf * j + lane, n - 1)];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (e0 + kHalf * j < n)
+                f(e0 + kHalf * j + lane, v[j], e0 + kHalf * j + lane < n);
+    }
+}
+
 // Entries that `tokens` tokens take; -1: not a length of a row
 __device__ __forceinline__ int entries_of(const PageParams &p, int tokens)
 {
@@ -112,35 +153,33 @@ constexpr int kList = 4096;  // pages handed out at a time
 __global__ __launch_bounds__(kThreads) void reserve_kernel(const PageParams p)
 {
     __shared__ int sums[kWaves], rows[kPageRequests], need[kPageRequests], first[kPageRequests], list[kList];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & (kHalf - 1);
     const int entries = tid < p.n ? entries_of(p, p.len[tid]) : 0;
     int state = 0;
     rows[tid] = tid < p.n ? p.row[tid] : -1;
+    const uint32_t open = p.num_pages > 0 ? free_pages(p, 0) : 0;
     __syncthreads();
-    if (tid < p.n) {
-        state = rows[tid] < 0 || rows[tid] >= p.rows || entries < 0 ? 2 : 0;
-        for (int i = 0; i < tid && state == 0; ++i)
-            state = rows[i] == rows[tid] ? 2 : 0;
-    }
+    if (tid < p.n)
+        state = rows[tid] < 0 || rows[tid] >= p.rows || entries < 0 || among(rows, tid, rows[tid]) ? 2 : 0;
     need[tid] = state == 0 ? entries : 0;
     first[tid] = 0;
     __syncthreads();
-    // a wave counts the entries that a request misses
-    for (int i = wave; i < p.n; i += kWaves) {
+    // the entries that a request misses
+    for (int i = tid / kHalf; i < p.n; i += kHalves) {
         const int32_t *row = p.table + (int64_t)rows[i] * p.table_stride;
         int missing = 0;
-        for (int e = lane; e < need[i]; e += 64)
-            missing += !is_page(p, row[e]);
-        for (int d = 32; d; d >>= 1)
-            missing += __shfl_xor(missing, d, 64);
+        each_entry(row, need[i], [&](int, int page, bool in) { missing += __popc(half_ballot(in && !is_page(p, page))); });
         if (lane == 0)
             first[i] = missing;
     }
     __syncthreads();
     const int wants = first[tid];
-    int all, base = 0, have = 0;
+    int all;
     const int before = scan(wants, sums, all);
-    lowest_free(p, all, base, have, sums, [](int, int) {});
+    const int have = lowest_free(p, all, open, sums, [&](int rank, int page) {
+        if (rank < kList)
+            list[rank] = page;
+    });
     if (wants > 0 && before + wants > have) {
         state = 1;
         need[tid] = 0;
@@ -151,24 +190,25 @@ __global__ __launch_bounds__(kThreads) void reserve_kernel(const PageParams p)
     int given;
     scan(state == 0 ? wants : 0, sums, given);
     for (int from = 0; from < given; from += kList) {
-        // the lowest pages that are free now: those handed out in a turn before are in use
         const int count = min(kList, given - from);
-        base = have = 0;
-        lowest_free(p, count, base, have, sums, [&](int rank, int page) { list[rank] = page; });
+        if (from > 0)  // the lowest pages that are free now: those handed out in a turn before are in use
+            lowest_free(p, count, free_pages(p, 0), sums, [&](int rank, int page) { list[rank] = page; });
         __syncthreads();
-        for (int i = wave; i < p.n; i += kWaves) {
+        for (int i = tid / kHalf; i < p.n; i += kHalves) {
             int32_t *row = p.table + (int64_t)rows[i] * p.table_stride;
             int rank = max(first[i] - from, 0);  // of the first entry that the row still misses
-            for (int e0 = 0; e0 < need[i] && first[i] < from + count; e0 += 64) {
-                const bool miss = e0 + lane < need[i] && !is_page(p, row[min(e0 + lane, need[i] - 1)]);
-                const uint64_t all_miss = __ballot(miss);
-                const int mine = rank + __popcll(all_miss & ((1ull << lane) - 1));
+            if (first[i] >= from + count)
+                continue;
+            each_entry(row, need[i], [&](int e, int page, bool in) {
+                const bool miss = in && !is_page(p, page);
+                const uint32_t all_miss = half_ballot(miss);
+                const int mine = rank + __popc(all_miss & ((1u << lane) - 1));
                 if (miss && mine < count) {
-                    row[e0 + lane] = list[mine];
+                    row[e] = list[mine];
                     p.refs[list[mine]] = 1;
                 }
-                rank += __popcll(all_miss);
-            }
+                rank += __popc(all_miss);
+            });
         }
         __syncthreads();
     }
@@ -178,38 +218,45 @@ __global__ __launch_bounds__(kThreads) void fork_kernel(const PageParams p)
 {
     __shared__ int sums[kWaves], srcs[kPageRequests], dsts[kPageRequests], full[kPageRequests], states[kPageRequests],
         ranks[kPageRequests], list[kPageRequests];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & (kHalf - 1);
     const int tokens = tid < p.n ? p.len[tid] : 0, entries = entries_of(p, tokens);
     srcs[tid] = tid < p.n ? p.src[tid] : -1;
     dsts[tid] = tid < p.n ? p.row[tid] : -1;
+    const uint32_t open = p.num_pages > 0 ? free_pages(p, 0) : 0;
     __syncthreads();
     int state = 2;
-    if (tid < p.n && entries >= 0 && srcs[tid] >= 0 && srcs[tid] < p.rows && dsts[tid] >= 0 && dsts[tid] < p.rows) {
-        state = 0;
-        for (int i = 0; i < p.n; ++i)
-            if ((i < tid && dsts[i] == dsts[tid]) || dsts[i] == srcs[tid])
-                state = 2;
-    }
+    if (tid < p.n && entries >= 0 && srcs[tid] >= 0 && srcs[tid] < p.rows && dsts[tid] >= 0 && dsts[tid] < p.rows)
+        state = among(dsts, tid, dsts[tid]) || among(dsts, p.n, srcs[tid]) ? 2 : 0;
     states[tid] = state;
     full[tid] = entries;
     __syncthreads();
-    // a wave looks through the rows of a request
-    for (int i = wave; i < p.n; i += kWaves) {
+    // both rows of a request, loads of either in flight together
+    for (int i = tid / kHalf; i < p.n; i += kHalves) {
         if (states[i] != 0)
             continue;
         const int32_t *src = p.table + (int64_t)srcs[i] * p.table_stride, *dst = p.table + (int64_t)dsts[i] * p.table_stride;
         bool bad = false;
-        for (int e = lane; e < p.width; e += 64)
-            bad = bad || (e < full[i] && !is_page(p, src[e])) || is_page(p, dst[e]);
-        if (__ballot(bad) != 0 && lane == 0)
+        for (int e0 = 0; e0 < p.width; e0 += 4 * kHalf) {
+            int from[4], to[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int e = min(e0 + kHalf * j + lane, p.width - 1);
+                from[j] = src[e];
+                to[j] = dst[e];
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                bad |= is_page(p, to[j]) || (e0 + kHalf * j + lane < full[i] && !is_page(p, from[j]));
+        }
+        if (half_ballot(bad) != 0 && lane == 0)
             states[i] = 2;
     }
     __syncthreads();
     state = states[tid];
     const bool part = state == 0 && tokens % p.page_size != 0;
-    int all, base = 0, have = 0;
+    int all;
     const int rank = scan(part, sums, all);
-    lowest_free(p, all, base, have, sums, [&](int r, int page) { list[r] = page; });
+    const int have = lowest_free(p, all, open, sums, [&](int r, int page) { list[r] = page; });
     if (part && rank >= have)
         state = 1;
     states[tid] = state;
@@ -220,17 +267,19 @@ __global__ __launch_bounds__(kThreads) void fork_kernel(const PageParams p)
         p.status[tid] = state;
     const Copies copies = copies_of(p.workspace);
     if (tid == 0)
-        *copies.count = min(all, have);
+        *copies.count = have;
     __syncthreads();
-    for (int i = wave; i < p.n; i += kWaves) {
+    for (int i = tid / kHalf; i < p.n; i += kHalves) {
         if (states[i] != 0)
             continue;
         const int32_t *src = p.table + (int64_t)srcs[i] * p.table_stride;
         int32_t *dst = p.table + (int64_t)dsts[i] * p.table_stride;
-        for (int e = lane; e < full[i]; e += 64) {
-            dst[e] = src[e];
-            atomicAdd(p.refs + src[e], 1);
-        }
+        each_entry(src, full[i], [&](int e, int page, bool in) {
+            if (in) {
+                dst[e] = page;
+                atomicAdd(p.refs + page, 1);
+            }
+        });
         if (lane == 0 && ranks[i] >= 0) {
             const int page = list[ranks[i]];
             dst[full[i]] = page;
