@@ -6,6 +6,8 @@
 
 namespace gdn {
 
+constexpr int kCus = 256;  // of an MI355X
+
 // Rotary positions (gdn_rope.hip). Strides in elements.
 struct RopeParams {
     int tokens, Hq, Hkv, D, rot, layout, dt;
@@ -56,7 +58,9 @@ struct AttnPrefillParams {
     const int32_t *cu_q, *cu_k, *lens;
     int max_keys;
     int splits, split_tiles, first_slot;  // runs of keys of a block of queries, their tiles, and the slot of the first
-    bool one_round;          // all workgroups are on the device at once (set by the launcher)
+    bool whole;              // rows whose keys are one run are written at once
+    int blocks;              // of rows, for each key head (this and the next are set by the launcher)
+    bool one_round;          // all workgroups are on the device at once
 };
 bool attn_supported(int D);
 // Runs of keys that a call is split into, and their length: by the offsets, or (cu_q NULL) one sequence against `keys` keys;

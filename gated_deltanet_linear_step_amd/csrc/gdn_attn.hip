@@ -38,6 +38,8 @@ __global__ __launch_bounds__(256) void join_few_kernel(const AttnParams p, int64
     if (row >= rows)
         return;
     const float2 st = lane < p.slots ? p.stat[first + lane] : make_float2(kNone, 0.f);
+    if (__shfl(st.y, 0, 64) == kJoined)
+        return;
     float most = st.y == 0.f ? kNone : st.x;
 #pragma unroll
     for (int x = 32; x; x >>= 1)
@@ -136,8 +138,6 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(const AttnParams p)
     store_joined<DT>(p, row, d, o, most, total);
 }
 
-constexpr int kBlock = 128;  // rows of a workgroup of the prefill kernel
-constexpr int kCus = 256;
 
 template <int DT>
 hipError_t join_few(const AttnParams &p, int64_t rows, unsigned grid, hipStream_t s)
@@ -153,43 +153,75 @@ hipError_t join_few(const AttnParams &p, int64_t rows, unsigned grid, hipStream_
 
 }  // namespace
 
+int64_t attn_prefill_blocks(int Hq, int Hkv, int N, int64_t total, bool packed)
+{
+    const int64_t G = Hq / Hkv;
+    // packed: an upper bound, of which up to one a sequence stays empty
+    const int64_t blocks = packed ? total * G / kBlock + N : N * ((total / std::max(N, 1) * G + kBlock - 1) / kBlock);
+    return blocks * Hkv;
+}
+
 bool attn_supported(int D) { return D == 64 || D == 96 || D == 128 || D == 256; }
 
 int attn_prefill_most_splits(int Hq, int Hkv, int64_t total)
 {
     const int64_t G = Hq / Hkv, blocks = std::max<int64_t>(1, (total * G + kBlock - 1) / kBlock) * Hkv;
-    return blocks >= kCus ? 1 : (int)std::min<int64_t>(1024 / blocks, 32);
+    return blocks > 2 * kCus ? 1 : blocks >= kCus ? 2 : (int)std::min<int64_t>(1024 / blocks, 32);
 }
 
 void attn_prefill_splits(int Hq, int Hkv, int D, int N, int64_t total, const int32_t *cu_q, const int32_t *cu_k, int keys, int *splits,
                          int *split_tiles)
 {
-    // Where the blocks of rows are fewer than the CUs, runs of keys of one length, so many that two workgroups for each CU
-    // have one; a run is at least four tiles.
     const int most = attn_prefill_most_splits(Hq, Hkv, total), KT = D <= 128 ? 64 : 32;
     const int64_t G = Hq / Hkv;
     *splits = 1;
     *split_tiles = 1 << 30;
     if (most == 1)
         return;
-    // (of queries that see all keys: few queries against many keys are what is split)
-    const auto over = [&](auto f) {
+    // f(tiles, block) for every block of rows, numbered as the kernel does
+    const auto blocks = [&](auto f) {
         for (int s = 0; s < N; ++s) {
             const int64_t len = cu_q ? cu_q[s + 1] - cu_q[s] : total, nk = cu_q ? cu_k[s + 1] - cu_k[s] : keys;
-            f((nk + KT - 1) / KT, (len * G + kBlock - 1) / kBlock * Hkv);
+            int64_t block = cu_q ? block_base(cu_q, s, (int)G) : 0;
+            for (int64_t row = 0; row < len * G; row += kBlock, ++block) {
+                const int64_t token = (std::min(row + kBlock, len * G) - 1) / G;
+                f((std::clamp<int64_t>(cu_q ? nk - len + 1 + token : nk, 0, nk) + KT - 1) / KT, block);
+            }
         }
     };
-    int64_t all = 0, longest = 0;
-    over([&](int64_t tiles, int64_t blocks) {
-        all += tiles * blocks;
-        longest = std::max(longest, blocks > 0 ? tiles : 0);
+    int64_t all = 0, longest = 0, count = 0;
+    blocks([&](int64_t tiles, int64_t) {
+        all += tiles * Hkv;
+        count += Hkv;
+        longest = std::max(longest, tiles);
     });
-    int64_t each = std::max<int64_t>({(all + 2 * kCus - 1) / (2 * kCus), 4, (longest + most - 1) / most});
-    for (; each < longest; ++each) {  // one workgroup too many would take a round of its own
-        int64_t workgroups = 0;
-        over([&](int64_t tiles, int64_t blocks) { workgroups += (tiles + each - 1) / each * blocks; });
-        if (workgroups <= 2 * kCus)
-            break;
+    constexpr int64_t kSlots = 2 * kCus;  // two workgroups on a CU
+    int64_t each = std::max<int64_t>({(all + kSlots - 1) / kSlots, 4, (longest + most - 1) / most});
+    if (count >= kCus) {
+        // Blocks for every CU, but of all lengths: a long one would be left alone on its CU, at about 0.6 of the rate of two. Cut at
+        // the average, their ends go where short ones were; it pays where that is more than writing and joining
+        // parts takes. Microseconds, as measured (4096 tokens, 16 heads of 256: 198 -> 155; 2048 tokens: no gain, not taken).
+        const double tile = D == 256 ? 1.25 : D == 128 ? 1.2 : D == 96 ? 0.9 : 0.7;
+        int64_t cut = 0;
+        blocks([&](int64_t tiles, int64_t) { cut += tiles > each ? Hkv : 0; });
+        const double gain = 0.7 * tile * (longest - each), cost = 8 + cut * 2.0 * kBlock * D * 4 * 2 / 4.5e6;
+        if (gain <= cost)
+            return;
+    } else {
+        // Fewer: runs of one length, as many as one round of workgroups holds on every XCD (they go to the 8 in turn, those
+        // that have no keys too)
+        const int64_t numbered = attn_prefill_blocks(Hq, Hkv, N, total, cu_q != nullptr) / Hkv;
+        for (; each < longest; ++each) {
+            const int64_t runs = (longest + each - 1) / each;
+            int64_t on[8] = {}, most_on = 0;
+            blocks([&](int64_t tiles, int64_t block) {
+                for (int64_t run = 0; run * each < tiles; ++run)
+                    for (int h = 0; h < Hkv; ++h)
+                        most_on = std::max(most_on, ++on[(((numbered - 1 - block) * runs + run) * Hkv + h) % 8]);
+            });
+            if (most_on <= kSlots / 8)
+                break;
+        }
     }
     if (longest > each) {
         *splits = (int)((longest + each - 1) / each);
@@ -197,21 +229,14 @@ void attn_prefill_splits(int Hq, int Hkv, int D, int N, int64_t total, const int
     }
 }
 
-int64_t attn_prefill_blocks(int Hq, int Hkv, int N, int64_t total, bool packed)
-{
-    const int64_t G = Hq / Hkv;
-    // packed: an upper bound, of which up to one a sequence stays empty
-    return (packed ? total * G / kBlock + N : N * ((total / std::max(N, 1) * G + kBlock - 1) / kBlock)) * Hkv;
-}
-
 hipError_t launch_attn_prefill(const AttnPrefillParams &given, hipStream_t s)
 {
     AttnPrefillParams p = given;
-    const int64_t blocks = attn_prefill_blocks(p.a.Hq, p.a.Hkv, p.N, p.total, p.cu_q != nullptr) * p.splits;
+    p.blocks = (int)(attn_prefill_blocks(p.a.Hq, p.a.Hkv, p.N, p.total, p.cu_q != nullptr) / p.a.Hkv);
+    const int64_t grid = (int64_t)p.blocks * p.a.Hkv * p.splits;
     // without the blocks that stay empty: one a sequence
-    const int64_t empty = p.cu_q ? (int64_t)p.N * p.a.Hkv * p.splits : 0;
-    p.one_round = blocks - empty <= 2 * kCus;
-    return p.a.dt == DT_BF16 ? launch_attn_prefill_bf16(p, (unsigned)blocks, s) : launch_attn_prefill_f16(p, (unsigned)blocks, s);
+    p.one_round = p.splits == 1 && (int64_t)(p.blocks - (p.cu_q ? p.N : 0)) * p.a.Hkv <= 2 * kCus;
+    return p.a.dt == DT_BF16 ? launch_attn_prefill_bf16(p, (unsigned)grid, s) : launch_attn_prefill_f16(p, (unsigned)grid, s);
 }
 
 namespace {

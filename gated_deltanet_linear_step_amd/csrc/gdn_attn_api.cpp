@@ -318,6 +318,7 @@ gdn_status gdn_attention_prefill(const gdn_attention_args *args, int32_t num_seq
     if (!aligned(workspace, 256))
         return GDN_ERR_ALIGN;
     carve(p.a, rows, p.splits, workspace);
+    p.whole = true;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     hipError_t e = gdn::launch_attn_prefill(p, s);
     if (e == hipSuccess && p.a.slots > 0)

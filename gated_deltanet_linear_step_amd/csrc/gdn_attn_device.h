@@ -18,8 +18,18 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) void lds_void;
 
+constexpr int kBlock = 128;  // rows of a workgroup of the prompts' kernel
+
+// First block of 128 rows that the sequences before cu[s] leave to sequence s (some blocks stay empty)
+__host__ __device__ __forceinline__ int block_base(const int32_t *cu, int s, int G)
+{
+    return (int)((int64_t)cu[s] * G / kBlock) + s;
+}
+
 // exp2 of a masked score, and the running maximum before any key
 constexpr float kNone = -__builtin_inff();
+// in place of the first run's sum: the outputs are there, nothing is joined
+constexpr float kJoined = -1.f;
 
 template <int DT>
 struct Type16;

@@ -22,7 +22,8 @@
 namespace gdn {
 namespace attn {
 
-constexpr int kRows = 32, kWaves = 4, kBlock = kRows * kWaves, kThreads = 64 * kWaves;
+constexpr int kRows = 32, kWaves = 4, kThreads = 64 * kWaves;
+static_assert(kBlock == kRows * kWaves, "the rows of a workgroup");
 
 template <int D>
 struct Geo {
@@ -54,12 +55,6 @@ struct Geo {
     }
 };
 
-// First block of 128 rows that the sequences before cu[s] leave to sequence s (some blocks stay empty)
-__host__ __device__ __forceinline__ int block_base(const int32_t *cu, int s, int G)
-{
-    return (int)((int64_t)cu[s] * G / kBlock) + s;
-}
-
 template <int DT, int D, bool PAGED>
 __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
 {
@@ -72,13 +67,14 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
     const int half = lane >> 5, col = lane & 31;
     const int G = p.a.Hq / p.a.Hkv;
 
-    // Work: a key head, a run of keys, a block of rows; the last blocks, which see most keys, first
+    // Work: a key head, a block of rows, a run of keys. The last blocks, which see most keys, come first. Where there are blocks
+    // for every CU, second runs, shorter than first ones, come last; where there are fewer, the runs of a block side by
+    // side (128 queries behind 16256 keys, 16 heads over 4: 38 us; the blocks of a run side by side: 48).
     const int kvh = blockIdx.x % p.a.Hkv, rest = blockIdx.x / p.a.Hkv;
-    const int split = rest % p.splits;
-    const int blocks_all = gridDim.x / (p.a.Hkv * p.splits);
-    int block = rest / p.splits;
+    const bool last_runs = p.blocks * p.a.Hkv >= kCus;
+    const int split = last_runs ? rest / p.blocks : rest % p.splits, order = last_runs ? rest % p.blocks : rest / p.splits;
     // (of one round of workgroups, two on a CU, the second half goes the other way, so that a CU has one of either kind)
-    block = p.one_round && block >= blocks_all / 2 ? block - blocks_all / 2 : blocks_all - 1 - block;
+    int block = p.one_round && order >= p.blocks / 2 ? order - p.blocks / 2 : p.blocks - 1 - order;
     int seq = 0, row0, len, nk;
     int64_t key0 = 0;
     if (p.cu_q) {
@@ -118,6 +114,10 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
     const int block_most = max(0, min(nk, ahead + step * ((min(m0 + kBlock, rows) - 1) / G)));
     const int tiles = (block_most + KT - 1) / KT;
     const int first = (int)min((int64_t)split * p.split_tiles, (int64_t)tiles), last = min(tiles - first, p.split_tiles) + first;
+    // a block whose keys are one run has nothing to join
+    const bool whole = p.whole && tiles <= p.split_tiles;
+    if (whole && split > 0)
+        return;
 
     // What a lane fetches of each tile: FETCH blocks of the wave's ROWS rows
     const unsigned char *const kb = static_cast<const unsigned char *>(p.a.kv.k), *const vb = static_cast<const unsigned char *>(p.a.kv.v);
@@ -437,7 +437,9 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
         return;
     const int end_token = end_row / G, end_head = kvh * G + end_row - end_token * G;
     const int64_t at = (int64_t)(row0 + end_token) * p.a.Hq + end_head;
-    if (p.a.slots > 0) {
+    if (whole && p.a.slots > 0 && half == 0)
+        p.a.stat[at * p.a.slots] = make_float2(kNone, kJoined);
+    if (p.a.slots > 0 && !whole) {
         const int64_t slot = at * p.a.slots + p.first_slot + split;
         if (half == 0)
             p.a.stat[slot] = make_float2(top, sum);
