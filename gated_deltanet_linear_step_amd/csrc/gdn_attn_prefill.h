@@ -315,6 +315,18 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
 
     // 32 keys from k0 on, of which a row may not see some; `none`: two bits, the groups of 16 without a page.
     auto attend_masked = [&](int k0, int none, uint32_t kt, uint32_t vt) {
+        // 0 times what is not finite in a masked place must not reach a row: those values are left out, and
+        // a row that sees one of them becomes NaN
+        uint32_t bad = 0;
+        const auto look = [&](int at) {
+            const u32x4 w = lds_read16(vt + at + 16 * lane);
+            bad |= not_finite<DT>(w.x) | not_finite<DT>(w.y) | not_finite<DT>(w.z) | not_finite<DT>(w.w);
+        };
+        if constexpr (AHEAD) {  // beside the products of the scores (D = 256 has no registers for that)
+#pragma unroll
+            for (int at = 0; at < 32 * G_::PITCH; at += 1024)
+                look(at);
+        }
         f32x16 s;
         scores(s, kt);
 #pragma unroll
@@ -323,26 +335,37 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
             s[i] = k0 + key < seen && !(none >> (i / 8) & 1) ? s[i] : kNone;
         }
         const float base = rescale(largest(s));
-        u32x4 pf[2], sees[2];
-        const uint32_t one = pack2<DT>(1.f, 1.f);
+        u32x4 pf[2];
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
             const float x = exp2_f(fmaf(s[i], scale, -base)), y = exp2_f(fmaf(s[i + 1], scale, -base));
             sum += x;
             sum += y;
             pf[i / 8][i % 8 / 2] = pack2<DT>(x, y);
+        }
+        if constexpr (!AHEAD) {
+#pragma unroll 1
+            for (int at = 0; at < 32 * G_::PITCH; at += 1024)
+                look(at);
+        }
+        const uint32_t v_at = opaque(vt + v_lane);
+        const bool finite = __ballot(bad != 0) == 0;
+        if constexpr (AHEAD)  // (two ways to the sums take more registers than D = 256 has)
+            if (finite) {
+#pragma unroll
+                for (int st = 0; st < 2; ++st)
+#pragma unroll
+                    for (int tv = 0; tv < TV; ++tv)
+                        o[tv] = T::mfma32(v_of(v_at, tv, st), pf[st], o[tv]);
+                return;
+            }
+        u32x4 sees[2];
+        const uint32_t one = pack2<DT>(1.f, 1.f);
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
             const int key = k0 + 8 * (i / 4) + 4 * half + i % 4, upto = none >> (i / 8) & 1 ? 0 : seen;
             sees[i / 8][i % 8 / 2] = (key < upto ? one & 0xffffu : 0u) | (key + 1 < upto ? one & 0xffff0000u : 0u);
         }
-        // 0 times what is not finite in a masked place must not reach a row: those values are left out, and
-        // a row that sees one of them becomes NaN
-        uint32_t bad = 0;
-        for (int at = 16 * lane; at < 32 * G_::PITCH; at += 1024) {
-            const u32x4 w = lds_read16(vt + at);
-            bad |= not_finite<DT>(w.x) | not_finite<DT>(w.y) | not_finite<DT>(w.z) | not_finite<DT>(w.w);
-        }
-        const uint32_t keep = __ballot(bad != 0) != 0 ? 0 : ~0u;
-        const uint32_t v_at = opaque(vt + v_lane);
 #pragma unroll
         for (int tv = 0; tv < TV; ++tv) {
             f32x16 hit = {};
@@ -356,10 +379,10 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
                     wrong[w] &= one;
                 }
                 o[tv] = T::mfma32(v, pf[st], o[tv]);
-                if (keep == 0)
+                if (!finite)
                     hit = T::mfma32(wrong, sees[st], hit);
             }
-            if (keep == 0) {
+            if (!finite) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     o[tv][i] = hit[i] > 0.f ? __builtin_nanf("") : o[tv][i];
