@@ -521,7 +521,9 @@ gdn_status gdn_rope_frequencies(int32_t rotary_dim, double theta, int32_t scalin
  * A query that sees no key, or whose scores are all -inf, has o = 0 and lse = -inf.
  * Infinities and NaN in keys, values or queries that a query does not see do not reach
  * it; in those it sees they make what the formula makes of them not finite (where that
- * is an infinity, a NaN may stand).
+ * is an infinity, a NaN may stand). Outputs are summed before they are divided by the sum of
+ * weights, of at most 2^8 each: values of 2^90 and more may leave f32 on the way, as may
+ * scores times scale.
  *
  *   q_heads, kv_heads   q_heads a multiple of kv_heads, both >= 1
  *   head_dim       64, 96, 128 or 256
@@ -567,7 +569,7 @@ typedef struct gdn_attention_args {
  * Rows behind cu_q[num_seqs] are not touched.
  * Errors: NULL, SHAPE (counts, strides, offsets; table rows shorter than a sequence),
  * UNSUPPORTED, OVERFLOW (a row stride of 2^24 elements or more, more than 2^31 - 1 rows times
- * heads), ALIGN, WORKSPACE, LAUNCH. */
+ * heads, more than 2^30 keys of a sequence or a grid of 2^32 threads), ALIGN, WORKSPACE, LAUNCH. */
 size_t gdn_attention_prefill_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                              int32_t num_seqs, int32_t total_tokens);
 gdn_status gdn_attention_prefill(const gdn_attention_args *args, int32_t num_seqs,

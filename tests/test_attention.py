@@ -374,3 +374,102 @@ def test_offsets_past_32_bits(paged):
     check_prompts(out, None, q, k, v, [n], [n], D ** -0.5)
     out = ops.attention_decode(q[-1:], *pools, table, torch.tensor([n], dtype=torch.int32, device=DEV), batch=1, max_len=n)
     check_steps(out, None, q[-1:], k, v, [n], 0, 1, D ** -0.5)
+
+
+# ---- how calls are split -------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("Hq,Hkv,D,tokens", [(8, 1, 256, 6000), (8, 2, 128, 7000)])
+def test_prompts_whose_long_blocks_are_cut(Hq, Hkv, D, tokens):
+    """Blocks for every CU, of all lengths; a short prompt behind the long one."""
+    lens = [tokens, 70]
+    q, k, v = packed(lens, lens, Hq, Hkv, D, B16, 3)
+    lse = torch.empty(sum(lens), Hq, device=DEV)
+    out = ops.attention_prefill(q, k, v, offsets(lens), lse=lse)
+    check_prompts(out, lse, q, k, v, lens, lens, D ** -0.5)
+
+
+@pytest.mark.parametrize("D,dtype", [(64, B16), (96, F16), (128, F16), (256, B16)])
+def test_sequences_split_beside_ones_that_are_not(D, dtype):
+    """Few queries behind many keys, behind few, behind none, and queries of their own prompt."""
+    lens, keys = [1, 3, 0, 64, 5, 200], [6000, 3, 900, 64, 0, 1400]
+    q, k, v = packed(lens, keys, 4, 2, D, dtype, D)
+    lse = torch.empty(sum(lens), 4, device=DEV)
+    kp, vp, table = on_pages(k, v, keys, 16, 3)
+    for paged in (False, True):
+        out = ops.attention_prefill(q, kp if paged else k, vp if paged else v, offsets(lens), cu_k=offsets(keys), lse=lse,
+                                    table=table if paged else None)
+        check_prompts(out, lse, q, k, v, lens, keys, D ** -0.5)
+
+
+@pytest.mark.parametrize("D,dtype", [(64, F16), (96, B16), (128, B16), (256, F16)])
+def test_a_bound_far_past_the_lengths(D, dtype):
+    """max_len of a whole context, sequences much shorter: most runs are empty, and there are hundreds of them."""
+    ps, most = 128, 100000
+    for lens, T in (([700], 1), ([1, 0, 300, 2, 40], 2), ([900, 5] * 40, 1)):
+        q, k, v, kp, vp, table, front = decode_inputs(lens, 200, T, 4, 2, D, dtype, ps, len(lens))
+        wide = torch.full((len(lens), -(-most // ps)), -1, dtype=torch.int32, device=DEV)
+        wide[:, :table.shape[1]] = table
+        lse = torch.empty(len(lens) * T, 4, device=DEV)
+        out = ops.attention_decode(q, kp, vp, wide, torch.tensor(lens, dtype=torch.int32, device=DEV), batch=len(lens), tokens_per_seq=T,
+                                   max_len=most, prefix_table=front, prefix_len=200, lse=lse)
+        check_steps(out, lse, q, k, v, lens, 200, T, D ** -0.5)
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D", [(33, 1, 1, 64), (9, 8, 2, 128), (5, 16, 2, 256), (70, 6, 2, 96), (200, 4, 4, 128)])
+def test_steps_of_many_rows(T, Hq, Hkv, D):
+    lens = [T, T + 1, 1500, 0, T - 1]
+    q, k, v, kp, vp, table, front = decode_inputs(lens, 90, T, Hq, Hkv, D, B16, 16, T)
+    lse = torch.empty(len(lens) * T, Hq, device=DEV)
+    out = ops.attention_decode(q, kp, vp, table, torch.tensor(lens, dtype=torch.int32, device=DEV), batch=5, tokens_per_seq=T, max_len=1500,
+                               prefix_table=front, prefix_len=90, lse=lse)
+    check_steps(out, lse, q, k, v, lens, 90, T, D ** -0.5)
+
+
+def test_tables_and_prefixes_that_share_pages():
+    """The same pages in several rows, twice in a row, and in the prefix: keys are only read."""
+    ps, n = 16, 64
+    q, k, v = packed([3], [n], 4, 2, 128, B16, 8)
+    kp, vp, table = on_pages(k, v, [n], ps, 3)
+    row = table[0, :4]
+    tables = torch.stack([row, row.flip(0), torch.cat([row[:2], row[:2]])]).contiguous()
+    order = [torch.arange(n), torch.arange(n).view(4, 16).flip(0).flatten(), torch.cat([torch.arange(32), torch.arange(32)])]
+    out = ops.attention_decode(q, kp, vp, tables, torch.tensor([64, 50, 40], dtype=torch.int32, device=DEV), batch=3, max_len=64,
+                               prefix_table=row.contiguous(), prefix_len=30)
+    for b, m in enumerate((64, 50, 40)):
+        at = torch.cat([torch.arange(30), order[b][:m]]).to(DEV)
+        want = attention64(q[b:b + 1], k[at], v[at], torch.ones(1, 30 + m, dtype=torch.bool, device=DEV), 128 ** -0.5)
+        near(out[b:b + 1], want[0], want[2])
+
+
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+def test_outputs_do_not_depend_on_what_the_workspace_held(D):
+    lens, keys = [2, 130], [3000, 700]
+    q, k, v = packed(lens, keys, 4, 2, D, B16, 1)
+    need = ops.attention_prefill_workspace_bytes(Hq=4, Hkv=2, head_dim=D, num_seqs=2, total_tokens=132)
+    outs = []
+    for fill in (0, 255, 127):
+        ws = torch.full((need,), fill, dtype=torch.uint8, device=DEV)
+        outs.append(ops.attention_prefill(q, k, v, offsets(lens), cu_k=offsets(keys), workspace=ws))
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    check_prompts(outs[0], None, q, k, v, lens, keys, D ** -0.5)
+    n = torch.tensor([5000, 10], dtype=torch.int32, device=DEV)
+    q, k, v, kp, vp, table, front = decode_inputs([5000, 10], 100, 1, 4, 2, D, B16, 64, 2)
+    need = ops.attention_decode_workspace_bytes(Hq=4, Hkv=2, head_dim=D, batch=2, max_len=5000, prefix_len=100)
+    outs = [ops.attention_decode(q, kp, vp, table, n, batch=2, max_len=5000, prefix_table=front, prefix_len=100,
+                                 workspace=torch.full((need,), fill, dtype=torch.uint8, device=DEV)) for fill in (0, 255, 127)]
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    check_steps(outs[0], None, q, k, v, [5000, 10], 100, 1, D ** -0.5)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_the_largest_values_stay_finite(D):
+    """Values of the order that the documents allow, weights that the running maximum lets grow."""
+    n = 300
+    q = torch.zeros(n, 1, D, device=DEV)
+    q[:, 0, 0] = 1
+    k = torch.zeros(n, 1, D, device=DEV)
+    k[:, 0, 0] = 0.02 * torch.arange(n, device=DEV)
+    v = torch.randn(n, 1, D, generator=torch.Generator(DEV).manual_seed(1), device=DEV) * 2.0 ** 86
+    q, k, v = q.to(B16), k.to(B16), v.to(B16)
+    out = ops.attention_prefill(q, k, v, offsets([n]), scale=1.0)
+    check_prompts(out, None, q, k, v, [n], [n], 1.0)

@@ -183,3 +183,11 @@ def test_the_binding_refuses_what_it_cannot_marshal():
         ops.prepare_rope(torch.zeros(4, dtype=torch.int32), torch.zeros(2, dtype=torch.float64), q=cpu, q_out=cpu)
     with pytest.raises(ValueError, match="GPU"):
         ops.prepare_pages_free(torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+
+
+def test_sequences_of_more_than_2_30_keys_are_refused():
+    far = (1 << 30) + 1
+    paged = dict(page_size=1024, num_pages=3, table=A, table_stride=1 << 22, k_stride=1 << 20, v_stride=1 << 20)
+    assert prefill(n=1, cq=(0, 5), ck=(0, far), **paged) == OVERFLOW
+    assert decode(max_len=far, **paged) == OVERFLOW
+    assert decode(max_len=5, prefix=A, prefix_len=far, **paged) == OVERFLOW
