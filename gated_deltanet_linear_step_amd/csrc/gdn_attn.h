@@ -91,7 +91,8 @@ hipError_t launch_attn_decode(const AttnDecodeParams &p, hipStream_t s);
 hipError_t launch_attn_decode_bf16(const AttnDecodeParams &p, unsigned grid, hipStream_t s);
 hipError_t launch_attn_decode_f16(const AttnDecodeParams &p, unsigned grid, hipStream_t s);
 
-// Joins the partial results of `rows` rows (queries times heads) into outputs.
+// Joins the partial results of `rows` rows (queries times heads) into outputs; its workgroups.
+int64_t attn_join_blocks(int D, int slots, int64_t rows);
 hipError_t launch_attn_join(const AttnParams &p, int64_t rows, hipStream_t s);
 
 // Pages of a cache (gdn_pages.hip).

@@ -372,6 +372,8 @@ gdn_status gdn_attention_decode(const gdn_attention_args *args, int32_t batch, i
         return GDN_ERR_OVERFLOW;
     const int64_t rows = queries * p.a.Hq;
     const int slots = d.prefix + d.own;
+    if (slots > 1 && gdn::attn_join_blocks(p.a.D, slots, rows) >= kMaxBlocks)
+        return GDN_ERR_OVERFLOW;
     const size_t need = split_bytes(rows, slots, p.a.D);
     if (need > 0 && (!workspace || workspace_bytes < need))
         return GDN_ERR_WORKSPACE;

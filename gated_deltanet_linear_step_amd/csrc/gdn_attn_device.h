@@ -137,9 +137,10 @@ __device__ __forceinline__ void copy16_runs(const unsigned char *base, const uin
     else
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %5\n\t"
                      "global_load_lds_dwordx4 %2, %5 offset:1024\n\tglobal_load_lds_dwordx4 %3, %5 offset:2048\n\t"
-                     "global_load_lds_dwordx4 %4, %5 offset:3072"
+                     "global_load_lds_dwordx4 %4, %5 offset:%6"
                      :
-                     : "s"(to), "v"(off[0]), "v"(off[1] - 1024), "v"(off[2] - 2048), "v"(off[3] - 3072), "s"(base)
+                     : "s"(to), "v"(off[0]), "v"(off[1] - 1024), "v"(off[2] - 2048), "v"(off[3] - 3 * 1024), "s"(base),
+                       "n"(3 * 1024)
                      : "memory");
 }
 

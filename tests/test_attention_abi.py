@@ -125,6 +125,15 @@ def test_decode_refusals():
     assert decode(prefix=A, prefix_len=16, ws_bytes=need - 1) == WORKSPACE
 
 
+def test_joins_past_a_launch_are_refused():
+    """A join takes four rows a workgroup, or with more than 64 runs 32 outputs of one: 2^24 of those are too many threads."""
+    few = dict(q_heads=64, q_stride=4096, out_stride=4096, table_stride=128, max_len=2048)
+    assert decode(batch=1 << 20, **few) == OVERFLOW
+    many = dict(q_heads=64, head_dim=256, q_stride=1 << 14, out_stride=1 << 14, k_stride=8192, v_stride=8192, table_stride=16640,
+                max_len=16640 * 16)
+    assert decode(batch=1 << 16, **many) == OVERFLOW
+
+
 def test_workspace_queries_of_bad_counts():
     pre = dict(Hq=4, Hkv=2, head_dim=64, num_seqs=1, total_tokens=5)
     for bad in (dict(Hq=3), dict(Hkv=0), dict(head_dim=48), dict(num_seqs=-1), dict(total_tokens=0)):
