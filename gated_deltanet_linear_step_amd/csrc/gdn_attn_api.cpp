@@ -17,6 +17,7 @@ using namespace gdn::checks;
 
 constexpr int64_t kMaxStride = (int64_t)1 << 24;   // a tile's rows are addressed with 32-bit byte offsets
 constexpr int64_t kMaxKeys = (int64_t)1 << 30;     // of a sequence
+constexpr int64_t kMaxPages = (int64_t)1 << 30;    // of a pool, and entries of its table
 constexpr int64_t kMaxBlocks = (int64_t)1 << 24;   // a launch holds fewer than 2^32 threads, 256 of them a workgroup
 
 // log2 of a page size that is built, -1 of others
@@ -119,6 +120,9 @@ gdn_status check_pages(const gdn_page_args *a, bool data, gdn::PageParams &p)
         return GDN_ERR_NULL;
     if (a->rows < 0 || a->width < 0 || a->num_pages < 0 || a->table_stride < a->width)
         return GDN_ERR_SHAPE;
+    // walked with 32-bit indices, and steps past the last
+    if (a->num_pages > kMaxPages || a->width > kMaxPages || (int64_t)a->rows * a->width > kMaxPages)
+        return GDN_ERR_OVERFLOW;
     if ((a->rows > 0 && a->width > 0 && !a->table) || (a->num_pages > 0 && !a->refs))
         return GDN_ERR_NULL;
     if (!aligned(a->table, 4) || !aligned(a->refs, 4))

@@ -613,7 +613,8 @@ gdn_status gdn_attention_decode(const gdn_attention_args *args, int32_t batch,
  * A request for a row outside [0, rows), to change a row that an earlier request of the
  * call names too, or on rows that do not hold what it needs is refused: its status is 2 and
  * nothing of it is done. Entries outside [0, num_pages) count as none.
- * Calls on one table and refs are ordered by the caller; n is at most 1024 (else OVERFLOW).
+ * Calls on one table and refs are ordered by the caller; n is at most 1024, num_pages, width
+ * and rows * width at most 2^30 (else OVERFLOW).
  * Errors: NULL, SHAPE, OVERFLOW, ALIGN, WORKSPACE, LAUNCH.
  * ------------------------------------------------------------------------- */
 typedef struct gdn_page_args {

@@ -200,3 +200,13 @@ def test_sequences_of_more_than_2_30_keys_are_refused():
     assert prefill(n=1, cq=(0, 5), ck=(0, far), **paged) == OVERFLOW
     assert decode(max_len=far, **paged) == OVERFLOW
     assert decode(max_len=5, prefix=A, prefix_len=far, **paged) == OVERFLOW
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_page_counts_past_their_walks_are_refused(name):
+    """Pages and entries are walked with 32-bit indices: more than 2^30 pages, or entries in all rows, are refused."""
+    most = 1 << 30
+    call, lib = CALLS[name], ops.load()
+    assert call(lib, pages(num_pages=most + 1)) == OVERFLOW
+    assert call(lib, pages(rows=1 << 15, width=(1 << 15) + 1, table_stride=1 << 16)) == OVERFLOW
+    assert call(lib, pages(rows=1, width=most + 1, table_stride=most + 1)) == OVERFLOW
