@@ -45,6 +45,8 @@ __global__ __launch_bounds__(256) void join_few_kernel(const AttnParams p, int64
     for (int x = 32; x; x >>= 1)
         most = fmaxf(most, __shfl_xor(most, x, 64));
     const float f = st.y == 0.f ? 0.f : exp2_f(st.x - most);
+    // a run without keys left its outputs as they were; one whose factor f32 holds as 0 counts, for what is not finite in it
+    const uint64_t there = __ballot(st.y != 0.f);
     float total = f * st.y;
 #pragma unroll
     for (int x = 32; x; x >>= 1)
@@ -53,18 +55,18 @@ __global__ __launch_bounds__(256) void join_few_kernel(const AttnParams p, int64
     for (int s0 = 0; s0 < p.slots; s0 += GROUPS * TURNS) {
         f32x4 v[TURNS];
         float w[TURNS];
+        bool in[TURNS];
 #pragma unroll
         for (int i = 0; i < TURNS; ++i) {
             const int s = s0 + i * GROUPS + group;
             w[i] = __shfl(f, s & 63, 64);
-            if (group >= GROUPS || s >= p.slots)
-                w[i] = 0.f;
-            // a run without keys left its outputs as they were: the first run's are read again, and left out
-            v[i] = *reinterpret_cast<const f32x4 *>(p.part + (first + (w[i] == 0.f ? 0 : s)) * D + d);
+            in[i] = group < GROUPS && s < p.slots && (there >> (s & 63) & 1);
+            // in place of what is left out the first run's are read
+            v[i] = *reinterpret_cast<const f32x4 *>(p.part + (first + (in[i] ? s : 0)) * D + d);
         }
 #pragma unroll
         for (int i = 0; i < TURNS; ++i)
-            o += w[i] == 0.f ? f32x4{} : w[i] * v[i];
+            o += in[i] ? w[i] * v[i] : f32x4{};
     }
     if constexpr (GROUPS > 1) {
 #pragma unroll
