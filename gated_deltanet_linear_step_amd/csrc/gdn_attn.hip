@@ -260,7 +260,7 @@ void attn_decode_splits(int Hq, int Hkv, int D, int B, int T, int max_len, int *
     if (!few_rows(Hq, Hkv, T)) {
         const int KT = D <= 128 ? 64 : 32;
         const int64_t tiles = (std::max(max_len, 1) + KT - 1) / KT, want = std::clamp<int64_t>(2 * kCus / blocks, 1, 64);
-        *split_keys = (int)std::max<int64_t>((tiles + want - 1) / want, 4);
+        *split_keys = (int)std::clamp<int64_t>((tiles + want - 1) / want, 4, kMostKeys / KT);
         *splits = (int)((tiles + *split_keys - 1) / *split_keys);
         return;
     }

@@ -16,7 +16,7 @@ namespace {
 using namespace gdn::checks;
 
 constexpr int64_t kMaxStride = (int64_t)1 << 24;   // a tile's rows are addressed with 32-bit byte offsets
-constexpr int64_t kMaxKeys = (int64_t)1 << 30;     // of a sequence
+constexpr int64_t kMaxKeys = (int64_t)1 << 30;     // of a sequence in a decode step, split into runs of at most kMostKeys
 constexpr int64_t kMaxPages = (int64_t)1 << 30;    // of a pool, and entries of its table
 constexpr int64_t kMaxBlocks = (int64_t)1 << 24;   // a launch holds fewer than 2^32 threads, 256 of them a workgroup
 
@@ -308,7 +308,7 @@ gdn_status gdn_attention_prefill(const gdn_attention_args *args, int32_t num_seq
         return GDN_ERR_NULL;
     if (args->page_size > 0 && longest_k > 0 && (args->num_pages < 1 || args->table_stride < (longest_k + args->page_size - 1) / args->page_size))
         return GDN_ERR_SHAPE;
-    if (longest_k > kMaxKeys)
+    if (longest_k > gdn::kMostKeys)
         return GDN_ERR_OVERFLOW;
     p.N = num_seqs;
     p.total = total;
@@ -353,7 +353,7 @@ gdn_status gdn_attention_decode(const gdn_attention_args *args, int32_t batch, i
     if (!args)
         return GDN_ERR_NULL;
     const int64_t queries = (int64_t)batch * tokens_per_seq;
-    if (queries > kI32Max || max_len > kMaxKeys || prefix_len > kMaxKeys)
+    if (queries > kI32Max || max_len > kMaxKeys || prefix_len > gdn::kMostKeys)
         return GDN_ERR_OVERFLOW;
     const gdn_status st = check_attention(args, queries, p.a);
     if (st != GDN_OK)

@@ -204,7 +204,9 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
     }
     const float scale = p.a.scale * 1.4426950408889634f;  // exponentials in base 2
     f32x16 o[TV] = {};
-    float top = kNone, sum = 0.f;
+    // The sum of the weights, those of up to 16 tiles apart: one sum of all would lose what is below 2^-25 of it and drift by the rounding of
+    // each (2^20 weights of 0.67: 0.35 % off, now 2e-5).
+    float top = kNone, sum = 0.f, recent = 0.f;
 
     auto largest = [&](const f32x16 &s) {
         float x = fmaxf(s[0], s[1]);
@@ -220,6 +222,7 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
             const float up = fmaxf(top, most), f = up == kNone ? 1.f : exp2_f(top - up);
             top = up;
             sum *= f;
+            recent *= f;
 #pragma unroll
             for (int t = 0; t < TV; ++t)
                 o[t] *= f;
@@ -283,8 +286,8 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
                         e[2 * i + 1] = exp2_f(fmaf(s[2 * i + 1], scale, -base));
                     }
                     if (i * KC / 8 + 1 == c) {
-                        sum += e[2 * i];
-                        sum += e[2 * i + 1];
+                        recent += e[2 * i];
+                        recent += e[2 * i + 1];
                         pf[i / 4][i % 4] = pack2<DT>(e[2 * i], e[2 * i + 1]);
                     }
                 }
@@ -311,8 +314,8 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
                 const float x = exp2_f(fmaf(s[i], scale, -base)), y = exp2_f(fmaf(s[i + 1], scale, -base));
-                sum += x;
-                sum += y;
+                recent += x;
+                recent += y;
                 pf[i / 8][i % 8 / 2] = pack2<DT>(x, y);
             }
 #pragma unroll
@@ -352,8 +355,8 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
             const float x = exp2_f(fmaf(s[i], scale, -base)), y = exp2_f(fmaf(s[i + 1], scale, -base));
-            sum += x;
-            sum += y;
+            recent += x;
+            recent += y;
             pf[i / 8][i % 8 / 2] = pack2<DT>(x, y);
         }
         if constexpr (!AHEAD) {
@@ -424,6 +427,10 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
     }
     // read_on: the next step's first operands are read as soon as the tile is here, at kt
     auto turn = [&](int tile, bool read_on, uint32_t kt) {
+        if (((tile - first) & 15) == 15) {
+            sum += recent;
+            recent = 0.f;
+        }
         From from{kb, vb, 0, 0};
         if (tile + 2 < last)
             from = locate(tile + 2);
@@ -467,7 +474,7 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
         turn(tile, false, 0);
     }
 
-    sum = half_sum(sum);
+    sum = half_sum(sum + recent);
     const int end_row = wrow + opaque(col);
     if (end_row >= rows)
         return;
@@ -503,8 +510,9 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
         p.a.lse[at] = sum == 0.f ? kNone : (top + __log2f(sum)) * 0.69314718055994531f;
 }
 
+// Waves of a SIMD: what the LDS holds, but of 64 wide heads three (168 registers), not four.
 template <int DT, int D, bool PAGED>
-__global__ __launch_bounds__(kThreads, 2) void prefill_kernel(const AttnPrefillParams p)
+__global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void prefill_kernel(const AttnPrefillParams p)
 {
     prefill_block<DT, D, PAGED>(p);
 }

@@ -569,7 +569,8 @@ typedef struct gdn_attention_args {
  * Rows behind cu_q[num_seqs] are not touched.
  * Errors: NULL, SHAPE (counts, strides, offsets; table rows shorter than a sequence),
  * UNSUPPORTED, OVERFLOW (a row stride of 2^24 elements or more, more than 2^31 - 1 rows times
- * heads, more than 2^30 keys of a sequence or a grid of 2^32 threads), ALIGN, WORKSPACE, LAUNCH. */
+ * heads, more than 2^21 keys of a sequence, which f32 sums no longer resolve, or a grid of 2^32
+ * threads), ALIGN, WORKSPACE, LAUNCH. */
 size_t gdn_attention_prefill_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                              int32_t num_seqs, int32_t total_tokens);
 gdn_status gdn_attention_prefill(const gdn_attention_args *args, int32_t num_seqs,
@@ -589,7 +590,7 @@ gdn_status gdn_attention_prefill(const gdn_attention_args *args, int32_t num_seq
  *   prefix_table   [ceil(prefix_len / page_size)] int32 pages of the prefix; NULL where
  *                  prefix_len is 0
  *   workspace      as above
- * Errors: as gdn_attention_prefill's. */
+ * Errors: as gdn_attention_prefill's (OVERFLOW: max_len above 2^30, prefix_len above 2^21). */
 size_t gdn_attention_decode_workspace_bytes(int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                             int32_t batch, int32_t tokens_per_seq, int32_t max_len,
                                             int32_t prefix_len);

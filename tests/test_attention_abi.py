@@ -210,3 +210,14 @@ def test_page_counts_past_their_walks_are_refused(name):
     assert call(lib, pages(num_pages=most + 1)) == OVERFLOW
     assert call(lib, pages(rows=1 << 15, width=(1 << 15) + 1, table_stride=1 << 16)) == OVERFLOW
     assert call(lib, pages(rows=1, width=most + 1, table_stride=most + 1)) == OVERFLOW
+
+
+def test_runs_of_more_keys_than_their_sums_resolve_are_refused():
+    """2^21 keys of a prompt's sequence and of a prefix; a step's own keys are split, whatever their number."""
+    most = 1 << 21
+    paged = dict(page_size=1024, num_pages=3, table=A, table_stride=1 << 22, k_stride=1 << 20, v_stride=1 << 20, ws=None)
+    assert prefill(n=1, cq=(0, 5), ck=(0, most), **paged) == WORKSPACE
+    assert prefill(n=1, cq=(0, 5), ck=(0, most + 1), **paged) == OVERFLOW
+    assert decode(max_len=5, prefix=A, prefix_len=most, **paged) == WORKSPACE
+    assert decode(max_len=5, prefix=A, prefix_len=most + 1, **paged) == OVERFLOW
+    assert decode(max_len=1 << 30, **paged) == WORKSPACE and decode(T=70, max_len=1 << 30, **paged) == WORKSPACE
