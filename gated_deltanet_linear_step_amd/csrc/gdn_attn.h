@@ -34,7 +34,8 @@ struct KvSource {
 };
 
 // What the attention kernels share. Partial results go to `part` where a query's keys are
-// split: [token][head][slot] rows of D f32, with (maximum, sum) pairs in `stat`.
+// split: [token][head][slot] rows of D f32, with pairs in `stat`: the score,
+// not scaled, that the weights are relative to, and their sum.
 struct AttnParams {
     int Hq, Hkv, D, dt;
     float scale;

@@ -3,7 +3,7 @@
 //
 // Where a call has few rows, a row's keys are split into runs that go to workgroups of
 // their own. Each leaves its outputs relative to its own maximum m, with m and the sum l:
-//     o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s,   M = max_s m_s
+//     o = sum_s e^(scale (m_s - M)) o_s / sum_s e^(scale (m_s - M)) l_s,   M = max_s m_s
 // joins them. A run without keys has l = 0 and no outputs.
 
 #include "gdn_attn_device.h"
@@ -24,7 +24,7 @@ __device__ __forceinline__ void store_joined(const AttnParams &p, int64_t row, i
     uint16_t *to = static_cast<uint16_t *>(p.out) + token * p.out_stride + head * p.D + d;
     *reinterpret_cast<u32x2 *>(to) = u32x2{pack2<DT>(o.x * inv, o.y * inv), pack2<DT>(o.z * inv, o.w * inv)};
     if (p.lse && d == 0)
-        p.lse[row] = total == 0.f ? kNone : (most + __log2f(total)) * 0.69314718055994531f;
+        p.lse[row] = total == 0.f ? kNone : (most * base2(p.scale) + __log2f(total)) * 0.69314718055994531f;
 }
 
 // Up to 64 runs: a wave joins a row (a query and head). A lane looks at one run's maximum and sum; then D / 4 lanes
@@ -44,7 +44,7 @@ __global__ __launch_bounds__(256) void join_few_kernel(const AttnParams p, int64
 #pragma unroll
     for (int x = 32; x; x >>= 1)
         most = fmaxf(most, __shfl_xor(most, x, 64));
-    const float f = st.y == 0.f ? 0.f : exp2_f(st.x - most);
+    const float f = st.y == 0.f ? 0.f : exp2_f((st.x - most) * base2(p.scale));
     // a run without keys left its outputs as they were; one whose factor f32 holds as 0 counts, for what is not finite in it
     const uint64_t there = __ballot(st.y != 0.f);
     float total = f * st.y;
@@ -111,7 +111,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(const AttnParams p)
         const float2 st = p.stat[first + s];
         if (st.y == 0.f)
             continue;
-        const float f = exp2_f(st.x - most);
+        const float f = exp2_f((st.x - most) * base2(p.scale));
         total += f * st.y;
         o += f * *reinterpret_cast<const f32x4 *>(p.part + (first + s) * p.D + d);
     }

@@ -123,7 +123,7 @@ __device__ __forceinline__ void decode_run(const AttnDecodeParams &p)
             asm volatile("" : "+v"(q[r][c]));
     asm volatile("" : "+v"(pages));
 
-    const float scale = p.a.scale * 1.4426950408889634f;  // exponentials in base 2
+    const float scale = base2(p.a.scale);
     f32x4 o[NR][TV] = {};
     float top[NR], sum[NR];
 #pragma unroll
@@ -179,9 +179,9 @@ __device__ __forceinline__ void decode_run(const AttnDecodeParams &p)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     most = fmaxf(most, s[r][t][i]);
-            most = rows_max(most) * scale;
-            if (__ballot(most > top[r] + 8.f) != 0) {  // as in the prompts' kernel
-                const float up = fmaxf(top[r], most), f = up == kNone ? 1.f : exp2_f(top[r] - up);
+            most = rows_max(most);
+            if (__ballot((most - top[r]) * scale > 8.f) != 0) {  // as in the prompts' kernel
+                const float up = fmaxf(top[r], most), f = up == kNone ? 1.f : exp2_f((top[r] - up) * scale);
                 top[r] = up;
                 sum[r] *= f;
 #pragma unroll
@@ -193,7 +193,7 @@ __device__ __forceinline__ void decode_run(const AttnDecodeParams &p)
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int i = 0; i < 4; i += 2) {
-                    const float x = exp2_f(fmaf(s[r][t][i], scale, -base)), y = exp2_f(fmaf(s[r][t][i + 1], scale, -base));
+                    const float x = exp2_f((s[r][t][i] - base) * scale), y = exp2_f((s[r][t][i + 1] - base) * scale);
                     sum[r] += x;
                     sum[r] += y;
                     pf[r][2 * t + i / 2] = pack2<DT>(x, y);
@@ -286,7 +286,7 @@ __device__ __forceinline__ void decode_run(const AttnDecodeParams &p)
         f32x4 x = {};
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) {
-            const float f = exp2_f(stats[w][row].x - base);
+            const float f = exp2_f((stats[w][row].x - base) * scale);
             total += f * stats[w][row].y;
             x += f * *reinterpret_cast<const f32x4 *>(results + (w * NR * 16 + row) * D + d);
         }
@@ -303,7 +303,7 @@ __device__ __forceinline__ void decode_run(const AttnDecodeParams &p)
             uint16_t *out = static_cast<uint16_t *>(p.a.out) + (int64_t)(b * p.T + token) * p.a.out_stride + (int64_t)head * D + d;
             *reinterpret_cast<u32x2 *>(out) = u32x2{pack2<DT>(x.x * inv, x.y * inv), pack2<DT>(x.z * inv, x.w * inv)};
             if (p.a.lse && d == 0)
-                p.a.lse[to] = total == 0.f ? kNone : (most + __log2f(total)) * 0.69314718055994531f;
+                p.a.lse[to] = total == 0.f ? kNone : (most * scale + __log2f(total)) * 0.69314718055994531f;
         }
     }
 }

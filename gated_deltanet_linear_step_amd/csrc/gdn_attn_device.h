@@ -157,6 +157,14 @@ __device__ __forceinline__ float half_sum(float x)
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+// Scores' factor for exponentials in base 2
+__device__ __forceinline__ float base2(float scale) { return scale * 1.4426950408889634f; }
+
+// Exponents in base 2 are formed as scale s - base in one instruction, with base the rounded product of scale and the row's
+// maximum. What that rounding left out raises every weight of a row alike: by less than 2^-14 of itself while |base| <= 2^10, but
+// without bound beyond (at 2^36, by 2^4096 or to nothing). Rows past that take the maximum from the scores first.
+constexpr float kFar = 1024.f;
+
 __device__ __forceinline__ float exp2_f(float x) { return __builtin_amdgcn_exp2f(x); }
 
 }  // namespace attn

@@ -202,11 +202,13 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
         for (int c = 0; c < KC; ++c)
             q[c] = *reinterpret_cast<const u32x4 *>(from + 32 * c);
     }
-    const float scale = p.a.scale * 1.4426950408889634f;  // exponentials in base 2
+    const float scale = base2(p.a.scale);
     f32x16 o[TV] = {};
     // The sum of the weights, those of up to 16 tiles apart: one sum of all would lose what is below 2^-25 of it and drift by the rounding of
     // each (2^20 weights of 0.67: 0.35 % off, now 2e-5).
     float top = kNone, sum = 0.f, recent = 0.f;
+    float base = 0.f;  // exponentials are 2^(scale s - base)
+    bool far = false;  // of any row of the wave: kFar
 
     auto largest = [&](const f32x16 &s) {
         float x = fmaxf(s[0], s[1]);
@@ -215,19 +217,23 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
             x = fmaxf(fmaxf(x, s[i]), s[i + 1]);
         return x;
     };
-    // Takes the largest of 32 scores into the running maximum where it passes that by 8
-    auto rescale = [&](float most) {
-        most = half_max(most) * scale;
-        if (__ballot(most > top + 8.f) != 0) {
-            const float up = fmaxf(top, most), f = up == kNone ? 1.f : exp2_f(top - up);
+    // Takes the largest of the 32 scores s into the running maximum where it passes that by 8 in base 2
+    auto rescale = [&](float most, f32x16 &s) {
+        most = half_max(most);
+        if (__ballot((most - top) * scale > 8.f) != 0) {
+            const float up = fmaxf(top, most), f = up == kNone ? 1.f : exp2_f((top - up) * scale);
             top = up;
+            base = up == kNone ? 0.f : up * scale;
+            far = __ballot(fabsf(base) > kFar) != 0;
+            base = far ? 0.f : base;
             sum *= f;
             recent *= f;
 #pragma unroll
             for (int t = 0; t < TV; ++t)
                 o[t] *= f;
         }
-        return top == kNone ? 0.f : top;
+        if (far)
+            s -= top == kNone ? 0.f : top;
     };
     auto scores = [&](f32x16 &s, uint32_t kt) {
         const uint32_t k_at = opaque(kt + G_::k_at(col, half));
@@ -252,7 +258,6 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
     constexpr bool AHEAD = D <= 128;
     constexpr int READ = 3;  // operands read ahead
     u32x4 kf[KC];
-    float base = 0.f;
     auto read_k = [&](uint32_t kt) {
         const uint32_t k_at = opaque(kt + G_::k_at(col, half));
 #pragma unroll
@@ -309,7 +314,7 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
                 __builtin_amdgcn_sched_barrier(0);
             }
             if (go_on)
-                base = rescale(most);
+                rescale(most, next);
         } else {
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
@@ -325,7 +330,7 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
                     o[tv] = T::mfma32(v_of(v_at, tv, st), pf[st], o[tv]);
             scores(next, next_kt);
             if (go_on)
-                base = rescale(largest(next));
+                rescale(largest(next), next);
         }
     };
 
@@ -350,7 +355,7 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
             const int key = 8 * (i / 4) + 4 * half + i % 4;
             s[i] = k0 + key < seen && !(none >> (i / 8) & 1) ? s[i] : kNone;
         }
-        const float base = rescale(largest(s));
+        rescale(largest(s), s);
         u32x4 pf[2];
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
@@ -451,7 +456,7 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
         f32x16 s[HALVES];
         static_assert(AHEAD == (HALVES == 2), "two sets of scores, or one");
         scores(s[0], lds0);
-        base = rescale(largest(s[0]));
+        rescale(largest(s[0]), s[0]);
         if constexpr (AHEAD)
             read_k(lds0 + 32 * G_::PITCH);
         do {
@@ -507,7 +512,7 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
             *reinterpret_cast<u32x2 *>(to + 32 * tv + 8 * g + 4 * half) = w;
         }
     if (p.a.lse && half == 0)
-        p.a.lse[at] = sum == 0.f ? kNone : (top + __log2f(sum)) * 0.69314718055994531f;
+        p.a.lse[at] = sum == 0.f ? kNone : (top * scale + __log2f(sum)) * 0.69314718055994531f;
 }
 
 // Waves of a SIMD: what the LDS holds, but of 64 wide heads three (168 registers), not four.

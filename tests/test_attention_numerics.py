@@ -6,7 +6,7 @@ import math
 import pytest
 import torch
 
-from attn_reference import E, half_step, near
+from attn_reference import E, attention64, causal, half_step, near
 from gated_deltanet_linear_step_amd import ops
 
 pytestmark = pytest.mark.gpu
@@ -79,3 +79,89 @@ def test_sums_of_many_weights(D, dtype, weak, n):
     cu, cu_k = torch.tensor([0, 1], dtype=torch.int32), torch.tensor([0, n], dtype=torch.int32)
     out = ops.attention_prefill(q, kp, vp, cu, cu_k=cu_k, table=table, lse=lse, scale=1.0)
     check_strong(out, lse, n, weak, 1.0, dtype)
+
+
+def huge(n, T, Hq, Hkv, D, dtype, seed):
+    """Queries and keys of small integers times a power of two: their products' f32 sums are exact, 2^22 (f16) or 2^36 (bf16) times an integer."""
+    gen = torch.Generator().manual_seed(seed)
+    times = 2.0 ** 11 if dtype == F16 else 2.0 ** 18
+    q, k = (torch.randint(-6, 7, (m, h, D), generator=gen).double() * times for m, h in ((T, Hq), (n, Hkv)))
+    v = torch.randn(n, Hkv, D, generator=gen)
+    return q.to(dtype).to(DEV), k.to(dtype).to(DEV), v.to(dtype).to(DEV)
+
+
+def check_huge(out, lse, q, k, v, sees, scale):
+    """The value of the largest score, the mean where several have it: the next is 2^22 times scale below, of weight 0. Equal scores have
+    equal weights, off by u where they enter the product and not in their sum; u of the result, 16 E for the rest. lse is a product and a
+    log2, of 8 E and 2^-20."""
+    T, Hq, D = q.shape
+    G = Hq // k.shape[1]
+    for h in range(Hq):
+        s = q[:, h].double() @ k[:, h // G].double().T
+        assert float(s.abs().max()) < 2.0 ** 24 * float(s[s != 0].abs().min())
+        s = torch.where(sees, s, -INF)
+        top = s.amax(1, keepdim=True)
+        hit = ((s == top) & sees).double()
+        some = hit.sum(1, keepdim=True).clamp_min(1)
+        want = hit @ v[:, h // G].double() / some
+        size = hit @ v[:, h // G].double().abs() / some
+        room = size * (16 * E + half_step(q.dtype)) + want.abs() * half_step(q.dtype) + (2.0 ** -25 if q.dtype == F16 else 0)
+        near(out[:, h], want, room)
+        want = torch.where(sees.any(1), top[:, 0] * scale + some[:, 0].log(), -INF)
+        near(lse[:, h], want, torch.where(sees.any(1), want.abs() * 8 * E + 2.0 ** -20, 0.0))
+
+
+@pytest.mark.parametrize("D,dtype", [(64, B16), (96, F16), (128, B16), (128, F16), (256, B16), (256, F16)])
+@pytest.mark.parametrize("T,n", [(200, 200), (300, 3000), (3, 20000)])
+def test_huge_scores(D, dtype, T, n):
+    Hq, Hkv = 4, 2
+    q, k, v = huge(n, T, Hq, Hkv, D, dtype, D + n)
+    lse = torch.empty(T, Hq, device=DEV)
+    scale = 0.11
+    cu, cu_k = torch.tensor([0, T], dtype=torch.int32), torch.tensor([0, n], dtype=torch.int32)
+    out = ops.attention_prefill(q, k, v, cu, cu_k=cu_k, lse=lse, scale=scale)
+    sees = torch.arange(n, device=DEV)[None] <= torch.arange(T, device=DEV)[:, None] + n - T
+    check_huge(out, lse, q, k, v, sees, scale)
+
+
+@pytest.mark.parametrize("D,dtype", [(64, F16), (96, B16), (128, B16), (256, B16)])
+@pytest.mark.parametrize("Hq,n,prefix,T", [(4, 90, 0, 1), (4, 9000, 0, 2), (4, 700, 640, 3), (4, 70000, 0, 1), (40, 300, 160, 2)])
+def test_huge_scores_in_steps(D, dtype, Hq, n, prefix, T):
+    Hkv, ps = 2, 32
+    q, k, v = huge(n + prefix, T, Hq, Hkv, D, dtype, D + n)
+    pages = -(-(n + prefix) // ps)
+    pad = torch.zeros(pages * ps - n - prefix, Hkv, D, dtype=dtype, device=DEV)
+    kp, vp = (torch.cat([x, pad]).view(pages, ps, Hkv, D).transpose(1, 2).contiguous() for x in (k, v))
+    table = torch.arange(pages, dtype=torch.int32, device=DEV)
+    lse = torch.empty(T, Hq, device=DEV)
+    out = ops.attention_decode(q, kp, vp, table[None, prefix // ps:].contiguous(), torch.tensor([n], dtype=torch.int32, device=DEV), batch=1,
+                               tokens_per_seq=T, max_len=n, prefix_table=table[:prefix // ps].contiguous() if prefix else None,
+                               prefix_len=prefix, lse=lse, scale=0.11)
+    sees = torch.arange(n + prefix, device=DEV)[None] <= torch.arange(T, device=DEV)[:, None] + n + prefix - T
+    check_huge(out, lse, q, k, v, sees, 0.11)
+
+
+@pytest.mark.parametrize("D,dtype", [(64, B16), (96, F16), (128, B16), (128, F16), (256, B16)])
+@pytest.mark.parametrize("n", [150, 4000])
+def test_rows_of_every_size_beside_one_another(D, dtype, n):
+    """Scores of 2^-8 to 2^18 in the rows of one wave, prompts and steps."""
+    gen = torch.Generator().manual_seed(D + n)
+    T, Hq, Hkv = 40, 4, 2
+    q = torch.randn(T, Hq, D, generator=gen) * 2.0 ** (torch.arange(T) % 20 - 8.0)[:, None, None]
+    k, v = (torch.randn(n, Hkv, D, generator=gen) for _ in range(2))
+    q, k, v = (x.to(dtype).to(DEV) for x in (q, k, v))
+    lse = torch.empty(T, Hq, device=DEV)
+    cu, cu_k = torch.tensor([0, T], dtype=torch.int32), torch.tensor([0, n], dtype=torch.int32)
+    sees = causal(T, n, DEV)
+    want = attention64(q, k, v, sees, 1.0)
+    out = ops.attention_prefill(q, k, v, cu, cu_k=cu_k, lse=lse, scale=1.0)
+    near(out, want[0], want[2])
+    near(lse, want[1], want[3])
+    pages = -(-n // 16)
+    kp, vp = (torch.cat([x, x[:pages * 16 - n]]).view(pages, 16, Hkv, D).transpose(1, 2).contiguous() for x in (k, v))
+    table = torch.arange(pages, dtype=torch.int32, device=DEV)[None]
+    for rows in (slice(0, 1), slice(33, 40), slice(0, 40)):
+        T = rows.stop - rows.start
+        lens = torch.tensor([n - 40 + rows.stop], dtype=torch.int32, device=DEV)
+        out = ops.attention_decode(q[rows], kp, vp, table, lens, batch=1, tokens_per_seq=T, max_len=n, scale=1.0)
+        near(out, want[0][rows], want[2][rows])
