@@ -24,7 +24,7 @@ __device__ __forceinline__ void store_joined(const AttnParams &p, int64_t row, i
     uint16_t *to = static_cast<uint16_t *>(p.out) + token * p.out_stride + head * p.D + d;
     *reinterpret_cast<u32x2 *>(to) = u32x2{pack2<DT>(o.x * inv, o.y * inv), pack2<DT>(o.z * inv, o.w * inv)};
     if (p.lse && d == 0)
-        p.lse[row] = total == 0.f ? kNone : (most * base2(p.scale) + __log2f(total)) * 0.69314718055994531f;
+        p.lse[row] = log_sum<DT>(most, p.scale, total);
 }
 
 // Up to 64 runs: a wave joins a row (a query and head). A lane looks at one run's maximum and sum; then D / 4 lanes

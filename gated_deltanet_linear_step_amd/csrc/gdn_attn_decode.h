@@ -193,7 +193,7 @@ __device__ __forceinline__ void decode_run(const AttnDecodeParams &p)
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int i = 0; i < 4; i += 2) {
-                    const float x = exp2_f((s[r][t][i] - base) * scale), y = exp2_f((s[r][t][i + 1] - base) * scale);
+                    const float x = exp2_f(fmaf(s[r][t][i] - base, scale, T::kLift)), y = exp2_f(fmaf(s[r][t][i + 1] - base, scale, T::kLift));
                     sum[r] += x;
                     sum[r] += y;
                     pf[r][2 * t + i / 2] = pack2<DT>(x, y);
@@ -303,7 +303,7 @@ __device__ __forceinline__ void decode_run(const AttnDecodeParams &p)
             uint16_t *out = static_cast<uint16_t *>(p.a.out) + (int64_t)(b * p.T + token) * p.a.out_stride + (int64_t)head * D + d;
             *reinterpret_cast<u32x2 *>(out) = u32x2{pack2<DT>(x.x * inv, x.y * inv), pack2<DT>(x.z * inv, x.w * inv)};
             if (p.a.lse && d == 0)
-                p.a.lse[to] = total == 0.f ? kNone : (most * scale + __log2f(total)) * 0.69314718055994531f;
+                p.a.lse[to] = log_sum<DT>(most, p.a.scale, total);
         }
     }
 }

@@ -31,6 +31,8 @@ constexpr float kNone = -__builtin_inff();
 // in place of the first run's sum: the outputs are there, nothing is joined
 constexpr float kJoined = -1.f;
 
+// kLift: weights are 2^kLift times what they are beside the row's largest, so that f16 keeps their accuracy down to 2^-21 of that and
+// drops them below 2^-32 (bf16 has f32's exponents). With a maximum that is passed by up to 2^8, at most 2^15.
 template <int DT>
 struct Type16;
 template <>
@@ -38,6 +40,7 @@ struct Type16<DT_BF16> {
     typedef __bf16 T8 __attribute__((ext_vector_type(8)));
     typedef __bf16 T2 __attribute__((ext_vector_type(2)));
     static constexpr uint32_t kExponents = 0x7f807f80u, kLow = 0x00800080u;
+    static constexpr int kLift = 0;
     __device__ __forceinline__ static f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c)
     {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(T8, a), __builtin_bit_cast(T8, b), c, 0, 0, 0);
@@ -52,6 +55,7 @@ struct Type16<DT_F16> {
     typedef _Float16 T8 __attribute__((ext_vector_type(8)));
     typedef _Float16 T2 __attribute__((ext_vector_type(2)));
     static constexpr uint32_t kExponents = 0x7c007c00u, kLow = 0x04000400u;
+    static constexpr int kLift = 7;
     __device__ __forceinline__ static f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c)
     {
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(T8, a), __builtin_bit_cast(T8, b), c, 0, 0, 0);
@@ -161,11 +165,19 @@ __device__ __forceinline__ float half_sum(float x)
 __device__ __forceinline__ float base2(float scale) { return scale * 1.4426950408889634f; }
 
 // Exponents in base 2 are formed as scale s - base in one instruction, with base the rounded product of scale and the row's
-// maximum. What that rounding left out raises every weight of a row alike: by less than 2^-14 of itself while |base| <= 2^10, but
-// without bound beyond (at 2^36, by 2^4096 or to nothing). Rows past that take the maximum from the scores first.
+// maximum (less kLift). What that rounding left out raises every weight of a row alike: by less than 2^-13 of itself while |base| <= 2^10,
+// but without bound beyond (at 2^36, by 2^4096 or to nothing). Rows past that take the maximum from the scores first.
 constexpr float kFar = 1024.f;
 
 __device__ __forceinline__ float exp2_f(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// ln of the sum of e^(scale s), from the sum of the weights relative to the score `top`
+template <int DT>
+__device__ __forceinline__ float log_sum(float top, float scale, float sum)
+{
+    constexpr float one = 1 << Type16<DT>::kLift;
+    return sum == 0.f ? kNone : (top * base2(scale) + __log2f(sum * (1.f / one))) * 0.69314718055994531f;
+}
 
 }  // namespace attn
 }  // namespace gdn

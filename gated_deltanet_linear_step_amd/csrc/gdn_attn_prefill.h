@@ -10,16 +10,15 @@
 //  * As they lie, the exponentials are the operand of O^T += V^T P^T: the product's slot 8 h + e is key 4 h + e (e < 4) or
 //    8 + 4 h + e - 4 of 16, and V^T is read in that order by transposing LDS reads. Nothing passes between lanes.
 //  * The running maximum moves only where a row's scores pass it by more than 2^8: sums and outputs are rescaled a few
-//    times at a row's start and hardly ever after. Exponentials are then at most 2^8, which f32 and either 16-bit type hold
-//    with the same relative error.
+//    times at a row's start and hardly ever after. Exponentials are then at most 2^8, of f16 2^15 (Type16: kLift).
 //  * K and V tiles go from memory straight to the LDS, one to two tiles ahead, two buffers for K and three for V: one barrier
 //    a tile. Their 16-byte blocks are permuted within a row by the address that a lane fetches from, so that
 //    reads fall into different banks.
 //  * Tiles that every row of the block sees run in a loop of their own without masks. It goes 32 keys at a time: the next
 //    scores are formed beside the exponentials of these, and the next maximum beside the products with V. Tiles with masked
 //    places (the diagonal, the last keys, missing pages) are apart.
-//  * P is rounded to the 16 bits of V, 2^-9 (bf16) or 2^-12 of each term, as much as the outputs' own rounding; its sum is of
-//    the unrounded ones.
+//  * P is rounded to the 16 bits of V, by up to 2^-8 (bf16) or 2^-11 (f16, of weights from 2^-21 of the row's largest on; below by
+//    up to 2^-32 of that) of each term, as much as the outputs' own rounding; its sum is of the unrounded ones.
 //
 // Eight prompts of 30,208 tokens, 32 heads over 8 of 128, bf16: 1290 us, 1020 TFLOP/s (a library's product of 8192^3
 // reaches 1356); 16384 tokens, 16 heads over 2 of 256: 1880 us, 1170; 4096 such tokens: 175, of which 21 join parts.
@@ -207,7 +206,7 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
     // The sum of the weights, those of up to 16 tiles apart: one sum of all would lose what is below 2^-25 of it and drift by the rounding of
     // each (2^20 weights of 0.67: 0.35 % off, now 2e-5).
     float top = kNone, sum = 0.f, recent = 0.f;
-    float base = 0.f;  // exponentials are 2^(scale s - base)
+    float base = -T::kLift;  // exponentials are 2^(scale s - base)
     bool far = false;  // of any row of the wave: kFar
 
     auto largest = [&](const f32x16 &s) {
@@ -225,7 +224,7 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
             top = up;
             base = up == kNone ? 0.f : up * scale;
             far = __ballot(fabsf(base) > kFar) != 0;
-            base = far ? 0.f : base;
+            base = (far ? 0.f : base) - T::kLift;
             sum *= f;
             recent *= f;
 #pragma unroll
@@ -512,7 +511,7 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
             *reinterpret_cast<u32x2 *>(to + 32 * tv + 8 * g + 4 * half) = w;
         }
     if (p.a.lse && half == 0)
-        p.a.lse[at] = sum == 0.f ? kNone : (top * scale + __log2f(sum)) * 0.69314718055994531f;
+        p.a.lse[at] = log_sum<DT>(top, p.a.scale, sum);
 }
 
 // Waves of a SIMD: what the LDS holds, but of 64 wide heads three (168 registers), not four.

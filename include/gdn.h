@@ -516,14 +516,14 @@ gdn_status gdn_rope_frequencies(int32_t rotary_dim, double theta, int32_t scalin
  *     o_i = sum_j p_ij v_j,   p_ij = exp(scale q_i k_j) / sum_j exp(scale q_i k_j)
  *
  * over the keys j that query i sees. Scores, their maximum and sum and the outputs are
- * f32 sums; p enters the product with v rounded to the 16 bits of v (relative to the
- * row's largest), and o is rounded once.
+ * f32 sums; p enters the product with v rounded to the 16 bits of v, by up to half a step
+ * (f16, below 2^-21 of the row's largest: by up to 2^-32 of that), and o is rounded once.
  * A query that sees no key, or whose scores are all -inf, has o = 0 and lse = -inf.
  * Infinities and NaN in keys, values or queries that a query does not see do not reach
  * it; in those it sees they make what the formula makes of them not finite (where that
  * is an infinity, a NaN may stand). Outputs are summed before they are divided by the sum of
- * weights, of at most 2^8 each: values of 2^90 and more may leave f32 on the way, as may
- * scores times scale.
+ * weights, of at most 2^8 each (f16 2^15): bf16 values of 2^90 and more may leave f32 on the
+ * way, as may scores times scale.
  *
  *   q_heads, kv_heads   q_heads a multiple of kv_heads, both >= 1
  *   head_dim       64, 96, 128 or 256

@@ -49,7 +49,7 @@ def one_strong_key(D, dtype, Hkv, weak, weak_v, ps):
     return kp, vp
 
 
-def check_strong(out, lse, n, weak, weak_v, dtype):
+def check_strong(out, lse, n, weak, weak_v, dtype, more=0.0):
     """Scores are exact. A weight is off by exp2's 2 E and its argument's 2 weak E, and by u where it enters the product with V. The
     sum of weights is one of at most 512 at a time, in 32 parts or more: (512 + n / 1024) E and 64 E for joins. An output takes 16 keys at
     a time: n / 16 additions of E. Log and product: 4 E of either's value and 8 E."""
@@ -57,7 +57,7 @@ def check_strong(out, lse, n, weak, weak_v, dtype):
     total = 1 + (n - 1) * w
     want = (n - 1) * w * weak_v / total
     weights, sums, u = (2 + 2 * weak) * E, (576 + n / 1024) * E, half_step(dtype)
-    room = abs(want) * (2 * u + 2 * weights + sums + (n / 16) * E)
+    room = abs(want) * (2 * u + 2 * weights + sums + (n / 16) * E) + more
     near(out, torch.full_like(out, want, dtype=torch.float64), torch.full_like(out, room, dtype=torch.float64))
     room = weights + sums + 4 * E * abs(math.log(total)) + 8 * E
     near(lse, torch.full_like(lse, math.log(total), dtype=torch.float64), torch.full_like(lse, room, dtype=torch.float64))
@@ -79,6 +79,40 @@ def test_sums_of_many_weights(D, dtype, weak, n):
     cu, cu_k = torch.tensor([0, 1], dtype=torch.int32), torch.tensor([0, n], dtype=torch.int32)
     out = ops.attention_prefill(q, kp, vp, cu, cu_k=cu_k, table=table, lse=lse, scale=1.0)
     check_strong(out, lse, n, weak, 1.0, dtype)
+
+
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+@pytest.mark.parametrize("weak", [17.5, 12.0])
+def test_f16_weights_far_below_the_largest_count(D, weak):
+    """Weights of e^-17.5 = 2^-25.2 and 2^-17.3 of the largest: off by 2^-32 of that at most where they enter the product."""
+    Hkv, n = 520, 1 << 17
+    kp, vp = one_strong_key(D, F16, Hkv, weak, 100.0, 64)
+    q = torch.zeros(1, Hkv, D, dtype=F16, device=DEV)
+    q[..., 0] = 1
+    table = torch.ones(1, n // 64, dtype=torch.int32, device=DEV)
+    table[0, 0] = 0
+    lse = torch.empty(1, Hkv, device=DEV)
+    cu, cu_k = torch.tensor([0, 1], dtype=torch.int32), torch.tensor([0, n], dtype=torch.int32)
+    out = ops.attention_prefill(q, kp, vp, cu, cu_k=cu_k, table=table, lse=lse, scale=1.0)
+    check_strong(out, lse, n, weak, 100.0, F16, n * 100.0 * 2.0 ** -32)
+
+
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+@pytest.mark.parametrize("weak", [17.5, 12.0])
+def test_f16_weights_far_below_the_largest_count_in_steps(D, weak):
+    """One run of 1024 keys of a sequence; the same keys as a prefix."""
+    n, B = 1024, 600
+    kp, vp = one_strong_key(D, F16, 1, weak, 60000.0, 16)
+    weak_v = float(vp[1, 0, 0, 0])
+    q = torch.zeros(B, 2, D, dtype=F16, device=DEV)
+    q[..., 0] = 1
+    table = torch.ones(B, n // 16, dtype=torch.int32, device=DEV)
+    table[:, 0] = 0
+    lens = torch.full((B,), n, dtype=torch.int32, device=DEV)
+    lse = torch.empty(B, 2, device=DEV)
+    for own, prefix in ((lens, {}), (torch.zeros_like(lens), dict(prefix_table=table[0], prefix_len=n))):
+        out = ops.attention_decode(q, kp, vp, table, own, batch=B, max_len=n, lse=lse, scale=1.0, **prefix)
+        check_strong(out, lse, n, weak, weak_v, F16, n * weak_v * 2.0 ** -32)
 
 
 def huge(n, T, Hq, Hkv, D, dtype, seed):
