@@ -88,12 +88,6 @@ __device__ __forceinline__ uint32_t finite_part(uint32_t w)
     return w & ~(bad * 0xffffu);
 }
 
-template <int DT>
-__device__ __forceinline__ float to_f32(uint32_t h)
-{
-    return DT == DT_BF16 ? bf16_bits_to_f32(h) : f16_bits_to_f32(h);
-}
-
 // 16 bytes at an LDS address, and a transposing read: a lane's four elements are column i (of lane i of 16) of the four rows
 // whose 16 columns, in groups of four, the lanes point at
 __device__ __forceinline__ u32x4 lds_read16(uint32_t at) { return *(const lds_u32x4 *)(uintptr_t)at; }
@@ -111,7 +105,8 @@ __device__ __forceinline__ int opaque(int x)
 
 // Copies 16 bytes a lane from base + off to the LDS, lane l's to byte `to` + 16 l, without waiting. Written out because
 // the compiler lets every transposing LDS read wait for all such copies, those to another buffer too: whoever
-// reads what was copied waits for it (vmcnt) itself. (m0 is the compiler's only as an operand set right before its use.)
+// reads what was copied waits for it (vmcnt) itself. (m0 is reserved: the compiler keeps nothing in it
+// and sets it right before each use of its own, and refuses it as a clobber.)
 __device__ __forceinline__ void copy16(const unsigned char *base, uint32_t off, uint32_t to)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
