@@ -22,7 +22,7 @@ __device__ __forceinline__ void store_joined(const AttnParams &p, int64_t row, i
     const float inv = total == 0.f ? 0.f : 1.f / total;
     const int64_t token = row / p.Hq, head = row - token * p.Hq;
     uint16_t *to = static_cast<uint16_t *>(p.out) + token * p.out_stride + head * p.D + d;
-    *reinterpret_cast<u32x2 *>(to) = u32x2{pack2<DT>(o.x * inv, o.y * inv), pack2<DT>(o.z * inv, o.w * inv)};
+    *reinterpret_cast<u32x2 *>(to) = u32x2{pack_outputs<DT>(o.x * inv, o.y * inv), pack_outputs<DT>(o.z * inv, o.w * inv)};
     if (p.lse && d == 0)
         p.lse[row] = log_sum<DT>(most, p.scale, total);
 }

@@ -301,7 +301,7 @@ __device__ __forceinline__ void decode_run(const AttnDecodeParams &p)
         } else {
             const float inv = total == 0.f ? 0.f : 1.f / total;
             uint16_t *out = static_cast<uint16_t *>(p.a.out) + (int64_t)(b * p.T + token) * p.a.out_stride + (int64_t)head * D + d;
-            *reinterpret_cast<u32x2 *>(out) = u32x2{pack2<DT>(x.x * inv, x.y * inv), pack2<DT>(x.z * inv, x.w * inv)};
+            *reinterpret_cast<u32x2 *>(out) = u32x2{pack_outputs<DT>(x.x * inv, x.y * inv), pack_outputs<DT>(x.z * inv, x.w * inv)};
             if (p.a.lse && d == 0)
                 p.a.lse[to] = log_sum<DT>(most, p.a.scale, total);
         }

@@ -73,6 +73,17 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), typename Type16<DT>::T2));
 }
 
+// Two outputs of a row. Averages of finite f16 values are at most the type's largest, which the rounding of their weights may pass by up
+// to half a step, to where it would become an infinity: they stop there.
+template <int DT>
+__device__ __forceinline__ uint32_t pack_outputs(float lo, float hi)
+{
+    const auto average = [](float x) {
+        return DT == DT_F16 && fabsf(x) < __builtin_inff() ? fminf(fmaxf(x, -65504.f), 65504.f) : x;
+    };
+    return pack2<DT>(average(lo), average(hi));
+}
+
 // The top bits of the halves of w that are infinite or NaN
 template <int DT>
 __device__ __forceinline__ uint32_t not_finite(uint32_t w)

@@ -507,7 +507,8 @@ __device__ __forceinline__ void prefill_block(const AttnPrefillParams &p)
     for (int tv = 0; tv < TV; ++tv)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-            const u32x2 w = {pack2<DT>(o[tv][4 * g] * inv, o[tv][4 * g + 1] * inv), pack2<DT>(o[tv][4 * g + 2] * inv, o[tv][4 * g + 3] * inv)};
+            const u32x2 w = {pack_outputs<DT>(o[tv][4 * g] * inv, o[tv][4 * g + 1] * inv),
+                             pack_outputs<DT>(o[tv][4 * g + 2] * inv, o[tv][4 * g + 3] * inv)};
             *reinterpret_cast<u32x2 *>(to + 32 * tv + 8 * g + 4 * half) = w;
         }
     if (p.a.lse && half == 0)

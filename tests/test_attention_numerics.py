@@ -199,3 +199,29 @@ def test_rows_of_every_size_beside_one_another(D, dtype, n):
         lens = torch.tensor([n - 40 + rows.stop], dtype=torch.int32, device=DEV)
         out = ops.attention_decode(q[rows], kp, vp, table, lens, batch=1, tokens_per_seq=T, max_len=n, scale=1.0)
         near(out, want[0][rows], want[2][rows])
+
+
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+@pytest.mark.parametrize("n", [70, 3000, 40000])
+def test_f16_outputs_of_the_largest_values_are_finite(D, n):
+    """Every value is f16's largest, of either sign by element, and so is every average of them, also where the weights were all
+    rounded up: one key has score 0, the others -0.6926, and e^-0.6926 = 0.50027 rounds to 0.50049."""
+    T, Hq, Hkv = 40, 4, 2
+    largest = torch.finfo(F16).max
+    k = torch.zeros(n, Hkv, D, dtype=F16, device=DEV)
+    k[1:, :, 0] = -1
+    v = torch.where(torch.arange(D, device=DEV) % 3 == 0, -largest, largest).to(F16).expand(n, Hkv, D).contiguous()
+    q = torch.zeros(T, Hq, D, dtype=F16, device=DEV)
+    q[..., 0] = 1
+    want = v[:1, 0].double().expand(T, Hq, D)
+    pages = -(-n // 16)
+    kp, vp = (torch.cat([x, x[:pages * 16 - n]]).view(pages, 16, Hkv, D).transpose(1, 2).contiguous() for x in (k, v))
+    table = torch.arange(pages, dtype=torch.int32, device=DEV)[None]
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    cu, cu_k = torch.tensor([0, T], dtype=torch.int32), torch.tensor([0, n], dtype=torch.int32)
+    outs = [ops.attention_prefill(q, k, v, cu, cu_k=cu_k, scale=0.6926)]
+    for m in (1, 2, T):
+        outs.append(ops.attention_decode(q[T - m:], kp, vp, table, lens, batch=1, tokens_per_seq=m, max_len=n, scale=0.6926))
+    # weights and the average are rounded by half a step each, the sums of weights and of outputs by n E
+    for out in outs:
+        near(out, want[:len(out)], want[:len(out)].abs() * (2 * half_step(F16) + 2 * n * E))
