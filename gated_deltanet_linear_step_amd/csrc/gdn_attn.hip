@@ -44,9 +44,9 @@ __global__ __launch_bounds__(256) void join_few_kernel(const AttnParams p, int64
 #pragma unroll
     for (int x = 32; x; x >>= 1)
         most = fmaxf(most, __shfl_xor(most, x, 64));
-    const float f = st.y == 0.f ? 0.f : exp2_f((st.x - most) * base2(p.scale));
-    // a run without keys left its outputs as they were; one whose factor f32 holds as 0 counts, for what is not finite in it
-    const uint64_t there = __ballot(st.y != 0.f);
+    // a run without keys left its outputs as they were: -1; one whose factor f32 holds as 0 counts, for what is not finite in it
+    // (no mask of runs shifted by a lane's own number here: gdn_device.h, on 64-bit shifts)
+    const float f = st.y == 0.f ? -1.f : exp2_f((st.x - most) * base2(p.scale));
     float total = f * st.y;
 #pragma unroll
     for (int x = 32; x; x >>= 1)
@@ -55,18 +55,18 @@ __global__ __launch_bounds__(256) void join_few_kernel(const AttnParams p, int64
     for (int s0 = 0; s0 < p.slots; s0 += GROUPS * TURNS) {
         f32x4 v[TURNS];
         float w[TURNS];
-        bool in[TURNS];
 #pragma unroll
         for (int i = 0; i < TURNS; ++i) {
             const int s = s0 + i * GROUPS + group;
             w[i] = __shfl(f, s & 63, 64);
-            in[i] = group < GROUPS && s < p.slots && (there >> (s & 63) & 1);
+            if (group >= GROUPS || s >= p.slots)
+                w[i] = -1.f;
             // in place of what is left out the first run's are read
-            v[i] = *reinterpret_cast<const f32x4 *>(p.part + (first + (in[i] ? s : 0)) * D + d);
+            v[i] = *reinterpret_cast<const f32x4 *>(p.part + (first + (w[i] < 0.f ? 0 : s)) * D + d);
         }
 #pragma unroll
         for (int i = 0; i < TURNS; ++i)
-            o += in[i] ? w[i] * v[i] : f32x4{};
+            o += w[i] < 0.f ? f32x4{} : w[i] * v[i];
     }
     if constexpr (GROUPS > 1) {
 #pragma unroll
