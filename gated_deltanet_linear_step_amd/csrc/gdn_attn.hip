@@ -200,13 +200,21 @@ void attn_prefill_splits(int Hq, int Hkv, int D, int N, int64_t total, const int
     int64_t each = std::max<int64_t>({(all + kSlots - 1) / kSlots, 4, (longest + most - 1) / most});
     if (count >= kCus) {
         // Blocks for every CU, but of all lengths: a long one would be left alone on its CU, at about 0.6 of the rate of two. Cut at
-        // the average, their ends go where short ones were; it pays where that is more than writing and joining
-        // parts takes (microseconds, as measured; 4096 tokens, 16 heads of 256: 213 us uncut, 194 cut).
-        const double tile = D == 256 ? 1.25 : D == 128 ? 1.2 : D == 96 ? 0.9 : 0.7;
-        int64_t cut = 0;
-        blocks([&](int64_t tiles, int64_t) { cut += tiles > each ? Hkv : 0; });
-        const double gain = 0.7 * tile * (longest - each), cost = 8 + cut * 2.0 * kBlock * D * 4 * 2 / 4.5e6;
-        if (gain <= cost)
+        // the average, their ends go where short ones were; it pays where that is more than writing and joining parts takes.
+        // Heads of 256 (us, uncut / cut): 2048 tokens, 32 heads over 4, 109 / 113; 4096, 16 over 2, 199 / 172; behind 16384, 1126 / 1104;
+        // 2048 behind 14336 725 / 488. Narrower ones gain less by a tile, and are cut where the longest has 64 tiles more. Of 128, 16
+        // heads over 2: 4096 tokens (31 more) 89 / 104, behind 16384 (31) 583 / 607, 8 x 300 behind 8000 (54) 222 / 232, 8 over 1 of
+        // 8192 (63) 168 / 169; 2048 behind 14336 (135) 299 / 279, 8 x 300 behind up to 16000 (200) 288 / 212; a prefix of 16000 for
+        // 1200 queries, 32 over 8 (101) 536 / 502. Heads of 96 turn at the same lengths (72 / 92, 186 / 194, 135 / 151; 244 / 233, 237 /
+        // 181, 438 / 400), those of 64 a little sooner (31: 69 / 87, 46: 117 / 120, 54: 180 / 148, 59: 89 / 86, 101: 372 / 284; but 63: 119 / 134).
+        bool pays = longest - each >= (D == 64 ? 50 : 64);
+        if (D == 256) {
+            int64_t cut = 0;
+            blocks([&](int64_t tiles, int64_t) { cut += tiles > each ? Hkv : 0; });
+            // microseconds: 1.25 a tile, 8 a launch, 4.5e6 bytes of parts written and read
+            pays = 0.7 * 1.25 * (longest - each) > 8 + cut * 2.0 * kBlock * D * 4 * 2 / 4.5e6;
+        }
+        if (!pays)
             return;
     } else {
         // Fewer: runs of one length, as many as one round of workgroups holds on every XCD (they go to the 8 in turn, those

@@ -100,3 +100,32 @@ def test_rows_of_queries_and_outputs_past_32_bits():
     ops.attention_decode(rows, kp, vp, table.expand(lens[0], -1).contiguous(), n.expand(lens[0]).contiguous(), batch=lens[0], max_len=lens[0], out=out)
     want = attention64(q, k, v, torch.ones(lens[0], lens[0], dtype=torch.bool, device=DEV), D ** -0.5)
     near(out, want[0], want[2])
+
+
+@pytest.mark.parametrize("D,dtype", [(64, B16), (96, F16), (128, B16), (256, F16)])
+@pytest.mark.parametrize("lens,past", [([2048], [10000]), ([150] * 8, [0, 1000, 3000, 500, 12000, 8, 4000, 70]), ([300] * 4, [6000] * 4)],
+                         ids=["one", "mixed", "alike"])
+def test_blocks_for_every_cu_behind_cached_keys(D, dtype, lens, past):
+    """256 to 512 blocks of rows, whose keys are cut where the longest are far longer than the average, and not where they are alike."""
+    keys = [a + b for a, b in zip(lens, past)]
+    Hq, Hkv = (16, 2) if len(lens) == 1 else (32, 2)
+    q, k, v = packed(lens, keys, Hq, Hkv, D, dtype, D)
+    lse = torch.empty(sum(lens), Hq, device=DEV)
+    kp, vp, table = on_pages(k, v, keys, 64, 5)
+    for paged in (False, True):
+        out = ops.attention_prefill(q, kp if paged else k, vp if paged else v, offsets(lens), cu_k=offsets(keys), lse=lse,
+                                    table=table if paged else None)
+        check_prompts(out, lse, q, k, v, lens, keys, D ** -0.5)
+
+
+@pytest.mark.parametrize("D,dtype", [(64, F16), (128, B16), (256, B16)])
+def test_a_prefix_behind_blocks_for_every_cu(D, dtype):
+    prefix, B = 7000, 1200
+    q, k, v, kp, vp, table, front = decode_inputs([3], prefix, 1, 32, 8, D, dtype, 64, D)
+    q = torch.randn(B, 32, D, generator=torch.Generator().manual_seed(1)).to(dtype).to(DEV)
+    lse = torch.empty(B, 32, device=DEV)
+    out = ops.attention_decode(q, kp, vp, table.expand(B, -1).contiguous(), torch.full((B,), 3, dtype=torch.int32, device=DEV), batch=B, max_len=3,
+                               prefix_table=front, prefix_len=prefix, lse=lse)
+    want = attention64(q, k, v, torch.ones(B, prefix + 3, dtype=torch.bool, device=DEV), D ** -0.5)
+    near(out, want[0], want[2])
+    near(lse, want[1], want[3])
