@@ -45,7 +45,7 @@ __global__ __launch_bounds__(256) void join_few_kernel(const AttnParams p, int64
     for (int x = 32; x; x >>= 1)
         most = fmaxf(most, __shfl_xor(most, x, 64));
     // a run without keys left its outputs as they were: -1; one whose factor f32 holds as 0 counts, for what is not finite in it
-    // (no mask of runs shifted by a lane's own number here: gdn_device.h, on 64-bit shifts)
+    // (no mask of runs shifted by a lane's own number here: gdn_attn_device.h, on 64-bit shifts)
     const float f = st.y == 0.f ? -1.f : exp2_f((st.x - most) * base2(p.scale));
     float total = f * st.y;
 #pragma unroll

@@ -36,7 +36,7 @@ def kernels(path, where):
 
 @pytest.mark.skipif(not all(os.path.exists(t) for t in TOOLS), reason="needs ROCm's LLVM tools")
 def test_no_64_bit_shift_takes_its_amount_from_the_last_register(tmp_path):
-    """csrc/gdn_device.h says what that did."""
+    """csrc/gdn_attn_device.h says what that did."""
     ops.load()
     seen, wrong = 0, []
     for name, allotted, lines in kernels(ops.LIB_PATH, tmp_path):
