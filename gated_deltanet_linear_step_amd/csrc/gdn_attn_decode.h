@@ -12,10 +12,11 @@
 //  * The pages of the whole run are looked up at once, a 16-key group a lane.
 //  * S^T = K Q^T (v_mfma_f32_16x16x32): a lane holds one row's scores; as they lie, the exponentials of two 16-key tiles are the
 //    operand of O^T += V^T P^T, whose V^T comes from transposing LDS reads. Blocks of 16 bytes are permuted within
-//    a row by the address that a lane copies from, so that reads of 16 rows fall into different banks.
+//    a row by the address that a lane copies from, so that reads of 16 rows fall into different banks (V's transposing ones of
+//    128 wide heads still conflict, in 57 % of the LDS's active clocks; the kernel waits for memory meanwhile).
 //  * P is rounded to the 16 bits of V as in the prompts' kernel.
-// 64 sequences of 128 to 8192 keys, 32 heads over 8 of 128, bf16: 197 us and 5 to join the runs, 5.4 TB/s (a large copy
-// reaches 5.1, the last-level cache holds part of the keys); one of 32768 keys, 16 heads over 2 of 256: 15 and 5 us.
+// 64 sequences of 128 to 8192 keys, 32 heads over 8 of 128, bf16: 200 us and 5 to join the runs, 5.4 TB/s (a large copy
+// reaches 5.1, the last-level cache holds part of the keys); one of 32768 keys, 16 heads over 2 of 256: 16 and 5 us.
 #pragma once
 
 #include "gdn_attn_prefill.h"

@@ -20,13 +20,13 @@
 //  * P is rounded to the 16 bits of V, by up to 2^-8 (bf16) or 2^-11 (f16, of weights from 2^-21 of the row's largest on; below by
 //    up to 2^-32 of that) of each term, as much as the outputs' own rounding; its sum is of the unrounded ones.
 //
-// Eight prompts of 30,208 tokens, 32 heads over 8 of 128, bf16: 1290 us, 1020 TFLOP/s (a library's product of 8192^3
-// reaches 1356); 16384 tokens, 16 heads over 2 of 256: 1880 us, 1170; 4096 such tokens: 175, of which 21 join parts.
-// Bound by the matrix unit and the vector instructions together: of 128 wide heads' time the one is busy 52 %, the other
-// issues 54 %, with no LDS conflicts, while the card holds 1.6 to 2.0 GHz. Wave priorities, operands read 4 to 8 products
-// ahead and the scheduler's own order of the exponentials made no difference (594 to 605 us at 8192 tokens), which
-// points to the power that the card allows; without the exponentials the same takes 5 % less, without the products of the
-// scores 28 %.
+// Eight prompts of 30,208 tokens, 32 heads over 8 of 128, bf16: 1286 to 1345 us on different cards, 980 to 1020 TFLOP/s (a library's
+// product of 8192^3 reaches 1356); 16384 tokens, 16 heads over 2 of 256: 1880 to 1955 us, 1125 to 1170; 4096 such tokens: 178 to
+// 182, of which 21 to 23 join parts.
+// Bound by the matrix unit and the vector instructions, which hardly overlap: of 128 wide heads' clocks the one is busy in 51 %, the
+// other issues in 51 %, with no LDS conflicts, although two waves share a SIMD; the card runs at 1.6 to 1.9 GHz meanwhile. Wave
+// priorities, operands read 4 to 8 products ahead and the scheduler's own order of the exponentials made no difference (594 to
+// 605 us at 8192 tokens); without the exponentials the same takes 5 % less, without the products of the scores 28 %.
 #pragma once
 
 #include "gdn_attn_device.h"

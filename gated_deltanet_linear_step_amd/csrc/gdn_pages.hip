@@ -6,7 +6,7 @@
 // outcome does not depend on the order in which threads run. Where pages move, it leaves a list
 // in the workspace, and a second launch over the whole card copies them, plane after plane:
 // bound by the bytes of the copied pages, each read and written once. 477 pages on 24 planes of 16 KB: 7 us of tables and
-// 61 of copies (6.1 TB/s); a fork of 32 samples 13 us, bound by the latency of a few dependent loads and 2400 atomics.
+// 71 of copies (5.3 TB/s); a fork of 32 samples 13 us, bound by the latency of a few dependent loads and 2400 atomics.
 
 #include "gdn_device.h"
 #include "gdn_attn.h"
