@@ -76,7 +76,7 @@ hipError_t launch_attn_prefill_bf16(const AttnPrefillParams &p, unsigned grid, h
 hipError_t launch_attn_prefill_f16(const AttnPrefillParams &p, unsigned grid, hipStream_t s);
 
 // Keys of one run: an output is an f32 sum that 16 keys are added to at a time, and drifts where all weights and values are alike, as each
-// addition is then rounded the same way. Measured with six such weights: at most 2^-8 (bf16's half step) at 2^20 and 2^-7 at 2^22 keys, 2^-5.4
+// addition is then rounded the same way. Measured with five such weights: at most 2^-8 (bf16's half step) at 2^20 and 2^-7 at 2^22 keys, 2^-5.4
 // at 2^24.
 constexpr int kMostKeys = 1 << 21;
 

@@ -175,9 +175,9 @@ __device__ __forceinline__ float half_sum(float x)
 __device__ __forceinline__ float base2(float scale) { return scale * 1.4426950408889634f; }
 
 // Exponents in base 2 are formed as scale s - base in one instruction, with base the rounded product of scale and the row's
-// maximum (less kLift). What that rounding left out raises every weight of a row alike: by less than 2^-13 of itself while |base| <= 2^10,
+// maximum (less kLift). What that rounding left out raises every weight of a row alike: by less than 2^-15 of itself while |base| <= 2^8,
 // but without bound beyond (at 2^36, by 2^4096 or to nothing). Rows past that take the maximum from the scores first.
-constexpr float kFar = 1024.f;
+constexpr float kFar = 256.f;
 
 __device__ __forceinline__ float exp2_f(float x) { return __builtin_amdgcn_exp2f(x); }
 

@@ -22,7 +22,7 @@
 //
 // Eight prompts of 30,208 tokens, 32 heads over 8 of 128, bf16: 1286 to 1345 us on different cards, 980 to 1020 TFLOP/s (a library's
 // product of 8192^3 reaches 1356); 16384 tokens, 16 heads over 2 of 256: 1880 to 1955 us, 1125 to 1170; 4096 such tokens: 178 to
-// 182, of which 21 to 23 join parts.
+// 183, of which 21 to 23 join parts.
 // Bound by the matrix unit and the vector instructions, which hardly overlap: of 128 wide heads' clocks the one is busy in 51 %, the
 // other issues in 51 %, with no LDS conflicts, although two waves share a SIMD; the card runs at 1.6 to 1.9 GHz meanwhile. Wave
 // priorities, operands read 4 to 8 products ahead and the scheduler's own order of the exponentials made no difference (594 to

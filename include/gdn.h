@@ -522,9 +522,9 @@ gdn_status gdn_rope_frequencies(int32_t rotary_dim, double theta, int32_t scalin
  * Infinities and NaN in keys, values or queries that a query does not see do not reach
  * it; in those it sees they make what the formula makes of them not finite (where that
  * is an infinity, a NaN may stand; the value of a key of score -inf may be left out instead).
- * Finite f16 values and scores have finite outputs. Outputs are summed before they are divided by the sum of
- * weights, of at most 2^8 each (f16 2^15): bf16 values of 2^90 and more may leave f32 on the
- * way, as may scores times scale.
+ * Finite f16 values and scores have finite outputs. Outputs are summed before they are divided
+ * by the sum of weights, of at most 2^8 each (f16 2^15): bf16 values of 2^90 and more may leave
+ * f32 on the way, as may scores times scale.
  *
  *   q_heads, kv_heads   q_heads a multiple of kv_heads, both >= 1
  *   head_dim       64, 96, 128 or 256
